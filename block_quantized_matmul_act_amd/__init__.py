@@ -25,8 +25,23 @@ KQ_ERR_FMT, KQ_ERR_SHAPE, KQ_ERR_NULL, KQ_ERR_ALIGN, KQ_ERR_UNSUPPORTED, KQ_ERR_
 (KQ_CALIB_MFMA_I8, KQ_CALIB_MFMA_I8_TOGGLE, KQ_CALIB_VALU_F32, KQ_CALIB_MFMA_I8_VALU,
  KQ_CALIB_HBM_READ) = 0, 1, 2, 3, 4
 
+KQ_T_F32, KQ_T_BF16, KQ_T_F16, KQ_T_F8 = 1, 2, 3, 4
+KQ_ATTN_MAX_TOKENS = KQ_KEEP_MAX_TOKENS = KQ_LOGPROBS_MAX_TOP = 64
+
 # Every symbol include/kq.h declares, with its ctypes signature.
-_P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+
+
+class kq_cache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("n_pages", _I64), ("type", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("page", ctypes.c_int32), ("k_scale", _F), ("v_scale", _F)]
+
+
+class kq_batch(ctypes.Structure):
+    _fields_ = [("offsets", _P), ("lens", _P), ("pages", _P), ("n_seqs", _I64), ("n_tokens", _I64),
+                ("max_pages", _I64)]
+
+
 SIGNATURES = {
     "kq_weight_bytes": (_SZ, [_I, _I64, _I64]),
     "kq_act_bytes": (_SZ, [_I, _I64, _I64]),
@@ -43,6 +58,12 @@ SIGNATURES = {
     "kq_dispatch_reset": (None, []),
     "kq_select_variant": (_I, [_I, _I64, _I64, _I64]),
     "kq_calib_launch": (_I, [_I, _I, _P, _I64, ctypes.POINTER(ctypes.c_double), _P]),
+    "kq_rope_append": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _F, _P, _I64, _I64, _I, _P, _I, _P, _P]),
+    "kq_attn_tree": (_I, [_P, _P, _I, _P, _I64, _P, _F, _I64, _I64, _I, _P, _P, _SZ, _P]),
+    "kq_attn_tree_workspace": (_SZ, [_P, _P, _I64, _I64, _I64]),
+    "kq_cache_keep": (_I, [_P, _I64, _P, _P, _P, _P]),
+    "kq_logprobs": (_I, [_I, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "kq_logprobs_workspace": (_SZ, [_I64, _I64, _I64]),
     "kq_strerror": (ctypes.c_char_p, [_I]),
     "kq_version": (_I, []),
 }
@@ -209,6 +230,45 @@ def kq_calib_launch(kind, param=0, buf=None, nbytes=0, stream=None):
     return work.value
 
 
+def _ref(d):
+    """A descriptor (kq_cache, kq_batch or an array of them) as an argument."""
+    return None if d is None else ctypes.addressof(d)
+
+
+def kq_rope_append(cache, batch, x, ldx, q_heads, q_norm, k_norm, eps, rope, n_pos, rot_dim, pairs, positions, q_type,
+                   q, stream=None):
+    return _check(lib().kq_rope_append(_ref(cache), _ref(batch), _ptr(x), ldx, q_heads, _ptr(q_norm), _ptr(k_norm), eps,
+                                       _ptr(rope), n_pos, rot_dim, int(pairs), _ptr(positions), q_type, _ptr(q),
+                                       _stream(stream)), "kq_rope_append")
+
+
+def kq_attn_tree_workspace(cache, batch, q_heads, max_tokens, max_len):
+    return lib().kq_attn_tree_workspace(_ref(cache), _ref(batch), q_heads, max_tokens, max_len)
+
+
+def kq_attn_tree(cache, batch, q_type, q, q_heads, mask, scale, max_tokens, max_len, out_type, out, workspace,
+                 workspace_bytes, stream=None):
+    return _check(lib().kq_attn_tree(_ref(cache), _ref(batch), q_type, _ptr(q), q_heads, _ptr(mask), scale, max_tokens,
+                                     max_len, out_type, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)),
+                  "kq_attn_tree")
+
+
+def kq_cache_keep(caches, n_caches, batch, path, counts, stream=None):
+    return _check(lib().kq_cache_keep(_ref(caches), n_caches, _ref(batch), _ptr(path), _ptr(counts), _stream(stream)),
+                  "kq_cache_keep")
+
+
+def kq_logprobs_workspace(M, V, n_top):
+    return lib().kq_logprobs_workspace(M, V, n_top)
+
+
+def kq_logprobs(type, logits, M, V, ldx, tokens, n_given, n_top, logprob, entropy, top_ids, top_logprobs, workspace,
+                workspace_bytes, stream=None):
+    return _check(lib().kq_logprobs(type, _ptr(logits), M, V, ldx, _ptr(tokens), n_given, n_top, _ptr(logprob),
+                                    _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), workspace_bytes,
+                                    _stream(stream)), "kq_logprobs")
+
+
 def kq_strerror(status):
     return lib().kq_strerror(status).decode()
 
@@ -285,3 +345,214 @@ def gemm_id(fmt, W, n_experts, a_q8, M, N, K, expert_offsets, rows, out=None, st
         out = torch.empty((R, N), dtype=torch.float32, device=a_q8.device)
     kq_gemm_id(fmt, W, n_experts, a_q8, M, N, K, expert_offsets, rows, R, out, stream)
     return out
+
+
+# ------------------------------- the step between two products (cache, attention, answer)
+
+_types = None
+
+
+def _type(t, where):
+    """KQ_T_* of a tensor's element type."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: KQ_T_F32, torch.bfloat16: KQ_T_BF16, torch.float16: KQ_T_F16,
+                  torch.float8_e4m3fn: KQ_T_F8}
+    kind = _types.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{where}: element type {t.dtype} not taken")
+    return kind
+
+
+def _tensor(t, dtype, shape, where, contiguous=True):
+    """Check one tensor argument (None in a shape: any size); its pointer."""
+    if not t.is_cuda:
+        raise ValueError(f"{where}: expected a device tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{where}: expected dtype {dtype}, got {t.dtype}")
+    have = t.shape
+    if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
+        raise ValueError(f"{where}: expected shape {shape}, got {tuple(have)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{where}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows(t, shape, where):
+    """Check a [rows][n] tensor whose rows may lie apart; (pointer, row stride)."""
+    p = _tensor(t, None, shape, where, contiguous=False)
+    rows, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: expected rows of neighbouring elements")
+    ld = t.stride(0) if rows > 1 else max(n, 1)
+    if ld < n:
+        raise ValueError(f"{where}: rows overlap (stride {ld}, {n} elements)")
+    return p, ld
+
+
+def _same_device(first, others, where):
+    at = first.device
+    for t in others:
+        if t is not None and t.device != at:
+            raise ValueError(f"{where}: tensors on {at} and {t.device}")
+
+
+def _on(stream, device):
+    """A context in which a stream (a torch stream or a raw handle) is torch's
+    current one: what is allocated in it belongs to that stream, so neither the
+    results nor the workspace can be handed to other work that it overtakes."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+class PagedCache:
+    """Keys [n_pages][heads][page][dim] and values [n_pages][heads][dim][page]
+    of one layer (bfloat16, float16 or float8_e4m3fn device tensors); what is
+    stored times k_scale / v_scale is the key / value."""
+
+    def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
+        where = "PagedCache"
+        if k.dim() != 4:
+            raise ValueError(f"{where} k: expected [n_pages][heads][page][dim], got {tuple(k.shape)}")
+        n, heads, page, dim = k.shape
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.c = kq_cache(_tensor(k, None, (n, heads, page, dim), where + " k"),
+                          _tensor(v, k.dtype, (n, heads, dim, page), where + " v"), n, _type(k, where), heads, dim,
+                          page, k_scale, v_scale)
+        _same_device(k, (v,), where)
+
+
+class Batch:
+    """The sequences of one step (int32 device tensors): offsets [n_seqs + 1] of
+    their token rows, lens [n_seqs] tokens already cached, pages [n_seqs][max_pages]."""
+
+    def __init__(self, offsets, lens, pages):
+        import torch
+        where, i32 = "Batch", torch.int32
+        n = lens.numel()
+        self.offsets, self.lens, self.pages = offsets, lens, pages
+        self.c = kq_batch(_tensor(offsets, i32, (n + 1,), where + " offsets"), _tensor(lens, i32, (n,), where + " lens"),
+                          _tensor(pages, i32, (n, None), where + " pages"), n, 0, pages.shape[1])
+        _same_device(offsets, (lens, pages), where)
+
+    def rows(self, n):
+        """The step's descriptor for n token rows (which the first tensor with a
+        row to each token tells: the offsets themselves stay on the device)."""
+        self.c.n_tokens = n
+        return self.c
+
+
+def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None, k_norm=None, eps=1e-6, pairs=False,
+                q_dtype=None, out=None, stream=None):
+    """Split x [n_tokens][(q_heads + 2 heads) dim] (float32): q normed, rotated and
+    returned as [n_tokens][q_heads][dim] (q_dtype: the cache's, bfloat16 for an
+    8-bit cache); k normed and rotated, and v, stored in the cache's slots of the
+    rows.  rope: float32 [n_pos][rot_dim], the cosines and then the sines."""
+    import torch
+    if stream is not None:
+        with _on(stream, x.device):
+            return rope_append(cache, batch, x, q_heads, rope, positions, q_norm, k_norm, eps, pairs, q_dtype, out)
+    where, f32, c = "rope_append", torch.float32, cache.c
+    px, ldx = _rows(x, (None, (q_heads + 2 * c.heads) * c.dim), where + " x")
+    if x.dtype is not f32:
+        raise ValueError(f"{where} x: expected dtype {f32}, got {x.dtype}")
+    M = x.shape[0]
+    if q_dtype is None:
+        q_dtype = out.dtype if out is not None else torch.bfloat16 if c.type == KQ_T_F8 else cache.dtype
+    if out is None:
+        out = torch.empty((M, q_heads, c.dim), dtype=q_dtype, device=x.device)
+    pq = _tensor(out, q_dtype, (M, q_heads, c.dim), where + " out")
+    pr, n_pos, rot = None, 0, 0
+    if rope is not None:
+        pr = _tensor(rope, f32, (None, None), where + " rope")
+        n_pos, rot = rope.shape
+    pn = [None if w is None else _tensor(w, f32, (c.dim,), where + " norm") for w in (q_norm, k_norm)]
+    pp = None if positions is None else _tensor(positions, torch.int32, (M,), where + " positions")
+    _same_device(x, (cache.k, batch.lens, out, rope, q_norm, k_norm, positions), where)
+    kq_rope_append(c, batch.rows(M), px, ldx, q_heads, pn[0], pn[1], eps, pr, n_pos, rot, pairs, pp, _type(out, where),
+                   pq)
+    return out
+
+
+def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOKENS, max_len=None, out_dtype=None,
+              out=None, stream=None):
+    """Attention of q [n_tokens][q_heads][dim] over the cache, each row over its
+    sequence's cached tokens and those of its new rows that its bits in mask
+    name (int64 [n_tokens], bit j: the j-th new row; None: the rows up to its
+    own).  max_tokens / max_len: upper bounds of a sequence's new rows and of its
+    whole length (default: what the pages hold).  out_dtype: q's or float32."""
+    import torch
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_tree(cache, batch, q, mask, scale, max_tokens, max_len, out_dtype, out)
+    where, c = "attn_tree", cache.c
+    pq = _tensor(q, None, (None, None, c.dim), where + " q")
+    M, heads, dim = q.shape
+    if out is None:
+        out = torch.empty((M, heads, dim), dtype=out_dtype or q.dtype, device=q.device)
+    po = _tensor(out, out_dtype, (M, heads, dim), where + " out")
+    pm = None if mask is None else _tensor(mask, torch.int64, (M,), where + " mask")
+    if max_len is None:
+        max_len = batch.c.max_pages * c.page
+    if scale is None:
+        scale = dim ** -0.5
+    _same_device(q, (cache.k, batch.lens, out, mask), where)
+    b = batch.rows(M)
+    need = kq_attn_tree_workspace(c, b, heads, max_tokens, max_len)
+    work = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    kq_attn_tree(c, b, _type(q, where), pq, heads, pm, scale, max_tokens, max_len, _type(out, where), po, work, need)
+    return out
+
+
+def cache_keep(caches, batch, path, counts, stream=None):
+    """Keep an accepted branch in every cache of a list (one per layer): slot
+    lens[b] + j takes what slot lens[b] + path[offsets[b] + j] held, j < counts[b]
+    (int32 [n_tokens] and [n_seqs])."""
+    import torch
+    where, i32 = "cache_keep", torch.int32
+    pp = _tensor(path, i32, (None,), where + " path")
+    pc = _tensor(counts, i32, (batch.c.n_seqs,), where + " counts")
+    n = len(caches)
+    _same_device(path, (batch.lens, counts, *(c.k for c in caches)), where)
+    kq_cache_keep((kq_cache * n)(*(c.c for c in caches)), n, batch.rows(path.shape[0]), pp, pc, stream)
+
+
+class LogProbs:
+    """What logprobs() found: logprob [M][n_given], entropy [M], top_ids and
+    top_logprobs [M][n_top] (None where not asked for)."""
+    __slots__ = ("logprob", "entropy", "top_ids", "top_logprobs")
+
+
+def logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
+    """Log probabilities of tokens [M][n_given] (int32) under logits [M][V]
+    (float32, bfloat16 or float16; rows may lie apart), the entropy of each row,
+    and the n_top largest logits' indices and log probabilities."""
+    import torch
+    if stream is not None:
+        with _on(stream, logits.device):
+            return logprobs(logits, tokens, n_top, entropy)
+    where, f32 = "logprobs", torch.float32
+    px, ldx = _rows(logits, (None, None), where + " logits")
+    M, V = logits.shape
+    kind, dev = _type(logits, where), logits.device
+    if kind == KQ_T_F8:
+        raise ValueError(f"{where}: element type {logits.dtype} not taken")
+    r = LogProbs()
+    r.logprob = r.entropy = r.top_ids = r.top_logprobs = None
+    pt, given = None, 0
+    if tokens is not None:
+        pt, given = _tensor(tokens, torch.int32, (M, None), where + " tokens"), tokens.shape[1]
+        _same_device(logits, (tokens,), where)
+        r.logprob = torch.empty((M, given), dtype=f32, device=dev)
+    if entropy:
+        r.entropy = torch.empty((M,), dtype=f32, device=dev)
+    if n_top:
+        r.top_ids = torch.empty((M, max(n_top, 0)), dtype=torch.int32, device=dev)
+        r.top_logprobs = torch.empty((M, max(n_top, 0)), dtype=f32, device=dev)
+    need = kq_logprobs_workspace(M, V, n_top)
+    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    kq_logprobs(kind, px, M, V, ldx, pt, given, n_top, r.logprob, r.entropy, r.top_ids, r.top_logprobs, work, need)
+    return r

@@ -1,0 +1,94 @@
+// kq_step.hpp -- launchers of the kernels between two products of a layer
+// (paged cache, attention over it, log probabilities), and the rules that cut
+// their work, shared by the launchers and the workspace queries.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/kq.h"
+
+namespace kq {
+
+// The device arrays and sizes of a cache and a step, as kernels take them.
+struct CacheArgs {
+    char *k, *v;
+    int64_t n_pages;
+    int heads, page_shift;  // page = 1 << page_shift tokens
+};
+struct BatchArgs {
+    const int32_t *offsets, *lens, *pages;
+    int n_seqs, n_tokens, max_pages;
+};
+
+struct RopeArgs {
+    CacheArgs cache;
+    BatchArgs batch;
+    const float *x;
+    int64_t ldx;
+    int q_heads;
+    const float *q_norm, *k_norm;
+    float eps, k_inv, v_inv;  // 1 / scale
+    const float *rope;
+    int n_pos, rot, pairs;
+    const int32_t *positions;
+    char *q;
+};
+// type / q_type: KQ_T_*; dim: 64, 128 or 256 (checked by the caller)
+hipError_t launch_rope_append(const RopeArgs &a, int type, int dim, int q_type, hipStream_t stream);
+
+// How attention over the cache is cut: rows_wave query rows to a wave, rows_wg
+// to a workgroup, each sequence's slots in parts of `part`.
+struct AttnPlan {
+    int rows_wave, rows_wg, row_blocks;
+    int part, parts;
+    int64_t o_bytes, bytes;  // workspace: sums of the parts, then their maxima and weights
+};
+AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len);
+
+struct AttnArgs {
+    CacheArgs cache;
+    BatchArgs batch;
+    const char *q;
+    int group;
+    const uint64_t *mask;
+    float score_scale, v_scale;  // score_scale: scale * k_scale * log2(e)
+    int max_tokens;
+    int out_f32;
+    char *out;
+    float *ws_o, *ws_ml;
+    int row_blocks, rows_wg, part, parts;
+};
+hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int type, int dim, int q_type, hipStream_t stream);
+
+constexpr int KEEP_CACHES = 64;  // caches to a launch (their pointers are kernel arguments)
+struct KeepArgs {
+    char *k[KEEP_CACHES], *v[KEEP_CACHES];
+    CacheArgs cache;
+    BatchArgs batch;
+    const int32_t *path, *counts;
+};
+hipError_t launch_keep(const KeepArgs &a, int n_caches, int elem_bytes, int dim, hipStream_t stream);
+
+// Rows of logits cut into parts of `part` values (parts = 1: one workgroup to
+// a row and no second kernel).
+struct LogprobsPlan {
+    int part, parts;
+    int64_t bytes;
+};
+LogprobsPlan logprobs_plan(int64_t M, int64_t V, int64_t n_top);
+
+struct LogprobsArgs {
+    const char *x;
+    int64_t ldx;
+    int V, part, parts;
+    const int32_t *tokens;
+    int n_given, n_top;
+    float *logprob, *entropy;
+    int32_t *top_ids;
+    float *top_logprobs;
+    char *ws;
+};
+hipError_t launch_logprobs(const LogprobsArgs &a, int type, int64_t M, hipStream_t stream);
+
+}  // namespace kq

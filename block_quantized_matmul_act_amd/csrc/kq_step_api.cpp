@@ -1,0 +1,291 @@
+// kq_step_api.cpp -- the C ABI between two products of a layer: the paged
+// cache, the attention over it and the log probabilities.  As in kq_api.cpp
+// every argument check comes before the first HIP call, so invalid calls return
+// a status without touching the runtime.
+#include "../../include/kq.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "kq_step.hpp"
+#include "kq_variants.hpp"
+
+namespace {
+
+using namespace kq;
+
+constexpr int64_t kMaxInt = INT32_MAX;
+constexpr int64_t kMaxLen = (int64_t)1 << 30;  // slots of a sequence: int arithmetic with room to spare
+constexpr int64_t kMaxPages = (int64_t)1 << 31;
+constexpr int64_t kMaxHeads = 65535;           // a grid's second dimension
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// KQ_OK, or the error of a cache descriptor
+int check_cache(const kq_cache *c) {
+    if (!c) return KQ_ERR_NULL;
+    if (c->type != KQ_T_BF16 && c->type != KQ_T_F16 && c->type != KQ_T_F8) return KQ_ERR_FMT;
+    if (c->n_pages < 0 || c->n_pages >= kMaxPages || c->heads < 1 || c->heads > kMaxHeads) return KQ_ERR_SHAPE;
+    if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
+        return KQ_ERR_SHAPE;
+    if (c->dim != 64 && c->dim != 128 && c->dim != 256) return KQ_ERR_UNSUPPORTED;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return KQ_ERR_UNSUPPORTED;
+    return KQ_OK;
+}
+// 1: work to do; KQ_OK: no rows; an error otherwise
+int check_batch(const kq_batch *s) {
+    if (!s) return KQ_ERR_NULL;
+    if (s->n_seqs < 0 || s->n_tokens < 0 || s->max_pages < 0) return KQ_ERR_SHAPE;
+    if (s->n_seqs > kMaxInt || s->n_tokens > kMaxInt / 2 || s->max_pages > kMaxInt) return KQ_ERR_SHAPE;
+    return s->n_tokens == 0 || s->n_seqs == 0 ? KQ_OK : 1;
+}
+// pointers and sizes that a call with rows needs
+int check_step(const kq_cache *c, const kq_batch *s) {
+    if (c->n_pages == 0 || s->max_pages == 0) return KQ_ERR_SHAPE;
+    if (!c->k || !c->v || !s->offsets || !s->lens || !s->pages) return KQ_ERR_NULL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(s->offsets, 4) || !aligned(s->lens, 4) ||
+        !aligned(s->pages, 4))
+        return KQ_ERR_ALIGN;
+    return KQ_OK;
+}
+CacheArgs cache_args(const kq_cache *c) {
+    int shift = 4;
+    while ((1 << shift) < c->page) ++shift;
+    return CacheArgs{static_cast<char *>(c->k), static_cast<char *>(c->v), c->n_pages, c->heads, shift};
+}
+BatchArgs batch_args(const kq_batch *s) {
+    return BatchArgs{s->offsets, s->lens, s->pages, (int)s->n_seqs, (int)s->n_tokens, (int)s->max_pages};
+}
+bool type16(int t) { return t == KQ_T_BF16 || t == KQ_T_F16; }
+
+// Sizes of kq_attn_tree and its workspace query (pointers aside)
+int check_attn(const kq_cache *c, const kq_batch *s, int64_t q_heads, int64_t max_tokens, int64_t max_len) {
+    int rc = check_cache(c);
+    if (rc != KQ_OK) return rc;
+    rc = check_batch(s);
+    if (rc < 0) return rc;
+    if (q_heads < 1 || q_heads > kMaxHeads || q_heads % c->heads) return KQ_ERR_SHAPE;
+    if (max_tokens < 0 || max_len < 0 || max_len > kMaxLen) return KQ_ERR_SHAPE;
+    if (max_tokens > KQ_ATTN_MAX_TOKENS) return KQ_ERR_UNSUPPORTED;
+    if (rc == KQ_OK) return KQ_OK;
+    if (s->n_tokens * q_heads >= ((int64_t)1 << 31) / c->dim) return KQ_ERR_UNSUPPORTED;
+    if (max_tokens == 0 || max_len == 0) return KQ_ERR_SHAPE;  // rows to compute, none allowed
+    const AttnPlan p = attn_plan(s->n_seqs, c->heads, q_heads / c->heads, c->dim, max_tokens, max_len);
+    const int64_t items = s->n_seqs * c->heads;
+    if (items > kMaxInt / p.parts || (items * p.parts + 8) > kMaxInt / p.row_blocks) return KQ_ERR_UNSUPPORTED;
+    return 1;
+}
+
+}  // namespace
+
+namespace kq {
+
+AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len) {
+    AttnPlan p;
+    const int64_t rows = max_tokens * group;
+    p.rows_wave = rows <= 16 || dim == 256 ? 16 : 32;
+    p.rows_wg = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || dim == 256 ? 64 : 128;
+    p.row_blocks = (int)((rows + p.rows_wg - 1) / p.rows_wg);
+    // parts: enough workgroups for several on each of 256 compute units (ragged
+    // sequences even out over them), of at least 128 slots (a tile to each wave)
+    const int64_t groups = std::max<int64_t>(1, n_seqs * heads * p.row_blocks);
+    const int64_t want = std::max<int64_t>(1, (2048 + groups - 1) / groups);
+    int64_t part = (max_len + want - 1) / want;
+    part = std::max<int64_t>(128, (part + 127) / 128 * 128);
+    p.part = (int)part;
+    p.parts = (int)((max_len + part - 1) / part);
+    const int64_t rows_ws = p.parts > 1 ? n_seqs * heads * p.parts * rows : 0;
+    p.o_bytes = rows_ws * dim * 4;
+    p.bytes = p.o_bytes + rows_ws * 8;
+    return p;
+}
+
+LogprobsPlan logprobs_plan(int64_t M, int64_t V, int64_t n_top) {
+    LogprobsPlan p;
+    // 4096 values (a batch to each wave of a workgroup) at least, and no more
+    // parts than give each compute unit a few workgroups
+    const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, M));
+    int64_t part = (V + want - 1) / want;
+    part = std::max<int64_t>(4096, (part + 4095) / 4096 * 4096);
+    p.part = (int)std::min<int64_t>(part, kMaxInt / 2 + 1);
+    p.parts = (int)std::max<int64_t>(1, (V + p.part - 1) / p.part);
+    p.bytes = p.parts > 1 ? M * p.parts * (12 + 8 * n_top) : 0;
+    return p;
+}
+
+}  // namespace kq
+
+extern "C" {
+
+int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x, int64_t ldx, int64_t q_heads,
+                   const float *q_norm, const float *k_norm, float eps, const float *rope, int64_t n_pos,
+                   int64_t rot_dim, int pairs, const int32_t *positions, int q_type, void *q, hipStream_t stream) {
+    int rc = check_cache(cache);
+    if (rc != KQ_OK) return rc;
+    if (!type16(q_type) || (cache->type != KQ_T_F8 && cache->type != q_type)) return KQ_ERR_FMT;
+    const int work = check_batch(batch);
+    if (work < 0) return work;
+    if (q_heads < 1 || q_heads > kMaxHeads) return KQ_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > cache->dim || rot_dim % 8 || n_pos < 0 || n_pos > kMaxInt) return KQ_ERR_SHAPE;
+    if (rot_dim && n_pos == 0 && work == 1) return KQ_ERR_SHAPE;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return KQ_ERR_SHAPE;
+    if (ldx % 4 || ldx < (q_heads + 2 * (int64_t)cache->heads) * cache->dim || ldx > kMaxLen) return KQ_ERR_SHAPE;
+    if (work == KQ_OK) return KQ_OK;
+    rc = check_step(cache, batch);
+    if (rc != KQ_OK) return rc;
+    if (!x || !q || (rot_dim && !rope)) return KQ_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(rope, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
+        !aligned(positions, 4))
+        return KQ_ERR_ALIGN;
+    // workgroups: at most a wave to a head and row, and 16 rows to a value head
+    if (batch->n_tokens > kMaxInt / (q_heads + 2 * cache->heads)) return KQ_ERR_UNSUPPORTED;
+    RopeArgs a;
+    a.cache = cache_args(cache);
+    a.batch = batch_args(batch);
+    a.x = x;
+    a.ldx = ldx;
+    a.q_heads = (int)q_heads;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    a.k_inv = 1.0f / cache->k_scale;
+    a.v_inv = 1.0f / cache->v_scale;
+    a.rope = rope;
+    a.n_pos = (int)n_pos;
+    a.rot = (int)rot_dim;
+    a.pairs = pairs != 0;
+    a.positions = positions;
+    a.q = static_cast<char *>(q);
+    if (launch_rope_append(a, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
+    count_dispatch(V_ROPE_APPEND);
+    return KQ_OK;
+}
+
+size_t kq_attn_tree_workspace(const kq_cache *cache, const kq_batch *batch, int64_t q_heads, int64_t max_tokens,
+                              int64_t max_len) {
+    if (check_attn(cache, batch, q_heads, max_tokens, max_len) <= 0) return 0;
+    return (size_t)attn_plan(batch->n_seqs, cache->heads, q_heads / cache->heads, cache->dim, max_tokens, max_len).bytes;
+}
+
+int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q, int64_t q_heads,
+                 const uint64_t *mask, float scale, int64_t max_tokens, int64_t max_len, int out_type, void *out,
+                 void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    int rc = check_cache(cache);
+    if (rc != KQ_OK) return rc;
+    if (!type16(q_type) || (cache->type != KQ_T_F8 && cache->type != q_type)) return KQ_ERR_FMT;
+    if (out_type != q_type && out_type != KQ_T_F32) return KQ_ERR_FMT;
+    if (!std::isfinite(scale)) return KQ_ERR_SHAPE;
+    rc = check_attn(cache, batch, q_heads, max_tokens, max_len);
+    if (rc <= 0) return rc;
+    rc = check_step(cache, batch);
+    if (rc != KQ_OK) return rc;
+    const AttnPlan p =
+        attn_plan(batch->n_seqs, cache->heads, q_heads / cache->heads, cache->dim, max_tokens, max_len);
+    if (!q || !out || (p.bytes && !workspace)) return KQ_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 8) || !aligned(workspace, 16)) return KQ_ERR_ALIGN;
+    if (workspace_bytes < (size_t)p.bytes) return KQ_ERR_SHAPE;
+    AttnArgs a;
+    a.cache = cache_args(cache);
+    a.batch = batch_args(batch);
+    a.q = static_cast<const char *>(q);
+    a.group = (int)(q_heads / cache->heads);
+    a.mask = mask;
+    a.score_scale = (float)((double)scale * cache->k_scale * 1.44269504088896340736);
+    a.v_scale = cache->v_scale;
+    a.max_tokens = (int)max_tokens;
+    a.out_f32 = out_type == KQ_T_F32;
+    a.out = static_cast<char *>(out);
+    a.ws_o = static_cast<float *>(workspace);
+    a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.o_bytes);
+    a.row_blocks = p.row_blocks;
+    a.rows_wg = p.rows_wg;
+    a.part = p.part;
+    a.parts = p.parts;
+    if (launch_attn(a, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
+    count_dispatch(p.rows_wave == 16 ? V_ATTN_FEW : V_ATTN_ROWS);
+    return KQ_OK;
+}
+
+int kq_cache_keep(const kq_cache *caches, int64_t n_caches, const kq_batch *batch, const int32_t *path,
+                  const int32_t *counts, hipStream_t stream) {
+    if (n_caches < 0 || n_caches > kMaxInt) return KQ_ERR_SHAPE;
+    if (n_caches && !caches) return KQ_ERR_NULL;
+    for (int64_t i = 0; i < n_caches; ++i) {
+        const int rc = check_cache(caches + i);
+        if (rc != KQ_OK) return rc;
+        const kq_cache &c = caches[i], &d = caches[0];
+        if (c.type != d.type || c.heads != d.heads || c.dim != d.dim || c.page != d.page || c.n_pages != d.n_pages)
+            return KQ_ERR_SHAPE;
+    }
+    int rc = check_batch(batch);
+    if (rc <= 0) return rc;
+    if (n_caches == 0) return KQ_OK;
+    for (int64_t i = 0; i < n_caches; ++i) {
+        rc = check_step(caches + i, batch);
+        if (rc != KQ_OK) return rc;
+    }
+    if (!path || !counts) return KQ_ERR_NULL;
+    if (!aligned(path, 4) || !aligned(counts, 4)) return KQ_ERR_ALIGN;
+    KeepArgs a;
+    a.cache = cache_args(caches);
+    a.batch = batch_args(batch);
+    a.path = path;
+    a.counts = counts;
+    for (int64_t i = 0; i < n_caches; i += KEEP_CACHES) {
+        const int n = (int)std::min<int64_t>(KEEP_CACHES, n_caches - i);
+        for (int j = 0; j < KEEP_CACHES; ++j) {
+            a.k[j] = static_cast<char *>(caches[i + (j < n ? j : 0)].k);
+            a.v[j] = static_cast<char *>(caches[i + (j < n ? j : 0)].v);
+        }
+        if (launch_keep(a, n, caches->type == KQ_T_F8 ? 1 : 2, caches->dim, stream) != hipSuccess) return KQ_ERR_HIP;
+        count_dispatch(V_CACHE_KEEP);
+    }
+    return KQ_OK;
+}
+
+size_t kq_logprobs_workspace(int64_t M, int64_t V, int64_t n_top) {
+    if (M < 1 || V < 1 || M > kMaxInt || V > kMaxLen || n_top < 0 || n_top > KQ_LOGPROBS_MAX_TOP || n_top > V) return 0;
+    return (size_t)logprobs_plan(M, V, n_top).bytes;
+}
+
+int kq_logprobs(int type, const void *logits, int64_t M, int64_t V, int64_t ldx, const int32_t *tokens,
+                int64_t n_given, int64_t n_top, float *logprob, float *entropy, int32_t *top_ids, float *top_logprobs,
+                void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (type != KQ_T_F32 && type != KQ_T_BF16 && type != KQ_T_F16) return KQ_ERR_FMT;
+    if (M < 0 || V < 0 || n_given < 0 || n_top < 0 || M > kMaxInt || V > kMaxLen || n_given > kMaxInt) return KQ_ERR_SHAPE;
+    if (ldx < V || ldx > ((int64_t)1 << 40)) return KQ_ERR_SHAPE;
+    if (M == 0) return KQ_OK;
+    if (V == 0 || n_top > V) return KQ_ERR_SHAPE;
+    if (n_top > KQ_LOGPROBS_MAX_TOP) return KQ_ERR_UNSUPPORTED;
+    const LogprobsPlan p = logprobs_plan(M, V, n_top);
+    if (M > kMaxInt / p.parts) return KQ_ERR_UNSUPPORTED;
+    if (!logits || (n_given && (!tokens || !logprob)) || (n_top && (!top_ids || !top_logprobs)) ||
+        (p.bytes && !workspace))
+        return KQ_ERR_NULL;
+    if (!aligned(logits, type == KQ_T_F32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprob, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || !aligned(workspace, 16))
+        return KQ_ERR_ALIGN;
+    if (workspace_bytes < (size_t)p.bytes) return KQ_ERR_SHAPE;
+    LogprobsArgs a;
+    a.x = static_cast<const char *>(logits);
+    a.ldx = ldx;
+    a.V = (int)V;
+    a.part = p.part;
+    a.parts = p.parts;
+    a.tokens = tokens;
+    a.n_given = (int)n_given;
+    a.n_top = (int)n_top;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.ws = static_cast<char *>(workspace);
+    if (launch_logprobs(a, type, M, stream) != hipSuccess) return KQ_ERR_HIP;
+    count_dispatch(p.parts == 1 ? V_LOGPROBS_ROW : V_LOGPROBS_PARTS);
+    return KQ_OK;
+}
+
+}  // extern "C"

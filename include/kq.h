@@ -16,8 +16,9 @@
  *
  * Conventions (all entry points):
  *   - Every pointer argument is a DEVICE pointer except where noted.  The
- *     caller allocates and frees all memory; the library allocates nothing,
- *     keeps no handles and needs no scratch.
+ *     caller allocates and frees all memory; the library allocates nothing and
+ *     keeps no handles.  The products need no scratch; kq_attn_tree and
+ *     kq_logprobs take a workspace whose size a query gives.
  *   - Work is enqueued asynchronously on `stream` (NULL = the default
  *     stream).  Device faults surface at the caller's next synchronization.
  *   - Arguments are validated on the host before any HIP call.  On any error
@@ -241,6 +242,148 @@ int kq_debug_unpack(int fmt, const void *W, int64_t nblocks, int8_t *q, int32_t 
 int kq_gemm_id(int fmt, const void *W, int64_t n_experts, const void *a_q8, int64_t M, int64_t N,
                int64_t K, const int32_t *expert_offsets, const int32_t *rows, int64_t R, float *out,
                hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Between two products of a layer: a paged cache of keys and values, the
+ * attention of drafted tokens over it, and the log probabilities of the
+ * logits.  One step of decoding with drafts runs
+ *
+ *   kq_gemm (q, k, v) -> kq_rope_append -> kq_attn_tree -> kq_quantize_act ->
+ *   kq_gemm (output) ... kq_gemm (logits) -> kq_logprobs -> kq_cache_keep
+ *
+ * and a step without drafts is the tree of one token.
+ */
+
+/* element types */
+#define KQ_T_F32 1
+#define KQ_T_BF16 2
+#define KQ_T_F16 3
+#define KQ_T_F8 4 /* OCP e4m3: largest finite value 448, no infinities */
+
+/*
+ * A paged cache of one layer (a host struct; k and v are device pointers,
+ * 16-byte aligned).  A page holds `page` consecutive tokens of one sequence:
+ *   k [n_pages][heads][page][dim]     v [n_pages][heads][dim][page]
+ * (values transposed, so that the product with the probabilities reads 8
+ * consecutive tokens of one feature as one load).  The stored value times
+ * k_scale / v_scale is the key / value; kq_cache_keep ignores the scales.
+ *   type   KQ_T_BF16, KQ_T_F16 or KQ_T_F8      heads  >= 1
+ *   dim    64, 128 or 256                      page   16, 32, 64, 128 or 256
+ */
+typedef struct kq_cache {
+    void *k, *v;
+    int64_t n_pages;
+    int32_t type, heads, dim, page;
+    float k_scale, v_scale; /* finite, > 0 */
+} kq_cache;
+
+/*
+ * The sequences of one step (a host struct of device int32 arrays, 4-byte
+ * aligned).  Sequence b brings the token rows [offsets[b], offsets[b + 1]) of
+ * the step's n_tokens; lens[b] tokens of it are in the cache already.  Row
+ * offsets[b] + i belongs to slot lens[b] + i, and slot s lives in page
+ * pages[b][s / page] at place s % page.  A sequence may bring no token.
+ * The arrays are not checked on the host: arrays that break the contract
+ * (offsets that fall, a length below zero, a page outside the cache, a slot
+ * past max_pages pages) give undefined values, but no access leaves the
+ * buffers.
+ */
+typedef struct kq_batch {
+    const int32_t *offsets; /* [n_seqs + 1], offsets[0] = 0, offsets[n_seqs] = n_tokens */
+    const int32_t *lens;    /* [n_seqs] */
+    const int32_t *pages;   /* [n_seqs][max_pages] */
+    int64_t n_seqs, n_tokens, max_pages;
+} kq_batch;
+
+/*
+ * Split the product x [n_tokens][(q_heads + 2 heads) dim] (fp32, row stride
+ * ldx elements, a multiple of 4; q heads, then k heads, then v heads) and, in
+ * one pass over it,
+ *   - scale every q and k head by its norm: y = x * w / sqrt(mean x^2 + eps),
+ *     w = q_norm / k_norm (fp32 [dim]; NULL: no norm for q / for k);
+ *   - rotate the first rot_dim features of every q and k head by the row's
+ *     position: (a, b) -> (a c - b s, b c + a s), where (a, b) are features
+ *     (j, j + rot_dim / 2), or (2j, 2j + 1) if pairs != 0, and c, s are
+ *     rope[position][j], rope[position][rot_dim / 2 + j] (fp32 [n_pos][rot_dim];
+ *     rot_dim a multiple of 8 up to dim, 0: no rotation, rope may be NULL);
+ *   - write q [n_tokens][q_heads][dim] (q_type KQ_T_BF16 or KQ_T_F16), and k
+ *     and v to the rows' slots of the cache, divided by k_scale / v_scale
+ *     (KQ_T_F8: clamped to +-448).
+ * positions (int32 [n_tokens]; NULL: the row's slot) is the place of each row
+ * in its text: in a tree of drafts several rows share one.  Positions outside
+ * [0, n_pos) are taken at the nearest end.  The arithmetic is fp32, each
+ * result rounded once (to nearest even).  Slots that no row belongs to keep what they
+ * held.  Two rows must not share a slot.
+ */
+int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x, int64_t ldx,
+                   int64_t q_heads, const float *q_norm, const float *k_norm, float eps,
+                   const float *rope, int64_t n_pos, int64_t rot_dim, int pairs,
+                   const int32_t *positions, int q_type, void *q, hipStream_t stream);
+
+/*
+ * Attention of each sequence's new rows (at most KQ_ATTN_MAX_TOKENS) over its
+ * cache, their own keys and values already in it:
+ *   out[i][h] = sum_s p_s v_s,   p = softmax_s(scale * q[i][h] . k_s),
+ * over the slots s < lens[b] and those slots lens[b] + j whose bit j is set in
+ * mask[i] (uint64 [n_tokens], bit j = the sequence's j-th new row, its own bit
+ * included where it attends to itself; NULL: row i sees the rows 0..i of its
+ * sequence).  Head h reads key head h / (q_heads / heads).  A row that sees
+ * nothing gives 0, and what an unseen slot holds (infinities and NaN too)
+ * does not count.
+ *   q     [n_tokens][q_heads][dim], KQ_T_BF16 or KQ_T_F16; the cache holds the
+ *         same type or KQ_T_F8 (converted to q's type, exactly)
+ *   out   [n_tokens][q_heads][dim], q's type or KQ_T_F32 (the same sums before
+ *         the last rounding)
+ * Scores, maxima and sums are fp32; the probabilities enter the second product
+ * in q's type.  max_tokens is an upper bound of the rows of a sequence (rows
+ * past it are not computed) and max_len of lens[b] + its rows (slots past it
+ * are not read): they size the launch.  The workspace holds the partial sums of
+ * the parts a long sequence is cut into; the same call gives the same bits.
+ * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31.
+ */
+#define KQ_ATTN_MAX_TOKENS 64
+int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q,
+                 int64_t q_heads, const uint64_t *mask, float scale, int64_t max_tokens,
+                 int64_t max_len, int out_type, void *out, void *workspace, size_t workspace_bytes,
+                 hipStream_t stream);
+/* Workspace bytes of that call (0: none needed); 0 for invalid arguments. */
+size_t kq_attn_tree_workspace(const kq_cache *cache, const kq_batch *batch, int64_t q_heads,
+                              int64_t max_tokens, int64_t max_len);
+
+/*
+ * Keep an accepted branch: for j < counts[b] (int32 [n_seqs], at most
+ * KQ_KEEP_MAX_TOKENS), slot lens[b] + j of sequence b takes what slot
+ * lens[b] + path[offsets[b] + j] held before the call (path: int32 [n_tokens],
+ * values in [0, rows of the sequence)), in the keys and values of every one of
+ * the n_caches caches (host array; one per layer, alike in all but k and v).
+ * The caller then counts counts[b] more tokens in the cache.
+ */
+#define KQ_KEEP_MAX_TOKENS 64
+int kq_cache_keep(const kq_cache *caches, int64_t n_caches, const kq_batch *batch,
+                  const int32_t *path, const int32_t *counts, hipStream_t stream);
+
+/*
+ * Log probabilities of the rows of logits [M][V] (type KQ_T_F32, KQ_T_BF16 or
+ * KQ_T_F16; row stride ldx elements): with lse = log sum_v exp(x_v),
+ *   logprob [M][n_given] = x[t] - lse for t = tokens[m][i] (int32
+ *                          [M][n_given]; a t outside [0, V) gives -infinity)
+ *   entropy [M]          = -sum p log p, p = exp(x - lse)
+ *   top_ids [M][n_top], top_logprobs [M][n_top]: the largest logits, the
+ *                          lowest index first among equal ones
+ * all fp32 (ids int32), from one pass over the logits.  n_given and n_top may
+ * be 0; entropy may be NULL.  n_top is at most KQ_LOGPROBS_MAX_TOP and V.
+ * A logit of -infinity has no probability (and counts 0 in the entropy); a row
+ * of nothing else, or with +infinity or a NaN in it, has no distribution: its
+ * floats are NaN (-infinity for a t outside [0, V)), and a NaN leaves its ids
+ * unspecified (in [0, V)).  The same call gives the same bits.
+ */
+#define KQ_LOGPROBS_MAX_TOP 64
+int kq_logprobs(int type, const void *logits, int64_t M, int64_t V, int64_t ldx,
+                const int32_t *tokens, int64_t n_given, int64_t n_top, float *logprob,
+                float *entropy, int32_t *top_ids, float *top_logprobs, void *workspace,
+                size_t workspace_bytes, hipStream_t stream);
+/* Workspace bytes of that call (0: none needed); 0 for invalid arguments. */
+size_t kq_logprobs_workspace(int64_t M, int64_t V, int64_t n_top);
 
 /* Per-variant dispatch counters (incremented on each successful launch) and
  * their names, so tests can prove which kernel variant ran (vllm.cpp PR 3036
