@@ -12,19 +12,16 @@
 // the keys are dealt such that the scores a lane gets ARE the 8 consecutive
 // keys it must supply.  K rows and (the cache keeps values transposed) V rows
 // are then operands as they lie in memory: 16 bytes of a lane, straight into
-// registers, no LDS.
+// registers.
 //
 // One pass over the keys with the running maximum m and sum l of a softmax in
 // fp32.  m is raised only when a score passes it by more than 8 (in log2
 // units): until then exp2(S - m) stays within 2^8, far inside every type, and
 // neither a cross-lane maximum nor a rescaling of O is needed.
 //
-// A wave takes 32 keys at a time for RW query rows: 16 where a sequence brings
-// no more, or where dim is 256 (a wave of 32 would need 320 registers for its
-// sums and operands alone), else 32.  The waves of a workgroup share the
-// rows (WR of them side by side) and cut the keys; their sums are joined in
-// LDS.  A sequence's slots are cut into parts so that few long sequences fill
-// the chip; a second kernel joins the parts.
+// A wave holds the sums of RW query rows (16 or 32).  A sequence's slots are cut
+// into parts so that few long sequences fill the chip; a second kernel joins
+// the parts.
 #include "kq_step_device.hpp"
 
 namespace kq {
@@ -69,6 +66,20 @@ struct Mfma<_Float16, 32> {
     }
 };
 
+// Which of 8 keys a row sees (bit e: the e-th), the first being node `node` of
+// the drafted tokens (below 0: that many cached ones come first).  sees: the
+// row's mask, cut to the sequence's rows.
+__device__ __forceinline__ uint32_t seen8(uint64_t sees, int node) {
+    const uint32_t drafted = node > 63 ? 0u : (uint32_t)(sees >> (node & 63));
+    const int cached = min(max(-node, 0), 8);
+    const uint32_t both = (uint32_t)sees << cached | ((1u << cached) - 1u);
+    return node >= 0 ? drafted : both;
+}
+
+// Marks of infinite and NaN values: whole numbers that both 16-bit types hold,
+// set so far apart that sums of 32 do not run into the next.
+constexpr float MARK_POS = 1.f, MARK_NEG = 128.f, MARK_NAN = 16384.f;
+
 // Eight cached values as they lie in memory, and as an operand.
 template <class E, bool F8>
 struct Frag;
@@ -84,23 +95,23 @@ struct Frag<E, false> {
             r[j] &= k >= 2 ? 0xFFFFFFFFu : k == 1 ? 0xFFFFu : 0u;
         }
     }
-    // the values that are infinite or NaN, zeros in place of the others
-    static __device__ __forceinline__ raw odd(raw r) {
+    // infinite and NaN values become zeros; whether there were any
+    static __device__ __forceinline__ bool drop_odd(raw &r) {
         constexpr uint32_t e = std::is_same_v<E, __bf16> ? 0x7F80u : 0x7C00u;
-        raw x;
+        bool any = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool lo = (r[j] & e) == e, hi = (r[j] & (e << 16)) == e << 16;
-            x[j] = r[j] & ((lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u));
+            r[j] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+            any = any || lo || hi;
         }
-        return x;
+        return any;
     }
-    static __device__ __forceinline__ bool any(raw r) { return (r[0] | r[1] | r[2] | r[3]) != 0; }
-    // value e alone (none for e < 0)
-    static __device__ __forceinline__ raw only(raw r, int e) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] &= e >> 1 == j ? (e & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-        return r;
+    // a value's mark: see add_odd
+    static __device__ __forceinline__ float mark(raw r, int i) {
+        constexpr uint32_t e = std::is_same_v<E, __bf16> ? 0x7F80u : 0x7C00u;
+        const uint32_t x = r[i >> 1] >> (16 * (i & 1)) & 0xFFFFu;
+        return (x & 0x7FFFu) < e ? 0.f : (x & 0x7FFFu) > e ? MARK_NAN : x >> 15 ? MARK_NEG : MARK_POS;
     }
     template <class OP>
     static __device__ __forceinline__ OP op(raw r) {
@@ -118,21 +129,19 @@ struct Frag<E, true> {
             r[j] &= k == 4 ? ~0u : (1u << (8 * k)) - 1u;
         }
     }
-    static __device__ __forceinline__ raw odd(raw r) {
-        raw x;
+    static __device__ __forceinline__ bool drop_odd(raw &r) {
+        uint32_t any = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            // bit 7 of a byte of n: its low 7 bits are all ones (the one NaN of either sign)
-            const uint32_t n = ((r[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            x[j] = r[j] & ((n >> 7) * 0xFFu);
+            // bit 7 of a byte: its low 7 bits are all ones (the NaN of either sign)
+            const uint32_t x = ((r[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            r[j] &= ~((x >> 7) * 0xFFu);
+            any |= x;
         }
-        return x;
+        return any != 0;
     }
-    static __device__ __forceinline__ bool any(raw r) { return (r[0] | r[1]) != 0; }
-    static __device__ __forceinline__ raw only(raw r, int e) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) r[j] &= e >> 2 == j ? 0xFFu << (8 * (e & 3)) : 0u;
-        return r;
+    static __device__ __forceinline__ float mark(raw r, int i) {
+        return ((r[i >> 2] >> (8 * (i & 3))) & 0x7Fu) == 0x7Fu ? MARK_NAN : 0.f;
     }
     static __device__ __forceinline__ uint32_t pair(uint32_t r, bool hi) {
         if constexpr (std::is_same_v<E, __bf16>)
@@ -149,42 +158,77 @@ struct Frag<E, true> {
     }
 };
 
-template <int D, int RW, int WR>
-constexpr int attn_lds_floats() {
-    constexpr int o = 4 * RW * (D + 4) + 8 * RW;
-    return o;
+// Where a sequence's values lie, for what add_odd reads again.
+struct ValueRows {
+    const CacheArgs &cache;
+    const BatchArgs &batch;
+    int b, h, len, total;
+};
+
+// An infinity or NaN among the values of drafted tokens belongs to the rows that
+// see its token and to no other, but a product with P would spoil them all (0 *
+// inf).  Such values are zeros in the product; here they are added for one step
+// of it (512 / RW keys from key0): marks of them times a 0 / 1 matrix of who
+// sees what count the infinities and NaNs that reach each sum.
+template <class E, bool F8, int D, int RW>
+__device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane, uint64_t sees,
+                                        typename Mfma<E, RW>::acc (&o)[D / RW]) {
+    typedef Mfma<E, RW> MM;
+    typedef Frag<E, F8> FR;
+    constexpr int ES = FR::BYTES;
+    const int n = lane & (RW - 1), g = lane / RW;
+    const int key = key0 + 8 * g;  // the first of this lane's 8
+    const uint32_t on = seen8(sees, key - va.len);
+    v4u w = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e >> 1] |= (on >> e & 1u) * (pack2<E>(1.f, 0.f) << (16 * (e & 1)));
+    const typename MM::op seen = __builtin_bit_cast(typename MM::op, w);
+    const int shift = va.cache.page_shift;
+    const int slot = min(key & ~15, (va.total - 1) & ~15);
+    const char *p = va.cache.v +
+                    (((int64_t)slot_page(va.cache, va.batch, va.b, slot) * va.cache.heads + va.h) * D << shift) * ES +
+                    ((slot & ((1 << shift) - 1)) + (key & 8)) * ES;
+#pragma unroll
+    for (int d = 0; d < D / RW; ++d) {
+        typename FR::raw r = *reinterpret_cast<const typename FR::raw *>(p + ((d * RW + n) << shift) * ES);
+        FR::first(r, min(max(va.total - key, 0), 8));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack2<E>(FR::mark(r, 2 * j), FR::mark(r, 2 * j + 1));
+        const typename MM::acc count =
+            MM::mul(__builtin_bit_cast(typename MM::op, w), seen, typename MM::acc{});
+#pragma unroll
+        for (int i = 0; i < RW * RW / 64; ++i) {
+            const int c = (int)count[i];
+            float x = (c & 127) ? __builtin_inff() : 0.f;
+            x = c & (127 << 7) ? x - __builtin_inff() : x;
+            o[d][i] += c >> 14 ? __builtin_nanf("") : x;
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one at a time: this path must not cost the others registers
+    }
 }
 
-// Workgroup: 4 waves, WR side by side over the rows, 4 / WR over the keys.
-template <class E, bool F8, int D, int RW, int WR>
-__global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
+// Up to 16 rows: one wave's worth, so the 4 waves of a workgroup cut the keys
+// (32 at a time in turn) and their sums are joined in LDS.
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void attn_few_kernel(const AttnArgs a) {
+    constexpr int RW = 16;
     typedef Mfma<E, RW> MM;
     typedef typename MM::op op_t;
     typedef typename MM::acc acc_t;
     typedef Frag<E, F8> FR;
     typedef typename FR::raw raw_t;
-    constexpr int NG = 64 / RW;         // lane groups
-    constexpr int KT = RW == 16 ? 2 : 1;  // results of the first product over 32 keys
-    constexpr int KS = RW == 16 ? 1 : 2;  // steps of the second product over 32 keys
-    constexpr int NK = D / (8 * NG);    // steps of the first product
-    constexpr int ND = D / RW;          // results of the second product
-    constexpr int NR = RW * RW / 64;    // result registers
-    constexpr int WK = 4 / WR;
+    constexpr int NK = D / 32;  // steps of the first product
+    constexpr int ND = D / RW;  // results of the second product
     constexpr int ES = FR::BYTES;
 
-    extern __shared__ float lds[];
+    __shared__ float lo[4 * RW * (D + 4)];  // sums of the waves: [wave][row][dim]
+    __shared__ float lm[4 * RW], ll[4 * RW];
 
-    // part c of key head h of sequence b, row block rb: the row blocks of one
-    // part run on one XCD (workgroups are dealt round robin to the 8), which
-    // then reads the part once
-    const int id = blockIdx.x;
-    const int rb = (id >> 3) % a.row_blocks;
-    const int64_t item = (int64_t)((id >> 3) / a.row_blocks) * 8 + (id & 7);
+    // part c of key head h of sequence b
+    const int64_t item = blockIdx.x;
     const int c = (int)(item % a.parts);
     const int h = (int)(item / a.parts % a.cache.heads);
-    const int64_t b64 = item / a.parts / a.cache.heads;
-    if (b64 >= a.batch.n_seqs) return;
-    const int b = (int)b64;
+    const int b = (int)(item / a.parts / a.cache.heads);
     int first, T;
     batch_rows(a.batch, b, first, T);
     T = min(T, a.max_tokens);
@@ -192,39 +236,30 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
     const int len = max(a.batch.lens[b], 0);
     const int total = min(len, INT32_MAX - 64) + T;
     const int from = c * a.part;
-    if (rb * a.rows_wg >= R || from >= total) return;
+    if (R == 0 || from >= total) return;
     const int to = min(from + a.part, total);
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & (RW - 1), g = lane / RW;
-    const int wr = wave / WK, wk = wave % WK;
-    const int row = rb * a.rows_wg + wr * RW + n;
-    const bool used = row < R;
-    const int tok = used ? row / G : 0;
-    const int head = h * G + (used ? row % G : 0);
+    const int n = lane & 15, g = lane >> 4;
+    const bool used = n < R;
+    const int tok = used ? n / G : 0;
+    const int head = h * G + (used ? n % G : 0);
     const int64_t q_row = (int64_t)(first + tok) * ((int64_t)a.cache.heads * G) + head;
 
     op_t qf[NK];
 #pragma unroll
     for (int kk = 0; kk < NK; ++kk) {
         v4u w = {0u, 0u, 0u, 0u};
-        if (used) w = *reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (kk * NG + g)) * 2);
+        if (used) w = *reinterpret_cast<const v4u *>(a.q + (q_row * D + 32 * kk + 8 * g) * 2);
         qf[kk] = __builtin_bit_cast(op_t, w);
     }
     uint64_t sees = 0;
-    if (used) sees = a.mask ? a.mask[first + tok] : (2ull << tok) - 1ull;
+    if (used) sees = (a.mask ? a.mask[first + tok] : (2ull << tok) - 1ull) & ((2ull << (T - 1)) - 1ull);
 
-    // Key of row m of the first product's result t: see the head of the file.
-    int krow[KT];
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-        const int j = n >> 2, i = n & 3;
-        if constexpr (RW == 16)
-            krow[t] = 8 * j + 4 * t + i;
-        else
-            krow[t] = 16 * (j >> 2) + 8 * (j & 1) + 4 * ((j >> 1) & 1) + i;
-    }
+    // Key of this lane's row of the first product's two results (of 16 keys each):
+    // see the head of the file.
+    const int krow[2] = {8 * (n >> 2) + (n & 3), 8 * (n >> 2) + 4 + (n & 3)};
     // Addresses: 16 consecutive slots from a multiple of 16 lie in one page, so a
     // tile of 32 has two runs whose addresses are the same for the whole wave
     // (scalar registers); a lane adds its place in its run, which never changes.
@@ -247,26 +282,21 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
         }
         return r;
     };
-    auto load_k = [&](const Runs &ru, raw_t(&kf)[KT][NK]) {
+    // (both of a lane's keys lie in the same run)
+    auto load_k = [&](const Runs &ru, raw_t(&kf)[2][NK]) {
+        const int64_t at = n >> 3 ? ru.page[1] + ru.slot[1] * (D * ES) : ru.page[0] + ru.slot[0] * (D * ES);
+        const char *p = a.cache.k + at + ((krow[0] & 15) * (D * ES) + 8 * g * ES);
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            const int i = krow[t] >> 4;
-            const int64_t at = i ? ru.page[1] + ru.slot[1] * (D * ES) : ru.page[0] + ru.slot[0] * (D * ES);
-            const char *p = a.cache.k + at + ((krow[t] & 15) * (D * ES) + 8 * g * ES);
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) kf[t][kk] = *reinterpret_cast<const raw_t *>(p + kk * NG * 8 * ES);
-        }
+            for (int kk = 0; kk < NK; ++kk) kf[t][kk] = *reinterpret_cast<const raw_t *>(p + (4 * t * D + 32 * kk) * ES);
     };
-    auto load_v = [&](const Runs &ru, raw_t(&vf)[ND][KS]) {
+    auto load_v = [&](const Runs &ru, raw_t(&vf)[ND]) {
+        const int64_t at = g >> 1 ? ru.page[1] + ru.slot[1] * ES : ru.page[0] + ru.slot[0] * ES;
+        const char *p = a.cache.v + at + ((n << page_shift) + 8 * (g & 1)) * ES;
+        const int step = (RW * ES) << page_shift;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int i = RW == 32 ? s : g >> 1;
-            const int64_t at = i ? ru.page[1] + ru.slot[1] * ES : ru.page[0] + ru.slot[0] * ES;
-            const char *p = a.cache.v + at + ((n << page_shift) + 8 * (g & 1)) * ES;
-            const int step = (RW * ES) << page_shift;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) vf[d][s] = *reinterpret_cast<const raw_t *>(p + d * step);
-        }
+        for (int d = 0; d < ND; ++d) vf[d] = *reinterpret_cast<const raw_t *>(p + d * step);
     };
 
     acc_t o[ND];
@@ -274,44 +304,54 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
     for (int d = 0; d < ND; ++d) o[d] = acc_t{};
     float m = M_START, l = 0.f;
 
-    int key0 = from + 32 * wk;
+    int key0 = from + 32 * wave;
     Runs ru = runs(key0);
-    raw_t kf[KT][NK];
-    if (key0 < to) load_k(ru, kf);
-    for (; key0 < to; key0 += 32 * WK) {
-        raw_t vf[ND][KS];
-        load_v(ru, vf);
-        const int next = key0 + 32 * WK;
-        ru = runs(next);
+    // Keys are loaded a turn ahead, values at the turn's begin, where the
+    // registers hold both (512 bytes of a lane at dim 256 they do not: there
+    // each is loaded when the other is done with).
+    constexpr bool AHEAD = D * ES <= 256;
+    raw_t kf[2][NK];
+    if (AHEAD && key0 < to) load_k(ru, kf);
+    for (; key0 < to; key0 += 128) {
+        raw_t vf[ND];
+        const int next = key0 + 128;
+        if constexpr (AHEAD) {
+            load_v(ru, vf);
+            ru = runs(next);
+        } else {
+            load_k(ru, kf);
+        }
 
-        acc_t sc[KT];
+        acc_t sc[2];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
+        for (int t = 0; t < 2; ++t) {
             sc[t] = acc_t{};
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(kf[t][kk]), qf[kk], sc[t]);
         }
-        if (next < to) load_k(ru, kf);
+        if constexpr (AHEAD) {
+            if (next < to) load_k(ru, kf);
+        } else {
+            load_v(ru, vf);
+            ru = runs(next);
+        }
 
-        // p[8 s + e]: key key0 + 16 s + 8 g + e of this lane's row
-        float p[8 * KS];
+        // p[e]: key key0 + 8 g + e of this lane's row
+        float p[8];
 #pragma unroll
-        for (int r = 0; r < 8 * KS; ++r) p[r] = sc[r / NR][r % NR] * a.score_scale;
+        for (int r = 0; r < 8; ++r) p[r] = sc[r >> 2][r & 3] * a.score_scale;
         const bool ragged = key0 + 32 > len;
         if (ragged) {
+            const uint32_t on = seen8(sees, key0 + 8 * g - len);
 #pragma unroll
-            for (int r = 0; r < 8 * KS; ++r) {
-                const int key = key0 + 16 * (r >> 3) + 8 * g + (r & 7);
-                const bool on = key < len || (key < total && ((sees >> (key - len)) & 1ull));
-                p[r] = on ? p[r] : -__builtin_inff();
-            }
+            for (int r = 0; r < 8; ++r) p[r] = on >> r & 1u ? p[r] : -__builtin_inff();
         }
         float top = p[0];
 #pragma unroll
-        for (int r = 1; r < 8 * KS; ++r) top = fmaxf(top, p[r]);
+        for (int r = 1; r < 8; ++r) top = fmaxf(top, p[r]);
         if (__any(top > m + M_SLACK)) {
-#pragma unroll
-            for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
             const float up = fmaxf(m, top);
             const float f = __builtin_amdgcn_exp2f(m - up);
             m = up;
@@ -319,94 +359,59 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] *= f;
         }
+        v4u w;
 #pragma unroll
-        for (int r = 0; r < 8 * KS; ++r) {
-            p[r] = __builtin_amdgcn_exp2f(p[r] - m);
-            l += p[r];
+        for (int j = 0; j < 4; ++j) {
+            const float p0 = __builtin_amdgcn_exp2f(p[2 * j] - m), p1 = __builtin_amdgcn_exp2f(p[2 * j + 1] - m);
+            l += p0 + p1;
+            w[j] = pack2<E>(p0, p1);
         }
-        op_t pf[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            v4u w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack2<E>(p[8 * s + 2 * j], p[8 * s + 2 * j + 1]);
-            pf[s] = __builtin_bit_cast(op_t, w);
-        }
+        const op_t pf = __builtin_bit_cast(op_t, w);
+        bool odd = false;
         if (ragged) {
-            // Slots past the end hold anything: zeros. An infinity or NaN of a
-            // slot that some rows do not see would spoil those rows too (0 *
-            // inf), so such values leave the product below and are added here,
-            // one key at a time, to the rows (columns, so lanes) that see it.
+            // slots past the end hold anything: zeros
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    FR::first(vf[d][s], min(max(total - (key0 + 16 * s + 8 * g), 0), 8));
-                    const raw_t odd = FR::odd(vf[d][s]);
-                    if (__any(FR::any(odd))) {
-#pragma nounroll
-                        for (int kx = 0; kx < 8 * NG; ++kx) {
-                            const int key = key0 + 16 * s + kx;
-                            const bool on = key < len || (key < total && ((sees >> ((key - len) & 63)) & 1ull));
-                            const int e = kx >> 3 == g ? kx & 7 : -1;
-                            const op_t pk = __builtin_bit_cast(
-                                op_t, Frag<E, false>::only(__builtin_bit_cast(v4u, pf[s]), e));
-                            const acc_t sum = MM::mul(FR::template op<op_t>(FR::only(odd, e)), pk, o[d]);
-#pragma unroll
-                            for (int r = 0; r < NR; ++r) o[d][r] = on ? sum[r] : o[d][r];
-                        }
-                        vf[d][s] ^= odd;
-                    }
-                }
+            for (int d = 0; d < ND; ++d) {
+                FR::first(vf[d], min(max(total - (key0 + 8 * g), 0), 8));
+                odd |= FR::drop_odd(vf[d]);
+            }
         }
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[d][s]), pf[s], o[d]);
+        for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[d]), pf, o[d]);
+        if (__any(odd)) add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, len, total}, key0, lane, sees, o);
     }
 
-    // Join the waves: o to LDS as [wave][row][dim], weights beside it.
+    // Join the waves.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
 #pragma unroll
-    for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
-    float *lo = lds, *lm = lds + 4 * RW * (D + 4), *ll = lm + 4 * RW;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < NR; r += 4) {
-            const int dim = d * RW + 8 * (r >> 2) + 4 * g;
-            *reinterpret_cast<v4f *>(lo + (wave * RW + n) * (D + 4) + dim) =
-                v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]};
-        }
+    for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f *>(lo + (wave * RW + n) * (D + 4) + d * RW + 4 * g) = o[d];
     if (g == 0) {
         lm[wave * RW + n] = m;
         ll[wave * RW + n] = l;
     }
     __syncthreads();
-    constexpr int TPR = 256 / (RW * WR);  // threads to a row
-    constexpr int VPT = D / TPR;          // values to a thread: 4 at a time, TPR * 4 apart
-    const int jr = threadIdx.x / TPR, jt = threadIdx.x % TPR;
-    const int out_row = rb * a.rows_wg + jr;
+    const int out_row = threadIdx.x >> 4, jt = threadIdx.x & 15;  // 16 threads to a row
     if (out_row >= R) return;
-    const int jn = (jr / RW) * WK * RW + jr % RW;  // [wave][row] index of the row's first key wave
     float mm = M_START;
 #pragma unroll
-    for (int k = 0; k < WK; ++k) mm = fmaxf(mm, lm[jn + k * RW]);
-    float f[WK], sum = 0.f;
+    for (int k = 0; k < 4; ++k) mm = fmaxf(mm, lm[out_row + k * RW]);
+    float f[4], sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < WK; ++k) {
-        f[k] = __builtin_amdgcn_exp2f(lm[jn + k * RW] - mm);
-        sum += f[k] * ll[jn + k * RW];
+    for (int k = 0; k < 4; ++k) {
+        f[k] = __builtin_amdgcn_exp2f(lm[out_row + k * RW] - mm);
+        sum += f[k] * ll[out_row + k * RW];
     }
     const int64_t part_row = (((int64_t)b * heads + h) * a.parts + c) * ((int64_t)a.max_tokens * G) + out_row;
     const bool whole = a.parts == 1;
     const float norm = whole ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
     const int64_t o_row = ((int64_t)(first + out_row / G) * ((int64_t)heads * G) + h * G + out_row % G) * D;
 #pragma unroll
-    for (int v = 0; v < VPT; v += 4) {
-        const int dim = v * TPR + jt * 4;
+    for (int v = 0; v < D; v += 64) {
+        const int dim = v + jt * 4;
         v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < WK; ++k) acc += f[k] * *reinterpret_cast<const v4f *>(lo + (jn + k * RW) * (D + 4) + dim);
+        for (int k = 0; k < 4; ++k) acc += f[k] * *reinterpret_cast<const v4f *>(lo + (out_row + k * RW) * (D + 4) + dim);
         acc *= norm;
         if (!whole)
             *reinterpret_cast<v4f *>(a.ws_o + part_row * D + dim) = acc;
@@ -418,6 +423,263 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
     if (!whole && jt == 0) {
         a.ws_ml[2 * part_row] = mm;
         a.ws_ml[2 * part_row + 1] = sum;
+    }
+}
+
+// The same sums for sequences that bring more than a wave's rows: 4 waves of 32
+// rows share tiles of KEYS keys staged in LDS (two tiles: one in use, one being
+// written; the registers hold the one after).  Read from memory a line at a
+// time, a tile is read once for 128 rows instead of once for each wave.
+// LDS holds 16-byte pieces; a row's pieces are permuted by an XOR with bits of
+// the row, so that the lanes of a read, which want one piece of many rows, meet
+// different banks.
+template <class E, bool F8, int D>
+struct Tile {
+    static constexpr int ES = F8 ? 1 : 2;
+    static constexpr int KEYS = D == 256 ? 32 : 64;
+    static constexpr int KB = D * ES, VB = KEYS * ES;          // bytes of a key row and of a feature row
+    static constexpr int KP = KB / 16, VP = VB / 16;           // their 16-byte pieces
+    static constexpr int KROWS = KEYS / 4, VROWS = D / 4;      // rows that one wave stages
+    static constexpr int KN = KROWS * KB / 1024, VN = VROWS * VB / 1024;  // loads of a lane
+    static constexpr int K_BYTES = KEYS * KB, BYTES = K_BYTES + D * VB;
+
+    static __device__ __forceinline__ int k_pos(int key, int piece) {
+        const int f = KP >= 8 ? (key & 3) | ((key >> 1) & 4) : (key >> 1) & (KP - 1);
+        return key * KB + (piece ^ f) * 16;
+    }
+    static __device__ __forceinline__ int v_pos(int d, int piece) {
+        const int f = VP == 8 ? d & 7 : VP == 4 ? (d >> 1) & 3 : (d >> 2) & 1;
+        return K_BYTES + d * VB + (piece ^ f) * 16;
+    }
+};
+
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
+    constexpr int RW = D == 256 ? 16 : 32;
+    typedef Mfma<E, RW> MM;
+    typedef typename MM::op op_t;
+    typedef typename MM::acc acc_t;
+    typedef Frag<E, F8> FR;
+    typedef typename FR::raw raw_t;
+    typedef Tile<E, F8, D> TL;
+    constexpr int ES = TL::ES, KEYS = TL::KEYS;
+    constexpr int NG = 64 / RW;                    // lane groups: 8 of a step's keys, 8 of a step's features to each
+    constexpr int NK = D / (8 * NG), ND = D / RW;  // steps of the first product, results of the second
+    constexpr int NT = KEYS / RW, NS = KEYS / (8 * NG);  // results of the first, steps of the second
+    constexpr int NR = RW * RW / 64;
+
+    __shared__ __align__(16) char tile[2 * TL::BYTES];
+    __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
+
+    const int id = blockIdx.x;
+    const int rb = (id >> 3) % a.row_blocks;
+    const int64_t item = (int64_t)((id >> 3) / a.row_blocks) * 8 + (id & 7);
+    const int c = (int)(item % a.parts);
+    const int h = (int)(item / a.parts % a.cache.heads);
+    const int64_t b64 = item / a.parts / a.cache.heads;
+    if (b64 >= a.batch.n_seqs) return;
+    const int b = (int)b64;
+    int first, T;
+    batch_rows(a.batch, b, first, T);
+    T = min(T, a.max_tokens);
+    const int G = a.group, R = T * G;
+    const int len = max(a.batch.lens[b], 0);
+    const int total = min(len, INT32_MAX - 64) + T;
+    const int from = c * a.part;
+    if (rb * a.rows_wg >= R || from >= total) return;
+    const int to = min(from + a.part, total);
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & (RW - 1), g = lane / RW;
+    const int row = rb * a.rows_wg + wave * RW + n;
+    const bool used = row < R;
+    const int tok = used ? row / G : 0;
+    const int head = h * G + (used ? row % G : 0);
+    const int heads = a.cache.heads;
+    const int64_t q_row = (int64_t)(first + tok) * ((int64_t)heads * G) + head;
+
+    op_t qf[NK];
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+        v4u w = {0u, 0u, 0u, 0u};
+        if (used) w = *reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (NG * kk + g)) * 2);
+        qf[kk] = __builtin_bit_cast(op_t, w);
+    }
+    uint64_t sees = 0;
+    if (used) sees = (a.mask ? a.mask[first + tok] : (2ull << tok) - 1ull) & ((2ull << (T - 1)) - 1ull);
+
+    // staging: this lane's rows and pieces
+    const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
+    const int64_t head_bytes = (int64_t)D * ES << page_shift;
+    const int last_run = (total - 1) & ~15;
+    const int k_row = wave * TL::KROWS + lane / TL::KP, k_piece = lane % TL::KP;  // + i * 64 / KP
+    const int v_row = wave * TL::VROWS + lane / TL::VP, v_piece = lane % TL::VP;
+    const int v_run = v_piece * (16 / ES) >> 4;
+    const int v_off = (v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1));
+    v4u stage[TL::KN + TL::VN];
+    auto head_page = [&](int slot) { return ((int64_t)slot_page(a.cache, a.batch, b, slot) * heads + h) * head_bytes; };
+    auto load = [&](int key0) {
+        const int k_slot = min(key0 + (wave * TL::KROWS & ~15), last_run);  // one run to a wave
+        const char *kp = a.cache.k + head_page(k_slot) + (k_slot & page_mask) * TL::KB;
+        const int k_off = (k_row & 15) * TL::KB + k_piece * 16;
+#pragma unroll
+        for (int i = 0; i < TL::KN; ++i) stage[i] = *reinterpret_cast<const v4u *>(kp + k_off + i * 1024);
+        const char *vp = a.cache.v;
+        int64_t at = 0;
+#pragma unroll
+        for (int r = 0; r < KEYS / 16; ++r) {
+            const int slot = min(key0 + 16 * r, last_run);
+            const int64_t o = head_page(slot) + (slot & page_mask) * ES;
+            at = r == v_run ? o : at;
+        }
+        vp += at + v_off;
+#pragma unroll
+        for (int i = 0; i < TL::VN; ++i)
+            stage[TL::KN + i] = *reinterpret_cast<const v4u *>(vp + ((int64_t)(i * (64 / TL::VP)) << page_shift) * ES);
+    };
+    auto store = [&](char *to_lds, int key0) {
+        if (key0 + KEYS > len) {
+            // slots past the end hold anything: zeros; infinite and NaN values of
+            // drafted tokens: zeros here, and noted
+            const int left = total - (key0 + v_piece * (16 / ES));
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < TL::VN; ++i) {
+                v4u &r = stage[TL::KN + i];
+                if constexpr (F8) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        raw_t half = {r[2 * j], r[2 * j + 1]};
+                        FR::first(half, min(max(left - 8 * j, 0), 8));
+                        found |= FR::drop_odd(half);
+                        r[2 * j] = half[0];
+                        r[2 * j + 1] = half[1];
+                    }
+                } else {
+                    FR::first(r, min(max(left, 0), 8));
+                    found |= FR::drop_odd(r);
+                }
+            }
+            if (found) odd = 1;
+        }
+#pragma unroll
+        for (int i = 0; i < TL::KN; ++i)
+            *reinterpret_cast<v4u *>(to_lds + TL::k_pos(k_row + i * (64 / TL::KP), k_piece)) = stage[i];
+#pragma unroll
+        for (int i = 0; i < TL::VN; ++i)
+            *reinterpret_cast<v4u *>(to_lds + TL::v_pos(v_row + i * (64 / TL::VP), v_piece)) = stage[TL::KN + i];
+    };
+    // where this lane reads: 8 values of a key (or feature) from an even or odd half piece
+    const int krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+    auto k_frag = [&](const char *at, int t, int kk) {
+        const int key = RW == 16 ? krow + 32 * (t >> 1) + 4 * (t & 1) : krow + 32 * t;
+        const int half = NG * kk + g;  // in units of 8 values
+        return *reinterpret_cast<const raw_t *>(at + TL::k_pos(key, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
+    };
+    auto v_frag = [&](const char *at, int d, int s) {
+        const int half = NG * s + g;
+        return *reinterpret_cast<const raw_t *>(at + TL::v_pos(RW * d + n, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
+    };
+
+    acc_t o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = acc_t{};
+    float m = M_START, l = 0.f;
+
+    load(from);
+    if (threadIdx.x == 0) odd = 0;
+    __syncthreads();
+    store(tile, from);
+    load(from + KEYS);  // (past the end: the last run again)
+    int odd_tile = 0;
+    for (int key0 = from; key0 < to; key0 += KEYS) {
+        __syncthreads();
+        const char *at = tile + odd_tile * TL::BYTES;
+        acc_t sc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            sc[t] = acc_t{};
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(k_frag(at, t, kk)), qf[kk], sc[t]);
+        }
+        // p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's row
+        float p[NT * NR];
+#pragma unroll
+        for (int r = 0; r < NT * NR; ++r) p[r] = sc[r / NR][r % NR] * a.score_scale;
+        const bool ragged = key0 + KEYS > len;
+        if (ragged) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t on = seen8(sees, key0 + 8 * NG * s + 8 * g - len);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
+            }
+        }
+        float top = p[0];
+#pragma unroll
+        for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
+        if (__any(top > m + M_SLACK)) {
+#pragma unroll
+            for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+            const float up = fmaxf(m, top);
+            const float f = __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= f;
+        }
+        op_t pf[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            v4u w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p0 = __builtin_amdgcn_exp2f(p[8 * s + 2 * j] - m);
+                const float p1 = __builtin_amdgcn_exp2f(p[8 * s + 2 * j + 1] - m);
+                l += p0 + p1;
+                w[j] = pack2<E>(p0, p1);
+            }
+            pf[s] = __builtin_bit_cast(op_t, w);
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(v_frag(at, d, s)), pf[s], o[d]);
+        if (ragged && odd) {
+            const ValueRows va = {a.cache, a.batch, b, h, len, total};
+#pragma nounroll
+            for (int s = 0; s < NS; ++s) add_odd<E, F8, D, RW>(va, key0 + 8 * NG * s, lane, sees, o);
+        }
+        odd_tile ^= 1;
+        if (key0 + KEYS < to) {
+            store(tile + odd_tile * TL::BYTES, key0 + KEYS);
+            load(key0 + 2 * KEYS);
+        }
+    }
+
+#pragma unroll
+    for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
+    if (!used) return;
+    const bool whole = a.parts == 1;
+    const float norm = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
+    const int64_t part_row = (((int64_t)b * heads + h) * a.parts + c) * ((int64_t)a.max_tokens * G) + row;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) {
+            const int dim = RW * d + 2 * r + 4 * g;
+            const v4f acc = v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * norm;
+            if (!whole)
+                *reinterpret_cast<v4f *>(a.ws_o + part_row * D + dim) = acc;
+            else if (a.out_f32)
+                *reinterpret_cast<v4f *>(reinterpret_cast<float *>(a.out) + q_row * D + dim) = acc;
+            else
+                *reinterpret_cast<v2u *>(a.out + (q_row * D + dim) * 2) = v2u{pack2<E>(acc[0], acc[1]), pack2<E>(acc[2], acc[3])};
+        }
+    if (!whole && g == 0) {
+        a.ws_ml[2 * part_row] = m;
+        a.ws_ml[2 * part_row + 1] = l;
     }
 }
 
@@ -487,32 +749,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
     }
 }
 
-template <class E, bool F8, int D, int RW, int WR>
-hipError_t launch(const AttnArgs &a, int64_t items, hipStream_t stream) {
-    const size_t lds = attn_lds_floats<D, RW, WR>() * sizeof(float);
-    auto *kernel = attn_kernel<E, F8, D, RW, WR>;
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    const unsigned grid = (unsigned)((items + 7) / 8 * 8 * a.row_blocks);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), lds, stream, a);
-    return hipGetLastError();
-}
-
 template <class E, bool F8, int D>
 hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
     const int64_t items = (int64_t)a.batch.n_seqs * a.cache.heads * a.parts;
-    hipError_t e;
-    if (p.rows_wave == 16 && p.rows_wg == 16)
-        e = launch<E, F8, D, 16, 1>(a, items, stream);
-    else if constexpr (D == 256)
-        e = p.rows_wg == 32 ? launch<E, F8, D, 16, 2>(a, items, stream) : launch<E, F8, D, 16, 4>(a, items, stream);
+    if (p.rows_wg == 16)
+        hipLaunchKernelGGL((attn_few_kernel<E, F8, D>), dim3((unsigned)items), dim3(256), 0, stream, a);
     else
-        e = p.rows_wg == 32   ? launch<E, F8, D, 32, 1>(a, items, stream)
-            : p.rows_wg == 64 ? launch<E, F8, D, 32, 2>(a, items, stream)
-                              : launch<E, F8, D, 32, 4>(a, items, stream);
+        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D>), dim3((unsigned)((items + 7) / 8 * 8 * a.row_blocks)), dim3(256),
+                           0, stream, a);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     hipLaunchKernelGGL((attn_join_kernel<E, D>), dim3((unsigned)a.batch.n_tokens, (unsigned)(a.cache.heads * a.group)),
                        dim3(256), 0, stream, a);

@@ -37,10 +37,10 @@ struct RopeArgs {
 // type / q_type: KQ_T_*; dim: 64, 128 or 256 (checked by the caller)
 hipError_t launch_rope_append(const RopeArgs &a, int type, int dim, int q_type, hipStream_t stream);
 
-// How attention over the cache is cut: rows_wave query rows to a wave, rows_wg
-// to a workgroup, each sequence's slots in parts of `part`.
+// How attention over the cache is cut: rows_wg query rows to a workgroup (16: the
+// kernel for few rows), each sequence's slots in parts of `part`.
 struct AttnPlan {
-    int rows_wave, rows_wg, row_blocks;
+    int rows_wg, row_blocks;
     int part, parts;
     int64_t o_bytes, bytes;  // workspace: sums of the parts, then their maxima and weights
 };

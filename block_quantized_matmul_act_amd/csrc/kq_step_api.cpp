@@ -86,8 +86,9 @@ namespace kq {
 AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len) {
     AttnPlan p;
     const int64_t rows = max_tokens * group;
-    p.rows_wave = rows <= 16 || dim == 256 ? 16 : 32;
-    p.rows_wg = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || dim == 256 ? 64 : 128;
+    // up to 16 rows: one wave of them; else 4 waves of 32 (dim 256: of 16, whose
+    // sums and operands fit the registers) on shared tiles
+    p.rows_wg = rows <= 16 ? 16 : dim == 256 ? 64 : 128;
     p.row_blocks = (int)((rows + p.rows_wg - 1) / p.rows_wg);
     // parts: enough workgroups for several on each of 256 compute units (ragged
     // sequences even out over them), of at least 128 slots (a tile to each wave)
@@ -205,7 +206,7 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     a.part = p.part;
     a.parts = p.parts;
     if (launch_attn(a, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
-    count_dispatch(p.rows_wave == 16 ? V_ATTN_FEW : V_ATTN_ROWS);
+    count_dispatch(p.rows_wg == 16 ? V_ATTN_FEW : V_ATTN_ROWS);
     return KQ_OK;
 }
 

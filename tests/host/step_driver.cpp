@@ -98,8 +98,7 @@ int main() {
                             EXPECT((int64_t)plan.part * (plan.parts - 1) < len);
                             EXPECT((int64_t)plan.rows_wg * plan.row_blocks >= T * G);
                             EXPECT((int64_t)plan.rows_wg * (plan.row_blocks - 1) < T * G);
-                            EXPECT(plan.rows_wave == 16 || (plan.rows_wave == 32 && dim < 256));
-                            EXPECT(plan.rows_wg == plan.rows_wave || plan.rows_wg == 2 * plan.rows_wave || plan.rows_wg == 4 * plan.rows_wave);
+                            EXPECT(plan.rows_wg == (T * G <= 16 ? 16 : dim == 256 ? 64 : 128));
                             const int64_t rows = plan.parts > 1 ? seqs * 2 * plan.parts * T * G : 0;
                             EXPECT((int64_t)bytes == rows * (dim * 4 + 8) && plan.o_bytes == rows * dim * 4);
                             EXPECT((char *)attn.ws_ml == A + plan.o_bytes && (char *)attn.ws_o == A);
