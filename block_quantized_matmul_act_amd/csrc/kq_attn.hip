@@ -19,9 +19,15 @@
 // units): until then exp2(S - m) stays within 2^8, far inside every type, and
 // neither a cross-lane maximum nor a rescaling of O is needed.
 //
-// A wave holds the sums of RW query rows (16 or 32).  A sequence's slots are cut
-// into parts so that few long sequences fill the chip; a second kernel joins
-// the parts.
+// A wave holds the sums of RW query rows (16 or 32).
+//
+// How the work is shared: a unit is UNIT slots of one (sequence, key head, block
+// of rows).  The lengths are known to the device alone, so every workgroup of a
+// grid that just fills the chip adds up the units itself and takes an equal run
+// of them, whatever the mix of lengths.  A run covers parts of at most two
+// blocks and any number of whole ones; whole ones are finished where they are,
+// a part leaves its sums (unnormalised, with m and l) in the workspace, and a
+// second kernel joins the parts.
 #include "kq_step_device.hpp"
 
 namespace kq {
@@ -30,6 +36,19 @@ namespace {
 
 constexpr float M_START = -1e30f;  // below every score, and finite: exp2(-inf - m) is 0, not NaN
 constexpr float M_SLACK = 8.f;
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// 4 neighbouring sums: finished ones to the output, a part's to the workspace.
+template <class E>
+__device__ __forceinline__ void put4(const AttnArgs &a, bool whole, v4f x, int64_t out, int64_t slot) {
+    if (!whole)
+        *reinterpret_cast<v4f *>(a.ws_o + slot) = x;
+    else if (a.out_f32)
+        *reinterpret_cast<v4f *>(reinterpret_cast<float *>(a.out) + out) = x;
+    else
+        *reinterpret_cast<v2u *>(a.out + out * 2) = v2u{pack2<E>(x[0], x[1]), pack2<E>(x[2], x[3])};
+}
 
 template <class E, int RW>
 struct Mfma;
@@ -65,6 +84,8 @@ struct Mfma<_Float16, 32> {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
 };
+
+__device__ __forceinline__ uint64_t first_bits(int n) { return n ? (2ull << (n - 1)) - 1ull : 0ull; }  // n <= 64
 
 // Which of 8 keys a row sees (bit e: the e-th), the first being node `node` of
 // the drafted tokens (below 0: that many cached ones come first).  sees: the
@@ -158,6 +179,99 @@ struct Frag<E, true> {
     }
 };
 
+// ---------------------------------------------------------------- sharing
+
+constexpr int UNIT = ATTN_UNIT;
+
+// A sequence as the kernels see it: rows and slots held inside the step and the
+// bounds of the call.
+struct Seq {
+    int first, T, len, total;
+};
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b) {
+    Seq q;
+    batch_rows(a.batch, b, q.first, q.T);
+    q.T = min(q.T, a.max_tokens);
+    q.len = min(max(a.batch.lens[b], 0), a.max_len);
+    q.total = min(q.len + q.T, a.max_len);
+    return q;
+}
+
+// What one wave knows of 64 sequences (lane i: sequence 64 chunk + i): their units
+// for one key head and how many come before.
+struct Share {
+    int chunk, before, incl, all, tiles, blocks;
+};
+__device__ __forceinline__ void share_chunk(const AttnArgs &a, Share &s, int chunk) {
+    const int lane = threadIdx.x & 63, b = chunk * 64 + lane;
+    int tiles = 0, blocks = 0;
+    if (b < a.batch.n_seqs) {
+        const Seq q = seq_of(a, b);
+        tiles = q.T ? (q.total + UNIT - 1) / UNIT : 0;
+        blocks = (q.T * a.group + a.rows_wg - 1) / a.rows_wg;
+    }
+    int incl = tiles * blocks;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+        const int left = __shfl_up(incl, x);
+        incl += lane >= x ? left : 0;
+    }
+    s.chunk = chunk;
+    s.incl = incl;
+    s.tiles = tiles;
+    s.blocks = blocks;
+}
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+// all the units of one key head, and the first chunk
+__device__ __forceinline__ Share share_of(const AttnArgs &a) {
+    Share s;
+    share_chunk(a, s, 0);
+    s.before = 0;
+    s.all = last_lane(s.incl);
+    if (a.batch.n_seqs > 64) {
+        Share t;
+        for (int c = 1; c * 64 < a.batch.n_seqs; ++c) {
+            share_chunk(a, t, c);
+            s.all += last_lane(t.incl);
+        }
+    }
+    return s;
+}
+// The run of workgroup w of `groups` (at least as many units as groups).
+__device__ __forceinline__ int run_begin(int w, int groups, int units) { return (int)((int64_t)w * units / groups); }
+
+// One block's share of a run: keys [from, to) of a row block of a head; `whole`
+// if that is all of its keys, else the workspace slot of its sums.
+struct Piece {
+    int b, h, rb, from, to, units;
+    bool whole;
+};
+// the piece that unit u (of all heads) begins or continues; s moves on with u
+__device__ __forceinline__ Piece piece_at(const AttnArgs &a, Share &s, int u, int end) {
+    const int heads = a.cache.heads;
+    const int x = u / heads;
+    while (x >= s.before + last_lane(s.incl)) {
+        const int before = s.before + last_lane(s.incl);
+        share_chunk(a, s, s.chunk + 1);
+        s.before = before;
+    }
+    const int lane = __ffsll((unsigned long long)__ballot(s.before + s.incl > x)) - 1;
+    const int tiles = __builtin_amdgcn_readlane(s.tiles, lane), blocks = __builtin_amdgcn_readlane(s.blocks, lane);
+    const int mine = tiles * blocks;
+    const int in_seq = u - heads * (s.before + __builtin_amdgcn_readlane(s.incl, lane) - mine);
+    Piece p;
+    p.b = s.chunk * 64 + lane;
+    p.h = in_seq / mine;
+    const int in_head = in_seq - p.h * mine;
+    p.rb = in_head / tiles;
+    const int tile = in_head - p.rb * tiles;
+    p.units = min(tiles - tile, end - u);
+    p.from = tile * UNIT;
+    p.to = (tile + p.units) * UNIT;  // (past the sequence's end in its last unit)
+    p.whole = p.units == tiles;
+    return p;
+}
+
 // Where a sequence's values lie, for what add_odd reads again.
 struct ValueRows {
     const CacheArgs &cache;
@@ -210,7 +324,7 @@ __device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane,
 // Up to 16 rows: one wave's worth, so the 4 waves of a workgroup cut the keys
 // (32 at a time in turn) and their sums are joined in LDS.
 template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void attn_few_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
     constexpr int RW = 16;
     typedef Mfma<E, RW> MM;
     typedef typename MM::op op_t;
@@ -224,224 +338,217 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void attn_few_
     __shared__ float lo[4 * RW * (D + 4)];  // sums of the waves: [wave][row][dim]
     __shared__ float lm[4 * RW], ll[4 * RW];
 
-    // part c of key head h of sequence b
-    const int64_t item = blockIdx.x;
-    const int c = (int)(item % a.parts);
-    const int h = (int)(item / a.parts % a.cache.heads);
-    const int b = (int)(item / a.parts / a.cache.heads);
-    int first, T;
-    batch_rows(a.batch, b, first, T);
-    T = min(T, a.max_tokens);
-    const int G = a.group, R = T * G;
-    const int len = max(a.batch.lens[b], 0);
-    const int total = min(len, INT32_MAX - 64) + T;
-    const int from = c * a.part;
-    if (R == 0 || from >= total) return;
-    const int to = min(from + a.part, total);
+    Share share = share_of(a);
+    const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
+    if ((int)blockIdx.x >= groups) return;
+    const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const bool used = n < R;
-    const int tok = used ? n / G : 0;
-    const int head = h * G + (used ? n % G : 0);
-    const int64_t q_row = (int64_t)(first + tok) * ((int64_t)a.cache.heads * G) + head;
-
-    op_t qf[NK];
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-        v4u w = {0u, 0u, 0u, 0u};
-        if (used) w = *reinterpret_cast<const v4u *>(a.q + (q_row * D + 32 * kk + 8 * g) * 2);
-        qf[kk] = __builtin_bit_cast(op_t, w);
-    }
-    uint64_t sees = 0;
-    if (used) sees = (a.mask ? a.mask[first + tok] : (2ull << tok) - 1ull) & ((2ull << (T - 1)) - 1ull);
-
-    // Key of this lane's row of the first product's two results (of 16 keys each):
-    // see the head of the file.
-    const int krow[2] = {8 * (n >> 2) + (n & 3), 8 * (n >> 2) + 4 + (n & 3)};
-    // Addresses: 16 consecutive slots from a multiple of 16 lie in one page, so a
-    // tile of 32 has two runs whose addresses are the same for the whole wave
-    // (scalar registers); a lane adds its place in its run, which never changes.
-    const int page_shift = a.cache.page_shift;
-    const int page_mask = (1 << page_shift) - 1;
+    const int G = a.group;
+    // Key of this lane's row of the first product's two results (of 16 keys each;
+    // the second: 4 on): see the head of the file.
+    const int krow = 8 * (n >> 2) + (n & 3);
+    const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
     const int64_t head_bytes = (int64_t)D * ES << page_shift;
-    const int heads = a.cache.heads;
-    const int last_run = (total - 1) & ~15;
-    struct Runs {
-        int64_t page[2];  // offset of the head's page
-        int slot[2];      // place in it
-    };
-    auto runs = [&](int key) {
-        Runs r;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int slot = min(key + 16 * i, last_run);  // (a run past the end: the last one again, masked)
-            r.page[i] = ((int64_t)slot_page(a.cache, a.batch, b, slot) * heads + h) * head_bytes;
-            r.slot[i] = slot & page_mask;
-        }
-        return r;
-    };
-    // (both of a lane's keys lie in the same run)
-    auto load_k = [&](const Runs &ru, raw_t(&kf)[2][NK]) {
-        const int64_t at = n >> 3 ? ru.page[1] + ru.slot[1] * (D * ES) : ru.page[0] + ru.slot[0] * (D * ES);
-        const char *p = a.cache.k + at + ((krow[0] & 15) * (D * ES) + 8 * g * ES);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) kf[t][kk] = *reinterpret_cast<const raw_t *>(p + (4 * t * D + 32 * kk) * ES);
-    };
-    auto load_v = [&](const Runs &ru, raw_t(&vf)[ND]) {
-        const int64_t at = g >> 1 ? ru.page[1] + ru.slot[1] * ES : ru.page[0] + ru.slot[0] * ES;
-        const char *p = a.cache.v + at + ((n << page_shift) + 8 * (g & 1)) * ES;
-        const int step = (RW * ES) << page_shift;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) vf[d] = *reinterpret_cast<const raw_t *>(p + d * step);
-    };
 
-    acc_t o[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d) o[d] = acc_t{};
-    float m = M_START, l = 0.f;
+    for (int u = begin; u < end;) {
+        const Piece pc = piece_at(a, share, u, end);
+        const int h = pc.h;
+        const Seq sq = seq_of(a, pc.b);
+        const int len = sq.len, total = sq.total, R = sq.T * G, to = min(pc.to, total);
+        const bool used = n < R;
+        const int tok = used ? n / G : 0;
+        const int64_t q_row = (int64_t)(sq.first + tok) * ((int64_t)heads * G) + h * G + (used ? n % G : 0);
 
-    int key0 = from + 32 * wave;
-    Runs ru = runs(key0);
-    // Keys are loaded a turn ahead, values at the turn's begin, where the
-    // registers hold both (512 bytes of a lane at dim 256 they do not: there
-    // each is loaded when the other is done with).
-    constexpr bool AHEAD = D * ES <= 256;
-    raw_t kf[2][NK];
-    if (AHEAD && key0 < to) load_k(ru, kf);
-    for (; key0 < to; key0 += 128) {
-        raw_t vf[ND];
-        const int next = key0 + 128;
-        if constexpr (AHEAD) {
-            load_v(ru, vf);
-            ru = runs(next);
-        } else {
-            load_k(ru, kf);
+        op_t qf[NK];
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            v4u w = {0u, 0u, 0u, 0u};
+            if (used) w = (*reinterpret_cast<const v4u *>(a.q + (q_row * D + 32 * kk + 8 * g) * 2) & a.q_keep) ^ a.q_flip;
+            qf[kk] = __builtin_bit_cast(op_t, w);
         }
+        uint64_t sees = 0;
+        if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(total - len);
 
-        acc_t sc[2];
+        // Addresses: 16 consecutive slots from a multiple of 16 lie in one page, so a
+        // tile of 32 has two runs whose addresses are the same for the whole wave
+        // (scalar registers); a lane adds its place in its run, which never changes.
+        const int last_run = (total - 1) & ~15;
+        struct Runs {
+            int64_t page[2];  // offset of the head's page
+            int slot[2];      // place in it
+        };
+        auto runs = [&](int key) {
+            Runs r;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            sc[t] = acc_t{};
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(kf[t][kk]), qf[kk], sc[t]);
-        }
-        if constexpr (AHEAD) {
-            if (next < to) load_k(ru, kf);
-        } else {
-            load_v(ru, vf);
-            ru = runs(next);
-        }
-
-        // p[e]: key key0 + 8 g + e of this lane's row
-        float p[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) p[r] = sc[r >> 2][r & 3] * a.score_scale;
-        const bool ragged = key0 + 32 > len;
-        if (ragged) {
-            const uint32_t on = seen8(sees, key0 + 8 * g - len);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) p[r] = on >> r & 1u ? p[r] : -__builtin_inff();
-        }
-        float top = p[0];
-#pragma unroll
-        for (int r = 1; r < 8; ++r) top = fmaxf(top, p[r]);
-        if (__any(top > m + M_SLACK)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float up = fmaxf(m, top);
-            const float f = __builtin_amdgcn_exp2f(m - up);
-            m = up;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] *= f;
-        }
-        v4u w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float p0 = __builtin_amdgcn_exp2f(p[2 * j] - m), p1 = __builtin_amdgcn_exp2f(p[2 * j + 1] - m);
-            l += p0 + p1;
-            w[j] = pack2<E>(p0, p1);
-        }
-        const op_t pf = __builtin_bit_cast(op_t, w);
-        bool odd = false;
-        if (ragged) {
-            // slots past the end hold anything: zeros
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                FR::first(vf[d], min(max(total - (key0 + 8 * g), 0), 8));
-                odd |= FR::drop_odd(vf[d]);
+            for (int i = 0; i < 2; ++i) {
+                const int slot = min(key + 16 * i, last_run);  // (a run past the end: the last one again, masked)
+                r.page[i] = ((int64_t)slot_page(a.cache, a.batch, pc.b, slot) * heads + h) * head_bytes;
+                r.slot[i] = slot & page_mask;
             }
-        }
+            return r;
+        };
+        // (both of a lane's keys lie in the same run)
+        auto load_k = [&](const Runs &ru, raw_t(&kf)[2][NK]) {
+            const int64_t at = n >> 3 ? ru.page[1] + ru.slot[1] * (D * ES) : ru.page[0] + ru.slot[0] * (D * ES);
+            const char *p = a.cache.k + at + ((krow & 15) * (D * ES) + 8 * g * ES);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[d]), pf, o[d]);
-        if (__any(odd)) add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, len, total}, key0, lane, sees, o);
-    }
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) kf[t][kk] = *reinterpret_cast<const raw_t *>(p + (4 * t * D + 32 * kk) * ES);
+        };
+        auto load_v = [&](const Runs &ru, raw_t(&vf)[ND]) {
+            const int64_t at = g >> 1 ? ru.page[1] + ru.slot[1] * ES : ru.page[0] + ru.slot[0] * ES;
+            const char *p = a.cache.v + at + ((n << page_shift) + 8 * (g & 1)) * ES;
+            const int step = (RW * ES) << page_shift;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) vf[d] = *reinterpret_cast<const raw_t *>(p + d * step);
+        };
 
-    // Join the waves.
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+        acc_t o[ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f *>(lo + (wave * RW + n) * (D + 4) + d * RW + 4 * g) = o[d];
-    if (g == 0) {
-        lm[wave * RW + n] = m;
-        ll[wave * RW + n] = l;
-    }
-    __syncthreads();
-    const int out_row = threadIdx.x >> 4, jt = threadIdx.x & 15;  // 16 threads to a row
-    if (out_row >= R) return;
-    float mm = M_START;
+        for (int d = 0; d < ND; ++d) o[d] = acc_t{};
+        float m = M_START, l = 0.f;
+
+        int key0 = pc.from + 32 * wave;
+        Runs ru = runs(key0);
+        // Keys are loaded a turn ahead, values at the turn's begin, where the
+        // registers hold both (512 bytes of a lane at dim 256 they do not: there
+        // each is loaded when the other is done with).
+        constexpr bool AHEAD = D * ES <= 256;
+        raw_t kf[2][NK];
+        if (AHEAD && key0 < to) load_k(ru, kf);
+        for (; key0 < to; key0 += 128) {
+            raw_t vf[ND];
+            const int next = key0 + 128;
+            if constexpr (AHEAD) {
+                load_v(ru, vf);
+                ru = runs(next);
+            } else {
+                load_k(ru, kf);
+            }
+
+            acc_t sc[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mm = fmaxf(mm, lm[out_row + k * RW]);
-    float f[4], sum = 0.f;
+            for (int t = 0; t < 2; ++t) {
+                sc[t] = acc_t{};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        f[k] = __builtin_amdgcn_exp2f(lm[out_row + k * RW] - mm);
-        sum += f[k] * ll[out_row + k * RW];
-    }
-    const int64_t part_row = (((int64_t)b * heads + h) * a.parts + c) * ((int64_t)a.max_tokens * G) + out_row;
-    const bool whole = a.parts == 1;
-    const float norm = whole ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
-    const int64_t o_row = ((int64_t)(first + out_row / G) * ((int64_t)heads * G) + h * G + out_row % G) * D;
+                for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(kf[t][kk]), qf[kk], sc[t]);
+            }
+            if constexpr (AHEAD) {
+                if (next < to) load_k(ru, kf);
+            } else {
+                load_v(ru, vf);
+                ru = runs(next);
+            }
+
+            // p[e]: key key0 + 8 g + e of this lane's row
+            float p[8];
 #pragma unroll
-    for (int v = 0; v < D; v += 64) {
-        const int dim = v + jt * 4;
-        v4f acc = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < 8; ++r) p[r] = sc[r >> 2][r & 3];
+            const bool ragged = key0 + 32 > len;
+            if (ragged) {
+                const uint32_t on = seen8(sees, key0 + 8 * g - len);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc += f[k] * *reinterpret_cast<const v4f *>(lo + (out_row + k * RW) * (D + 4) + dim);
-        acc *= norm;
-        if (!whole)
-            *reinterpret_cast<v4f *>(a.ws_o + part_row * D + dim) = acc;
-        else if (a.out_f32)
-            *reinterpret_cast<v4f *>(reinterpret_cast<float *>(a.out) + o_row + dim) = acc;
-        else
-            *reinterpret_cast<v2u *>(a.out + (o_row + dim) * 2) = v2u{pack2<E>(acc[0], acc[1]), pack2<E>(acc[2], acc[3])};
-    }
-    if (!whole && jt == 0) {
-        a.ws_ml[2 * part_row] = mm;
-        a.ws_ml[2 * part_row + 1] = sum;
+                for (int r = 0; r < 8; ++r) p[r] = on >> r & 1u ? p[r] : -__builtin_inff();
+            }
+            float top = p[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r) top = fmaxf(top, p[r]);
+            top *= a.score_scale;
+            if (__any(top > m + M_SLACK)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float up = fmaxf(m, top);
+                const float f = __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] *= f;
+            }
+            v4u w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(p[2 * j], a.score_scale, -m));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(p[2 * j + 1], a.score_scale, -m));
+                l += p0 + p1;
+                w[j] = pack2<E>(p0, p1);
+            }
+            const op_t pf = __builtin_bit_cast(op_t, w);
+            bool odd = false;
+            if (ragged) {
+                // slots past the end hold anything: zeros
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    FR::first(vf[d], min(max(total - (key0 + 8 * g), 0), 8));
+                    odd |= FR::drop_odd(vf[d]);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[d]), pf, o[d]);
+            if (__any(odd))
+                add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, pc.b, h, len, total}, key0, lane, sees, o);
+        }
+
+        // Join the waves.
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (u != begin) __syncthreads();  // the piece before has been read
+#pragma unroll
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f *>(lo + (wave * RW + n) * (D + 4) + d * RW + 4 * g) = o[d];
+        if (g == 0) {
+            lm[wave * RW + n] = m;
+            ll[wave * RW + n] = l;
+        }
+        __syncthreads();
+        const int out_row = threadIdx.x >> 4, jt = threadIdx.x & 15;  // 16 threads to a row
+        if (out_row < R) {
+            float mm = M_START;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mm = fmaxf(mm, lm[out_row + k * RW]);
+            float f[4], sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f[k] = __builtin_amdgcn_exp2f(lm[out_row + k * RW] - mm);
+                sum += f[k] * ll[out_row + k * RW];
+            }
+            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + out_row;
+            const float norm = pc.whole ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
+            const int64_t o_row = ((int64_t)(sq.first + out_row / G) * ((int64_t)heads * G) + h * G + out_row % G) * D;
+#pragma unroll
+            for (int v = 0; v < D; v += 64) {
+                const int dim = v + jt * 4;
+                v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc += f[k] * *reinterpret_cast<const v4f *>(lo + (out_row + k * RW) * (D + 4) + dim);
+                put4<E>(a, pc.whole, acc * norm, o_row + dim, slot_row * D + dim);
+            }
+            if (!pc.whole && jt == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{mm, sum};
+        }
+        u += pc.units;
     }
 }
 
-// The same sums for sequences that bring more than a wave's rows: 4 waves of 32
-// rows share tiles of KEYS keys staged in LDS (two tiles: one in use, one being
-// written; the registers hold the one after).  Read from memory a line at a
-// time, a tile is read once for 128 rows instead of once for each wave.
+// The same sums for sequences that bring more rows: WAVES waves of RW rows share
+// tiles of KEYS keys staged in LDS (two tiles: one in use, one being written; the
+// registers hold the one after).  Memory is read a line at a time, and once for
+// all the rows of the workgroup.
 // LDS holds 16-byte pieces; a row's pieces are permuted by an XOR with bits of
 // the row, so that the lanes of a read, which want one piece of many rows, meet
 // different banks.
-template <class E, bool F8, int D>
+template <class E, bool F8, int D, int WAVES>
 struct Tile {
     static constexpr int ES = F8 ? 1 : 2;
     static constexpr int KEYS = D == 256 ? 32 : 64;
-    static constexpr int KB = D * ES, VB = KEYS * ES;          // bytes of a key row and of a feature row
-    static constexpr int KP = KB / 16, VP = VB / 16;           // their 16-byte pieces
-    static constexpr int KROWS = KEYS / 4, VROWS = D / 4;      // rows that one wave stages
-    static constexpr int KN = KROWS * KB / 1024, VN = VROWS * VB / 1024;  // loads of a lane
-    static constexpr int K_BYTES = KEYS * KB, BYTES = K_BYTES + D * VB;
+    static constexpr int KB = D * ES, VB = KEYS * ES;  // bytes of a key row and of a feature row
+    static constexpr int KP = KB / 16, VP = VB / 16;   // their 16-byte pieces
+    static constexpr int THREADS = WAVES * 64;
+    static constexpr int PIECES = KEYS * KP;           // of the keys, and as many of the values
+    static constexpr int N = (PIECES + THREADS - 1) / THREADS;  // loads of a thread for each
+    static constexpr int K_BYTES = KEYS * KB, BYTES = 2 * K_BYTES;
 
     static __device__ __forceinline__ int k_pos(int key, int piece) {
         const int f = KP >= 8 ? (key & 3) | ((key >> 1) & 4) : (key >> 1) & (KP - 1);
@@ -453,15 +560,15 @@ struct Tile {
     }
 };
 
-template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
+template <class E, bool F8, int D, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs a) {
     constexpr int RW = D == 256 ? 16 : 32;
     typedef Mfma<E, RW> MM;
     typedef typename MM::op op_t;
     typedef typename MM::acc acc_t;
     typedef Frag<E, F8> FR;
     typedef typename FR::raw raw_t;
-    typedef Tile<E, F8, D> TL;
+    typedef Tile<E, F8, D, WAVES> TL;
     constexpr int ES = TL::ES, KEYS = TL::KEYS;
     constexpr int NG = 64 / RW;                    // lane groups: 8 of a step's keys, 8 of a step's features to each
     constexpr int NK = D / (8 * NG), ND = D / RW;  // steps of the first product, results of the second
@@ -471,106 +578,25 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
     __shared__ __align__(16) char tile[2 * TL::BYTES];
     __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
 
-    const int id = blockIdx.x;
-    const int rb = (id >> 3) % a.row_blocks;
-    const int64_t item = (int64_t)((id >> 3) / a.row_blocks) * 8 + (id & 7);
-    const int c = (int)(item % a.parts);
-    const int h = (int)(item / a.parts % a.cache.heads);
-    const int64_t b64 = item / a.parts / a.cache.heads;
-    if (b64 >= a.batch.n_seqs) return;
-    const int b = (int)b64;
-    int first, T;
-    batch_rows(a.batch, b, first, T);
-    T = min(T, a.max_tokens);
-    const int G = a.group, R = T * G;
-    const int len = max(a.batch.lens[b], 0);
-    const int total = min(len, INT32_MAX - 64) + T;
-    const int from = c * a.part;
-    if (rb * a.rows_wg >= R || from >= total) return;
-    const int to = min(from + a.part, total);
+    Share share = share_of(a);
+    const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
+    if ((int)blockIdx.x >= groups) return;
+    const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & (RW - 1), g = lane / RW;
-    const int row = rb * a.rows_wg + wave * RW + n;
-    const bool used = row < R;
-    const int tok = used ? row / G : 0;
-    const int head = h * G + (used ? row % G : 0);
-    const int heads = a.cache.heads;
-    const int64_t q_row = (int64_t)(first + tok) * ((int64_t)heads * G) + head;
-
-    op_t qf[NK];
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-        v4u w = {0u, 0u, 0u, 0u};
-        if (used) w = *reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (NG * kk + g)) * 2);
-        qf[kk] = __builtin_bit_cast(op_t, w);
-    }
-    uint64_t sees = 0;
-    if (used) sees = (a.mask ? a.mask[first + tok] : (2ull << tok) - 1ull) & ((2ull << (T - 1)) - 1ull);
-
-    // staging: this lane's rows and pieces
+    const int G = a.group;
     const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
     const int64_t head_bytes = (int64_t)D * ES << page_shift;
-    const int last_run = (total - 1) & ~15;
-    const int k_row = wave * TL::KROWS + lane / TL::KP, k_piece = lane % TL::KP;  // + i * 64 / KP
-    const int v_row = wave * TL::VROWS + lane / TL::VP, v_piece = lane % TL::VP;
+    // staging: piece threadIdx.x (+ i * THREADS) of the keys and of the values
+    const int k_row = threadIdx.x / TL::KP, k_piece = threadIdx.x % TL::KP;
+    const int v_row = threadIdx.x / TL::VP, v_piece = threadIdx.x % TL::VP;
     const int v_run = v_piece * (16 / ES) >> 4;
     const int v_off = (v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1));
-    v4u stage[TL::KN + TL::VN];
-    auto head_page = [&](int slot) { return ((int64_t)slot_page(a.cache, a.batch, b, slot) * heads + h) * head_bytes; };
-    auto load = [&](int key0) {
-        const int k_slot = min(key0 + (wave * TL::KROWS & ~15), last_run);  // one run to a wave
-        const char *kp = a.cache.k + head_page(k_slot) + (k_slot & page_mask) * TL::KB;
-        const int k_off = (k_row & 15) * TL::KB + k_piece * 16;
-#pragma unroll
-        for (int i = 0; i < TL::KN; ++i) stage[i] = *reinterpret_cast<const v4u *>(kp + k_off + i * 1024);
-        const char *vp = a.cache.v;
-        int64_t at = 0;
-#pragma unroll
-        for (int r = 0; r < KEYS / 16; ++r) {
-            const int slot = min(key0 + 16 * r, last_run);
-            const int64_t o = head_page(slot) + (slot & page_mask) * ES;
-            at = r == v_run ? o : at;
-        }
-        vp += at + v_off;
-#pragma unroll
-        for (int i = 0; i < TL::VN; ++i)
-            stage[TL::KN + i] = *reinterpret_cast<const v4u *>(vp + ((int64_t)(i * (64 / TL::VP)) << page_shift) * ES);
-    };
-    auto store = [&](char *to_lds, int key0) {
-        if (key0 + KEYS > len) {
-            // slots past the end hold anything: zeros; infinite and NaN values of
-            // drafted tokens: zeros here, and noted
-            const int left = total - (key0 + v_piece * (16 / ES));
-            bool found = false;
-#pragma unroll
-            for (int i = 0; i < TL::VN; ++i) {
-                v4u &r = stage[TL::KN + i];
-                if constexpr (F8) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        raw_t half = {r[2 * j], r[2 * j + 1]};
-                        FR::first(half, min(max(left - 8 * j, 0), 8));
-                        found |= FR::drop_odd(half);
-                        r[2 * j] = half[0];
-                        r[2 * j + 1] = half[1];
-                    }
-                } else {
-                    FR::first(r, min(max(left, 0), 8));
-                    found |= FR::drop_odd(r);
-                }
-            }
-            if (found) odd = 1;
-        }
-#pragma unroll
-        for (int i = 0; i < TL::KN; ++i)
-            *reinterpret_cast<v4u *>(to_lds + TL::k_pos(k_row + i * (64 / TL::KP), k_piece)) = stage[i];
-#pragma unroll
-        for (int i = 0; i < TL::VN; ++i)
-            *reinterpret_cast<v4u *>(to_lds + TL::v_pos(v_row + i * (64 / TL::VP), v_piece)) = stage[TL::KN + i];
-    };
-    // where this lane reads: 8 values of a key (or feature) from an even or odd half piece
+    const bool stages = TL::PIECES >= TL::THREADS || (int)threadIdx.x < TL::PIECES;
+    // where this lane reads: its row of the first product's results (see the head
+    // of the file) and of the second's, 8 values from an even or odd half piece
     const int krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
     auto k_frag = [&](const char *at, int t, int kk) {
         const int key = RW == 16 ? krow + 32 * (t >> 1) + 4 * (t & 1) : krow + 32 * t;
@@ -581,184 +607,253 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
         const int half = NG * s + g;
         return *reinterpret_cast<const raw_t *>(at + TL::v_pos(RW * d + n, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
     };
-
-    acc_t o[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d) o[d] = acc_t{};
-    float m = M_START, l = 0.f;
-
-    load(from);
     if (threadIdx.x == 0) odd = 0;
-    __syncthreads();
-    store(tile, from);
-    load(from + KEYS);  // (past the end: the last run again)
-    int odd_tile = 0;
-    for (int key0 = from; key0 < to; key0 += KEYS) {
-        __syncthreads();
-        const char *at = tile + odd_tile * TL::BYTES;
-        acc_t sc[NT];
+
+    for (int u = begin; u < end;) {
+        const Piece pc = piece_at(a, share, u, end);
+        const int h = pc.h;
+        const Seq sq = seq_of(a, pc.b);
+        const int len = sq.len, total = sq.total, R = sq.T * G, to = min(pc.to, total);
+        const int row = pc.rb * a.rows_wg + wave * RW + n;
+        const bool used = row < R;
+        const int tok = used ? row / G : 0;
+        const int64_t q_row = (int64_t)(sq.first + tok) * ((int64_t)heads * G) + h * G + (used ? row % G : 0);
+
+        op_t qf[NK];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            sc[t] = acc_t{};
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(k_frag(at, t, kk)), qf[kk], sc[t]);
+        for (int kk = 0; kk < NK; ++kk) {
+            v4u w = {0u, 0u, 0u, 0u};
+            if (used)
+                w = (*reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (NG * kk + g)) * 2) & a.q_keep) ^ a.q_flip;
+            qf[kk] = __builtin_bit_cast(op_t, w);
         }
-        // p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's row
-        float p[NT * NR];
+        uint64_t sees = 0;
+        if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(total - len);
+
+        const int last_run = (total - 1) & ~15;
+        v4u stage[2 * TL::N];
+        auto run_at = [&](int slot) { return ((int64_t)slot_page(a.cache, a.batch, pc.b, slot) * heads + h) * head_bytes; };
+        auto load = [&](int key0) {
+            if (!stages) return;
 #pragma unroll
-        for (int r = 0; r < NT * NR; ++r) p[r] = sc[r / NR][r % NR] * a.score_scale;
-        const bool ragged = key0 + KEYS > len;
-        if (ragged) {
+            for (int i = 0; i < TL::N; ++i) {  // a wave's pieces lie in one run of 16 slots (from a multiple of 16)
+                const int run = __builtin_amdgcn_readfirstlane((k_row + i * (TL::THREADS / TL::KP)) & ~15);
+                const int slot = min(key0 + run, last_run);  // (a run past the end: the last one again, masked)
+                const char *p = a.cache.k + run_at(slot) + (slot & page_mask) * TL::KB;
+                stage[i] = *reinterpret_cast<const v4u *>(p + ((k_row + i * (TL::THREADS / TL::KP)) & 15) * TL::KB + k_piece * 16);
+            }
+            int64_t at = 0;
+#pragma unroll
+            for (int r = 0; r < KEYS / 16; ++r) {
+                const int slot = min(key0 + 16 * r, last_run);
+                const int64_t o = run_at(slot) + (slot & page_mask) * ES;
+                at = r == v_run ? o : at;
+            }
+            const char *p = a.cache.v + at + v_off;
+#pragma unroll
+            for (int i = 0; i < TL::N; ++i)
+                stage[TL::N + i] = *reinterpret_cast<const v4u *>(p + (i * (TL::THREADS / TL::VP) << page_shift) * ES);
+        };
+        auto store = [&](char *to_lds, int key0) {
+            if (!stages) return;
+            if (key0 + KEYS > len) {
+                // slots past the end hold anything: zeros; infinite and NaN values of
+                // drafted tokens: zeros here, and noted
+                const int left = total - (key0 + v_piece * (16 / ES));
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < TL::N; ++i) {
+                    v4u &r = stage[TL::N + i];
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            raw_t half = {r[2 * j], r[2 * j + 1]};
+                            FR::first(half, min(max(left - 8 * j, 0), 8));
+                            found |= FR::drop_odd(half);
+                            r[2 * j] = half[0];
+                            r[2 * j + 1] = half[1];
+                        }
+                    } else {
+                        FR::first(r, min(max(left, 0), 8));
+                        found |= FR::drop_odd(r);
+                    }
+                }
+                if (found) odd = 1;
+            }
+#pragma unroll
+            for (int i = 0; i < TL::N; ++i) {
+                *reinterpret_cast<v4u *>(to_lds + TL::k_pos(k_row + i * (TL::THREADS / TL::KP), k_piece)) = stage[i];
+                *reinterpret_cast<v4u *>(to_lds + TL::v_pos(v_row + i * (TL::THREADS / TL::VP), v_piece)) = stage[TL::N + i];
+            }
+        };
+
+        acc_t o[ND];
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] = acc_t{};
+        float m = M_START, l = 0.f;
+
+        load(pc.from);
+        __syncthreads();  // the piece before has been read
+        store(tile, pc.from);
+        load(pc.from + KEYS);
+        int second = 0;
+        for (int key0 = pc.from; key0 < to; key0 += KEYS) {
+            __syncthreads();
+            const char *at = tile + second * TL::BYTES;
+            acc_t sc[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                sc[t] = acc_t{};
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(k_frag(at, t, kk)), qf[kk], sc[t]);
+            }
+            // p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's row
+            float p[NT * NR];
+#pragma unroll
+            for (int r = 0; r < NT * NR; ++r) p[r] = sc[r / NR][r % NR];
+            const bool ragged = key0 + KEYS > len;
+            if (ragged) {
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    const uint32_t on = seen8(sees, key0 + 8 * NG * s + 8 * g - len);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
+                }
+            }
+            float top = p[0];
+#pragma unroll
+            for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
+            top *= a.score_scale;
+            if (__any(top > m + M_SLACK)) {
+#pragma unroll
+                for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+                const float up = fmaxf(m, top);
+                const float f = __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] *= f;
+            }
+            op_t pf[NS];
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                const uint32_t on = seen8(sees, key0 + 8 * NG * s + 8 * g - len);
+                v4u w;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
+                for (int j = 0; j < 4; ++j) {
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], a.score_scale, -m));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], a.score_scale, -m));
+                    l += p0 + p1;
+                    w[j] = pack2<E>(p0, p1);
+                }
+                pf[s] = __builtin_bit_cast(op_t, w);
             }
-        }
-        float top = p[0];
 #pragma unroll
-        for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
-        if (__any(top > m + M_SLACK)) {
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-            const float up = fmaxf(m, top);
-            const float f = __builtin_amdgcn_exp2f(m - up);
-            m = up;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] *= f;
-        }
-        op_t pf[NS];
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            v4u w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p0 = __builtin_amdgcn_exp2f(p[8 * s + 2 * j] - m);
-                const float p1 = __builtin_amdgcn_exp2f(p[8 * s + 2 * j + 1] - m);
-                l += p0 + p1;
-                w[j] = pack2<E>(p0, p1);
-            }
-            pf[s] = __builtin_bit_cast(op_t, w);
-        }
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(v_frag(at, d, s)), pf[s], o[d]);
-        if (ragged && odd) {
-            const ValueRows va = {a.cache, a.batch, b, h, len, total};
+                for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(v_frag(at, d, s)), pf[s], o[d]);
+            if (ragged && odd) {
 #pragma nounroll
-            for (int s = 0; s < NS; ++s) add_odd<E, F8, D, RW>(va, key0 + 8 * NG * s, lane, sees, o);
+                for (int s = 0; s < NS; ++s)
+                    add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, pc.b, h, len, total}, key0 + 8 * NG * s, lane, sees, o);
+            }
+            second ^= 1;
+            if (key0 + KEYS < to) {
+                store(tile + second * TL::BYTES, key0 + KEYS);
+                load(key0 + 2 * KEYS);
+            }
         }
-        odd_tile ^= 1;
-        if (key0 + KEYS < to) {
-            store(tile + odd_tile * TL::BYTES, key0 + KEYS);
-            load(key0 + 2 * KEYS);
-        }
-    }
 
 #pragma unroll
-    for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
-    if (!used) return;
-    const bool whole = a.parts == 1;
-    const float norm = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
-    const int64_t part_row = (((int64_t)b * heads + h) * a.parts + c) * ((int64_t)a.max_tokens * G) + row;
+        for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
+        if (used) {
+            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + wave * RW + n;
+            const float norm = pc.whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+            for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int r = 0; r < NR; r += 4) {
-            const int dim = RW * d + 2 * r + 4 * g;
-            const v4f acc = v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * norm;
-            if (!whole)
-                *reinterpret_cast<v4f *>(a.ws_o + part_row * D + dim) = acc;
-            else if (a.out_f32)
-                *reinterpret_cast<v4f *>(reinterpret_cast<float *>(a.out) + q_row * D + dim) = acc;
-            else
-                *reinterpret_cast<v2u *>(a.out + (q_row * D + dim) * 2) = v2u{pack2<E>(acc[0], acc[1]), pack2<E>(acc[2], acc[3])};
+                for (int r = 0; r < NR; r += 4) {
+                    const int dim = RW * d + 2 * r + 4 * g;
+                    put4<E>(a, pc.whole, v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * norm, q_row * D + dim,
+                            slot_row * D + dim);
+                }
+            if (!pc.whole && g == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{m, l};
         }
-    if (!whole && g == 0) {
-        a.ws_ml[2 * part_row] = m;
-        a.ws_ml[2 * part_row + 1] = l;
+        u += pc.units;
     }
 }
 
-// out = sum over the parts, each weighted by exp2(its maximum - the largest).
-// One workgroup to a (token, head): the waves cut the parts, lanes the dim.
+// out = sum over the parts of a cut block, each weighted by exp2(its maximum -
+// the largest).  One workgroup to a (token, head); D / 4 threads read a part's
+// sums, 256 / (D / 4) parts at a time.
 template <class E, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-    constexpr int VPL = D / 64;
-    __shared__ float so[4][D];
-    __shared__ float sm[4], sl[4];
+    constexpr int TPP = D / 4, AT_ONCE = 256 / TPP;
+    __shared__ v4f so[256];
+    __shared__ v2f sml[AT_ONCE];
     const int heads = a.cache.heads, G = a.group;
-    const int tok = blockIdx.x, head = blockIdx.y;
+    const int tok = blockIdx.x, head = blockIdx.y, h = head / G;
     const int b = batch_seq(a.batch, tok);
-    int first, T;
-    batch_rows(a.batch, b, first, T);
-    T = min(T, a.max_tokens);
-    const int i = tok - first;
-    if (i < 0 || i >= T) return;
-    const int total = min(max(a.batch.lens[b], 0), INT32_MAX - 64) + T;
-    const int parts = min((int)(((int64_t)total + a.part - 1) / a.part), a.parts);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t stride = (int64_t)a.max_tokens * G;
-    const int64_t row0 = (((int64_t)b * heads + head / G) * a.parts) * stride + (int64_t)i * G + head % G;
-    float m = M_START, l = 0.f, o[VPL];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) o[v] = 0.f;
-    for (int c = wave; c < parts; c += 4) {
-        const int64_t r = row0 + c * stride;
-        const float pm = a.ws_ml[2 * r], pl = a.ws_ml[2 * r + 1];
-        float po[VPL];
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) po[v] = a.ws_o[r * D + lane * VPL + v];
-        const float up = fmaxf(m, pm);
-        const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(pm - up);
+    const Seq sq = seq_of(a, b);
+    const int i = tok - sq.first;
+    Share s = share_of(a);
+    for (int c = 0; c < b >> 6; ++c) {
+        const int before = s.before + last_lane(s.incl);
+        share_chunk(a, s, c + 1);
+        s.before = before;
+    }
+    if (i < 0 || i >= sq.T) return;
+    const int units = s.all * heads, groups = min(a.grid, units);
+    const int tiles = __builtin_amdgcn_readlane(s.tiles, b & 63), blocks = __builtin_amdgcn_readlane(s.blocks, b & 63);
+    const int mine = tiles * blocks;
+    const int row = i * G + head % G, rb = row / a.rows_wg;
+    const int from = heads * (s.before + __builtin_amdgcn_readlane(s.incl, b & 63) - mine) + h * mine + rb * tiles;
+    // the workgroups that hold the first and the last unit
+    const int w0 = (int)(((int64_t)(from + 1) * groups - 1) / units);
+    const int w1 = (int)(((int64_t)(from + tiles) * groups - 1) / units);
+    if (w0 == w1) return;  // one workgroup had them all: finished there
+    const int lane = threadIdx.x % TPP, which = threadIdx.x / TPP;
+    float m = M_START, l = 0.f;
+    v4f o = {0.f, 0.f, 0.f, 0.f};
+    for (int w = w0 + which; w <= w1; w += AT_ONCE) {
+        // a workgroup's first piece lies in its first slot
+        const int second = run_begin(w, groups, units) < from;
+        const int64_t r = (2 * (int64_t)w + second) * a.slot_rows + (row - rb * a.rows_wg);
+        const v2f ml = *reinterpret_cast<const v2f *>(a.ws_ml + 2 * r);
+        const v4f po = *reinterpret_cast<const v4f *>(a.ws_o + r * D + 4 * lane);
+        const float up = fmaxf(m, ml[0]);
+        const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
         m = up;
-        l = l * f + pl * pf;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) o[v] = o[v] * f + po[v] * pf;
+        l = l * f + ml[1] * pf;
+        o = o * f + po * pf;
     }
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) so[wave][lane * VPL + v] = o[v];
-    if (lane == 0) {
-        sm[wave] = m;
-        sl[wave] = l;
-    }
+    so[threadIdx.x] = o;
+    if (lane == 0) sml[which] = v2f{m, l};
     __syncthreads();
-    if (wave) return;
-    float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float sum = 0.f, acc[VPL];
+    if (which) return;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sm[w] - mm);
-        sum += f * sl[w];
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) acc[v] += f * so[w][lane * VPL + v];
+    for (int k = 1; k < AT_ONCE; ++k) {
+        const v2f ml = sml[k];
+        const float up = fmaxf(m, ml[0]);
+        const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
+        m = up;
+        l = l * f + ml[1] * pf;
+        o = o * f + so[k * TPP + lane] * pf;
     }
-    const float norm = sum == 0.f ? 0.f : a.v_scale / sum;
-    const int64_t at = ((int64_t)tok * ((int64_t)heads * G) + head) * D + lane * VPL;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        if (a.out_f32)
-            reinterpret_cast<float *>(a.out)[at + v] = acc[v] * norm;
-        else
-            reinterpret_cast<E *>(a.out)[at + v] = (E)(acc[v] * norm);
-    }
+    const float norm = l == 0.f ? 0.f : a.v_scale / l;
+    put4<E>(a, true, o * norm, ((int64_t)tok * ((int64_t)heads * G) + head) * D + 4 * lane, 0);
 }
 
 template <class E, bool F8, int D>
 hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-    const int64_t items = (int64_t)a.batch.n_seqs * a.cache.heads * a.parts;
-    if (p.rows_wg == 16)
-        hipLaunchKernelGGL((attn_few_kernel<E, F8, D>), dim3((unsigned)items), dim3(256), 0, stream, a);
+    const dim3 grid((unsigned)p.grid);
+    if (p.waves == 0)
+        hipLaunchKernelGGL((attn_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, a);
+    else if (p.waves == 4)
+        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D, 4>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D>), dim3((unsigned)((items + 7) / 8 * 8 * a.row_blocks)), dim3(256),
-                           0, stream, a);
+        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D, 8>), grid, dim3(512), 0, stream, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.parts == 1) return e;
+    if (e != hipSuccess || p.bytes == 0) return e;  // no workspace: nothing is cut
     hipLaunchKernelGGL((attn_join_kernel<E, D>), dim3((unsigned)a.batch.n_tokens, (unsigned)(a.cache.heads * a.group)),
                        dim3(256), 0, stream, a);
     return hipGetLastError();

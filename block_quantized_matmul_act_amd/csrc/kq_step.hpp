@@ -37,12 +37,14 @@ struct RopeArgs {
 // type / q_type: KQ_T_*; dim: 64, 128 or 256 (checked by the caller)
 hipError_t launch_rope_append(const RopeArgs &a, int type, int dim, int q_type, hipStream_t stream);
 
-// How attention over the cache is cut: rows_wg query rows to a workgroup (16: the
-// kernel for few rows), each sequence's slots in parts of `part`.
+// How attention over the cache is shared out: `waves` waves (0: the kernel for
+// up to 16 rows) hold rows_wg query rows, `grid` workgroups take equal runs of
+// units of ATTN_UNIT slots and leave at most two cut blocks each (slot_rows rows
+// of the workspace to a block).
+constexpr int ATTN_UNIT = 128;
 struct AttnPlan {
-    int rows_wg, row_blocks;
-    int part, parts;
-    int64_t o_bytes, bytes;  // workspace: sums of the parts, then their maxima and weights
+    int waves, rows_wg, row_blocks, slot_rows, grid;
+    int64_t o_bytes, bytes;  // workspace: sums, then their maxima and weights
 };
 AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len);
 
@@ -52,12 +54,15 @@ struct AttnArgs {
     const char *q;
     int group;
     const uint64_t *mask;
-    float score_scale, v_scale;  // score_scale: scale * k_scale * log2(e)
-    int max_tokens;
+    // scores are (q & q_keep ^ q_flip) . k * score_scale in log2 units, score_scale
+    // > 0: a negative scale flips the signs of q, a zero one clears q
+    uint32_t q_keep, q_flip;
+    float score_scale, v_scale;
+    int max_tokens, max_len;
     int out_f32;
     char *out;
     float *ws_o, *ws_ml;
-    int row_blocks, rows_wg, part, parts;
+    int rows_wg, slot_rows, grid;
 };
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int type, int dim, int q_type, hipStream_t stream);
 

@@ -73,9 +73,9 @@ int check_attn(const kq_cache *c, const kq_batch *s, int64_t q_heads, int64_t ma
     if (rc == KQ_OK) return KQ_OK;
     if (s->n_tokens * q_heads >= ((int64_t)1 << 31) / c->dim) return KQ_ERR_UNSUPPORTED;
     if (max_tokens == 0 || max_len == 0) return KQ_ERR_SHAPE;  // rows to compute, none allowed
-    const AttnPlan p = attn_plan(s->n_seqs, c->heads, q_heads / c->heads, c->dim, max_tokens, max_len);
-    const int64_t items = s->n_seqs * c->heads;
-    if (items > kMaxInt / p.parts || (items * p.parts + 8) > kMaxInt / p.row_blocks) return KQ_ERR_UNSUPPORTED;
+    // the kernels count units in int32: at most a row block to every 16 rows
+    const int64_t blocks = (max_tokens * (q_heads / c->heads) + 15) / 16;
+    if (s->n_seqs > kMaxInt / (c->heads * ((max_len + ATTN_UNIT - 1) / ATTN_UNIT) * blocks)) return KQ_ERR_UNSUPPORTED;
     return 1;
 }
 
@@ -85,22 +85,21 @@ namespace kq {
 
 AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len) {
     AttnPlan p;
+    // Waves of 32 rows, at dim 256 of 16 (whose sums and operands fit the
+    // registers); 8 of them where there are rows for more than 4.
     const int64_t rows = max_tokens * group;
-    // up to 16 rows: one wave of them; else 4 waves of 32 (dim 256: of 16, whose
-    // sums and operands fit the registers) on shared tiles
-    p.rows_wg = rows <= 16 ? 16 : dim == 256 ? 64 : 128;
+    const int rows_wave = dim == 256 ? 16 : 32;
+    p.waves = rows <= 16 ? 0 : rows <= 4 * rows_wave ? 4 : 8;
+    p.rows_wg = p.waves ? p.waves * rows_wave : 16;
     p.row_blocks = (int)((rows + p.rows_wg - 1) / p.rows_wg);
-    // parts: enough workgroups for several on each of 256 compute units (ragged
-    // sequences even out over them), of at least 128 slots (a tile to each wave)
-    const int64_t groups = std::max<int64_t>(1, n_seqs * heads * p.row_blocks);
-    const int64_t want = std::max<int64_t>(1, (2048 + groups - 1) / groups);
-    int64_t part = (max_len + want - 1) / want;
-    part = std::max<int64_t>(128, (part + 127) / 128 * 128);
-    p.part = (int)part;
-    p.parts = (int)((max_len + part - 1) / part);
-    const int64_t rows_ws = p.parts > 1 ? n_seqs * heads * p.parts * rows : 0;
-    p.o_bytes = rows_ws * dim * 4;
-    p.bytes = p.o_bytes + rows_ws * 8;
+    p.slot_rows = (int)std::min<int64_t>(rows, p.rows_wg);
+    // Workgroups: as many as stay on 256 compute units together (8 waves each),
+    // or the units there can be.
+    const int64_t units = n_seqs * heads * p.row_blocks * ((max_len + ATTN_UNIT - 1) / ATTN_UNIT);
+    p.grid = (int)std::min<int64_t>(units, p.waves == 8 ? 256 : 512);
+    const int64_t slots = max_len > ATTN_UNIT ? 2 * (int64_t)p.grid * p.slot_rows : 0;
+    p.o_bytes = slots * dim * 4;
+    p.bytes = p.o_bytes + slots * 8;
     return p;
 }
 
@@ -194,19 +193,22 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     a.q = static_cast<const char *>(q);
     a.group = (int)(q_heads / cache->heads);
     a.mask = mask;
-    a.score_scale = (float)((double)scale * cache->k_scale * 1.44269504088896340736);
+    const float c = (float)((double)scale * cache->k_scale * 1.44269504088896340736);
+    a.q_keep = c == 0.f ? 0u : ~0u;
+    a.q_flip = c < 0.f ? 0x80008000u : 0u;
+    a.score_scale = c == 0.f ? 1.f : std::fabs(c);
     a.v_scale = cache->v_scale;
     a.max_tokens = (int)max_tokens;
+    a.max_len = (int)max_len;
     a.out_f32 = out_type == KQ_T_F32;
     a.out = static_cast<char *>(out);
     a.ws_o = static_cast<float *>(workspace);
     a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.o_bytes);
-    a.row_blocks = p.row_blocks;
     a.rows_wg = p.rows_wg;
-    a.part = p.part;
-    a.parts = p.parts;
+    a.slot_rows = p.slot_rows;
+    a.grid = p.grid;
     if (launch_attn(a, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
-    count_dispatch(p.rows_wg == 16 ? V_ATTN_FEW : V_ATTN_ROWS);
+    count_dispatch(p.waves == 0 ? V_ATTN_FEW : V_ATTN_ROWS);
     return KQ_OK;
 }
 

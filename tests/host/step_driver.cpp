@@ -78,9 +78,9 @@ int main() {
                 kq_cache_keep(&c, n < 2 ? n : 1, &s, I, I, nullptr);
             }
 
-    // plans: parts of whole tiles for every wave that cover max_len, rows covered by
-    // the blocks, a workspace of one row of sums, maximum and weight to each
-    // (sequence, head, part, row)
+    // plans: rows covered by the blocks, no more workgroups than units, and a
+    // workspace of two blocks' rows of sums, maximum and weight to each workgroup
+    // where a block can be cut
     for (int dim : dims)
         for (int page : pages)
             for (int64_t seqs : {1, 3, 64, 4096})
@@ -94,16 +94,19 @@ int main() {
                             const int rc = kq_attn_tree(&c, &s, KQ_T_F16, A, 2 * G, nullptr, 1.f, T, len, KQ_T_F16, A, A, bytes, nullptr);
                             if (rc == KQ_ERR_UNSUPPORTED) continue;
                             EXPECT(rc == KQ_OK && attns == before + 1);
-                            EXPECT(plan.part % 128 == 0 && (int64_t)plan.part * plan.parts >= len);
-                            EXPECT((int64_t)plan.part * (plan.parts - 1) < len);
+                            const int wave = dim == 256 ? 16 : 32;
+                            EXPECT(plan.waves == (T * G <= 16 ? 0 : T * G <= 4 * wave ? 4 : 8));
+                            EXPECT(plan.rows_wg == (plan.waves ? plan.waves * wave : 16));
                             EXPECT((int64_t)plan.rows_wg * plan.row_blocks >= T * G);
                             EXPECT((int64_t)plan.rows_wg * (plan.row_blocks - 1) < T * G);
-                            EXPECT(plan.rows_wg == (T * G <= 16 ? 16 : dim == 256 ? 64 : 128));
-                            const int64_t rows = plan.parts > 1 ? seqs * 2 * plan.parts * T * G : 0;
+                            EXPECT(plan.slot_rows == (T * G < plan.rows_wg ? T * G : plan.rows_wg));
+                            const int64_t units = seqs * 2 * plan.row_blocks * ((len + 127) / 128);
+                            EXPECT(units <= INT32_MAX && plan.grid >= 1 && plan.grid <= units && plan.grid <= 512);
+                            const int64_t rows = len > 128 ? 2 * (int64_t)plan.grid * plan.slot_rows : 0;
                             EXPECT((int64_t)bytes == rows * (dim * 4 + 8) && plan.o_bytes == rows * dim * 4);
                             EXPECT((char *)attn.ws_ml == A + plan.o_bytes && (char *)attn.ws_o == A);
-                            EXPECT(1 << attn.cache.page_shift == page && attn.group == G);
-                            EXPECT(seqs * 2 * plan.parts * (int64_t)plan.row_blocks < INT32_MAX);
+                            EXPECT(1 << attn.cache.page_shift == page && attn.group == G && attn.grid == plan.grid);
+                            EXPECT(attn.rows_wg == plan.rows_wg && attn.slot_rows == plan.slot_rows && attn.max_len == len);
                             if (bytes) EXPECT(kq_attn_tree(&c, &s, KQ_T_F16, A, 2 * G, nullptr, 1.f, T, len, KQ_T_F16, A, A, bytes - 1, nullptr) == KQ_ERR_SHAPE);
                         }
 

@@ -145,23 +145,22 @@ def test_attn_size_limits(kq):
     big = batch(kq, n_tokens=(1 << 31) // (4 * 128))
     assert attn(kq, cache(kq), big) == kq.KQ_ERR_UNSUPPORTED
     many = batch(kq, n_seqs=1 << 30)
-    assert attn(kq, cache(kq, heads=4), many) == kq.KQ_ERR_UNSUPPORTED
+    assert attn(kq, cache(kq, heads=4), many) == kq.KQ_ERR_UNSUPPORTED   # units past int32
 
 
 def test_attn_workspace(kq):
-    """Short calls need none; the size covers every (sequence, head, part, row)
-    and grows with no argument falling."""
+    """Calls that cut nothing need none; the size is bounded however long the
+    sequences, and falls with no argument."""
     c = cache(kq)
     size = lambda n, t, q, m: kq.kq_attn_tree_workspace(c, batch(kq, n_seqs=n, n_tokens=n * t), q, t, m)  # noqa: E731
-    assert size(1, 1, 4, 1) == 0
+    assert size(1, 1, 4, 1) == size(9, 1, 4, 128) == 0
     assert size(1, 1, 4, 100000) > 0
     for n in (1, 5, 64):
         for t in (1, 7, 64):
             last = 0
             for m in (1, 128, 129, 1000, 8191, 131072, 1 << 20):
                 s = size(n, t, 16, m)
-                assert s == 0 or s % (n * 2 * t * 8 * (128 * 4 + 8)) == 0
-                assert s >= last or m > 128
+                assert last <= s <= 2 * 512 * 256 * (128 * 4 + 8)
                 last = s
     for bad in (size(1, 65, 4, 10), size(-1, 1, 4, 10), size(1, 1, 5, 10), size(1, 1, 4, 0), size(1, 1, 4, 1 << 31)):
         assert bad == 0
