@@ -222,7 +222,8 @@ __device__ __forceinline__ void share_chunk(const AttnArgs &a, Share &s, int chu
     s.blocks = blocks;
 }
 __device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
-// all the units of one key head, and the first chunk
+// all the units of one key head, and the first chunk; one wave of the grid notes
+// them for the kernel that joins the parts
 __device__ __forceinline__ Share share_of(const AttnArgs &a) {
     Share s;
     share_chunk(a, s, 0);
@@ -233,6 +234,18 @@ __device__ __forceinline__ Share share_of(const AttnArgs &a) {
         for (int c = 1; c * 64 < a.batch.n_seqs; ++c) {
             share_chunk(a, t, c);
             s.all += last_lane(t.incl);
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x < 64 && a.ws_seq) {
+        Share t = s;
+        for (int c = 0; c * 64 < a.batch.n_seqs; ++c) {
+            if (c) {
+                t.before += last_lane(t.incl);
+                share_chunk(a, t, c);
+            }
+            const int b = c * 64 + threadIdx.x;
+            if (b < a.batch.n_seqs)
+                reinterpret_cast<v4i *>(a.ws_seq)[b] = v4i{t.before + t.incl - t.tiles * t.blocks, t.tiles, t.blocks, s.all};
         }
     }
     return s;
@@ -331,6 +344,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
     typedef typename MM::acc acc_t;
     typedef Frag<E, F8> FR;
     typedef typename FR::raw raw_t;
+    constexpr int U = D * FR::BYTES <= 128 ? 2 : 1;
     constexpr int NK = D / 32;  // steps of the first product
     constexpr int ND = D / RW;  // results of the second product
     constexpr int ES = FR::BYTES;
@@ -412,51 +426,77 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
         for (int d = 0; d < ND; ++d) o[d] = acc_t{};
         float m = M_START, l = 0.f;
 
-        int key0 = pc.from + 32 * wave;
-        Runs ru = runs(key0);
-        // Keys are loaded a turn ahead, values at the turn's begin, where the
-        // registers hold both (512 bytes of a lane at dim 256 they do not: there
-        // each is loaded when the other is done with).
+        // A turn of a wave is U tiles of 32 keys, 128 apart (the waves take tiles in
+        // turn); the second may lie past the piece.  Keys are loaded a turn ahead,
+        // values at the turn's begin, where the registers hold both (at dim 256 and
+        // 16 bits they do not: there each is loaded when the other is done with).
         constexpr bool AHEAD = D * ES <= 256;
-        raw_t kf[2][NK];
-        if (AHEAD && key0 < to) load_k(ru, kf);
-        for (; key0 < to; key0 += 128) {
-            raw_t vf[ND];
-            const int next = key0 + 128;
+        int key0 = pc.from + 32 * wave;
+        raw_t kf[U][2][NK];
+        Runs ru[U];
+        auto find = [&](int key) {
+#pragma unroll
+            for (int x = 0; x < U; ++x) ru[x] = runs(key + 128 * x);
+        };
+        auto keys = [&](int key) {
+#pragma unroll
+            for (int x = 0; x < U; ++x)
+                if (key + 128 * x < to) load_k(ru[x], kf[x]);
+        };
+        find(key0);
+        if (AHEAD) keys(key0);
+        for (; key0 < to; key0 += 128 * U) {
+            raw_t vf[U][ND];
+            auto values = [&] {
+#pragma unroll
+                for (int x = 0; x < U; ++x) {
+                    if (key0 + 128 * x < to) {
+                        load_v(ru[x], vf[x]);
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < ND; ++d) vf[x][d] = raw_t{};
+                    }
+                }
+            };
+            const int next = key0 + 128 * U;
             if constexpr (AHEAD) {
-                load_v(ru, vf);
-                ru = runs(next);
+                values();
+                find(next);
             } else {
-                load_k(ru, kf);
+                keys(key0);
             }
 
-            acc_t sc[2];
+            // p[8 x + e]: key key0 + 128 x + 8 g + e of this lane's row
+            float p[8 * U];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                sc[t] = acc_t{};
+            for (int x = 0; x < U; ++x)
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(kf[t][kk]), qf[kk], sc[t]);
-            }
+                for (int t = 0; t < 2; ++t) {
+                    acc_t sc = acc_t{};
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk) sc = MM::mul(FR::template op<op_t>(kf[x][t][kk]), qf[kk], sc);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) p[8 * x + 4 * t + r] = sc[r];
+                }
             if constexpr (AHEAD) {
-                if (next < to) load_k(ru, kf);
+                keys(next);
             } else {
-                load_v(ru, vf);
-                ru = runs(next);
+                values();
+                find(next);
             }
 
-            // p[e]: key key0 + 8 g + e of this lane's row
-            float p[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) p[r] = sc[r >> 2][r & 3];
-            const bool ragged = key0 + 32 > len;
+            const bool ragged = key0 + 128 * (U - 1) + 32 > min(len, to);
             if (ragged) {
-                const uint32_t on = seen8(sees, key0 + 8 * g - len);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) p[r] = on >> r & 1u ? p[r] : -__builtin_inff();
+                for (int x = 0; x < U; ++x) {
+                    const uint32_t on = key0 + 128 * x < to ? seen8(sees, key0 + 128 * x + 8 * g - len) : 0u;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) p[8 * x + r] = on >> r & 1u ? p[8 * x + r] : -__builtin_inff();
+                }
             }
             float top = p[0];
 #pragma unroll
-            for (int r = 1; r < 8; ++r) top = fmaxf(top, p[r]);
+            for (int r = 1; r < 8 * U; ++r) top = fmaxf(top, p[r]);
             top *= a.score_scale;
             if (__any(top > m + M_SLACK)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
@@ -468,28 +508,37 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int d = 0; d < ND; ++d) o[d] *= f;
             }
-            v4u w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(p[2 * j], a.score_scale, -m));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(p[2 * j + 1], a.score_scale, -m));
-                l += p0 + p1;
-                w[j] = pack2<E>(p0, p1);
-            }
-            const op_t pf = __builtin_bit_cast(op_t, w);
             bool odd = false;
             if (ragged) {
                 // slots past the end hold anything: zeros
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    FR::first(vf[d], min(max(total - (key0 + 8 * g), 0), 8));
-                    odd |= FR::drop_odd(vf[d]);
-                }
+                for (int x = 0; x < U; ++x)
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {
+                        FR::first(vf[x][d], min(max(total - (key0 + 128 * x + 8 * g), 0), 8));
+                        odd |= FR::drop_odd(vf[x][d]);
+                    }
             }
 #pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[d]), pf, o[d]);
-            if (__any(odd))
-                add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, pc.b, h, len, total}, key0, lane, sees, o);
+            for (int x = 0; x < U; ++x) {
+                v4u w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * x + 2 * j], a.score_scale, -m));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * x + 2 * j + 1], a.score_scale, -m));
+                    l += p0 + p1;
+                    w[j] = pack2<E>(p0, p1);
+                }
+                const op_t pf = __builtin_bit_cast(op_t, w);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[x][d]), pf, o[d]);
+            }
+            if (__any(odd)) {
+#pragma nounroll
+                for (int x = 0; x < U; ++x)
+                    if (key0 + 128 * x < to)
+                        add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, pc.b, h, len, total}, key0 + 128 * x, lane, sees, o);
+            }
         }
 
         // Join the waves.
@@ -783,64 +832,67 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs
 }
 
 // out = sum over the parts of a cut block, each weighted by exp2(its maximum -
-// the largest).  One workgroup to a (token, head); D / 4 threads read a part's
-// sums, 256 / (D / 4) parts at a time.
+// the largest).  A workgroup has `rows` (1 or group) rows of a token's heads; D / 4
+// threads read a part's sums, and the 256 / (D / 4) such sets share out the rows
+// and, where there are more sets than rows, the parts.
 template <class E, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-    constexpr int TPP = D / 4, AT_ONCE = 256 / TPP;
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int rows) {
+    constexpr int TPP = D / 4, SETS = 256 / TPP;
     __shared__ v4f so[256];
-    __shared__ v2f sml[AT_ONCE];
+    __shared__ v2f sml[SETS];
     const int heads = a.cache.heads, G = a.group;
-    const int tok = blockIdx.x, head = blockIdx.y, h = head / G;
+    const int tok = blockIdx.x, head0 = blockIdx.y * rows, h = head0 / G;
     const int b = batch_seq(a.batch, tok);
     const Seq sq = seq_of(a, b);
     const int i = tok - sq.first;
-    Share s = share_of(a);
-    for (int c = 0; c < b >> 6; ++c) {
-        const int before = s.before + last_lane(s.incl);
-        share_chunk(a, s, c + 1);
-        s.before = before;
-    }
     if (i < 0 || i >= sq.T) return;
-    const int units = s.all * heads, groups = min(a.grid, units);
-    const int tiles = __builtin_amdgcn_readlane(s.tiles, b & 63), blocks = __builtin_amdgcn_readlane(s.blocks, b & 63);
-    const int mine = tiles * blocks;
-    const int row = i * G + head % G, rb = row / a.rows_wg;
-    const int from = heads * (s.before + __builtin_amdgcn_readlane(s.incl, b & 63) - mine) + h * mine + rb * tiles;
-    // the workgroups that hold the first and the last unit
-    const int w0 = (int)(((int64_t)(from + 1) * groups - 1) / units);
-    const int w1 = (int)(((int64_t)(from + tiles) * groups - 1) / units);
-    if (w0 == w1) return;  // one workgroup had them all: finished there
-    const int lane = threadIdx.x % TPP, which = threadIdx.x / TPP;
-    float m = M_START, l = 0.f;
-    v4f o = {0.f, 0.f, 0.f, 0.f};
-    for (int w = w0 + which; w <= w1; w += AT_ONCE) {
-        // a workgroup's first piece lies in its first slot
-        const int second = run_begin(w, groups, units) < from;
-        const int64_t r = (2 * (int64_t)w + second) * a.slot_rows + (row - rb * a.rows_wg);
-        const v2f ml = *reinterpret_cast<const v2f *>(a.ws_ml + 2 * r);
-        const v4f po = *reinterpret_cast<const v4f *>(a.ws_o + r * D + 4 * lane);
-        const float up = fmaxf(m, ml[0]);
-        const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
-        m = up;
-        l = l * f + ml[1] * pf;
-        o = o * f + po * pf;
+    const v4i sh = reinterpret_cast<const v4i *>(a.ws_seq)[b];  // units before, tiles, blocks, all units
+    const int units = sh[3] * heads, groups = min(a.grid, units), tiles = sh[1];
+    int sets = 1;  // sets of threads to a row
+    while (2 * sets * rows <= SETS) sets *= 2;
+    const int lane = threadIdx.x % TPP, set = threadIdx.x / TPP, sub = set % sets;
+    for (int j = set / sets; j < rows + SETS; j += SETS / sets) {  // (the same number of turns for all)
+        if (j - set / sets >= rows) break;
+        const int row = i * G + head0 % G + min(j, rows - 1), rb = row / a.rows_wg;
+        const int from = heads * sh[0] + h * tiles * sh[2] + rb * tiles;
+        // the workgroups that hold the block's first and last unit
+        const int w0 = (int)(((int64_t)(from + 1) * groups - 1) / units);
+        const int w1 = (int)(((int64_t)(from + tiles) * groups - 1) / units);
+        float m = M_START, l = 0.f;
+        v4f o = {0.f, 0.f, 0.f, 0.f};
+        for (int w = w0 == w1 ? w1 + 1 : w0 + sub; w <= w1; w += sets) {  // (one workgroup: finished there)
+            // a workgroup's first piece lies in its first slot
+            const int second = run_begin(w, groups, units) < from;
+            const int64_t r = (2 * (int64_t)w + second) * a.slot_rows + (row - rb * a.rows_wg);
+            const v2f ml = *reinterpret_cast<const v2f *>(a.ws_ml + 2 * r);
+            const v4f po = *reinterpret_cast<const v4f *>(a.ws_o + r * D + 4 * lane);
+            const float up = fmaxf(m, ml[0]);
+            const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
+            m = up;
+            l = l * f + ml[1] * pf;
+            o = o * f + po * pf;
+        }
+        if (sets > 1) {
+            __syncthreads();
+            so[threadIdx.x] = o;
+            if (lane == 0) sml[set] = v2f{m, l};
+            __syncthreads();
+            if (sub == 0) {
+                for (int k = 1; k < sets; ++k) {
+                    const v2f ml = sml[set + k];
+                    const float up = fmaxf(m, ml[0]);
+                    const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
+                    m = up;
+                    l = l * f + ml[1] * pf;
+                    o = o * f + so[threadIdx.x + k * TPP] * pf;
+                }
+            }
+        }
+        if (sub == 0 && j < rows && w0 != w1) {
+            const float norm = l == 0.f ? 0.f : a.v_scale / l;
+            put4<E>(a, true, o * norm, ((int64_t)tok * ((int64_t)heads * G) + head0 + j) * D + 4 * lane, 0);
+        }
     }
-    so[threadIdx.x] = o;
-    if (lane == 0) sml[which] = v2f{m, l};
-    __syncthreads();
-    if (which) return;
-#pragma unroll
-    for (int k = 1; k < AT_ONCE; ++k) {
-        const v2f ml = sml[k];
-        const float up = fmaxf(m, ml[0]);
-        const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
-        m = up;
-        l = l * f + ml[1] * pf;
-        o = o * f + so[k * TPP + lane] * pf;
-    }
-    const float norm = l == 0.f ? 0.f : a.v_scale / l;
-    put4<E>(a, true, o * norm, ((int64_t)tok * ((int64_t)heads * G) + head) * D + 4 * lane, 0);
 }
 
 template <class E, bool F8, int D>
@@ -854,8 +906,11 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
         hipLaunchKernelGGL((attn_tile_kernel<E, F8, D, 8>), grid, dim3(512), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.bytes == 0) return e;  // no workspace: nothing is cut
-    hipLaunchKernelGGL((attn_join_kernel<E, D>), dim3((unsigned)a.batch.n_tokens, (unsigned)(a.cache.heads * a.group)),
-                       dim3(256), 0, stream, a);
+    // many rows: the heads of a group together, which find their parts once
+    const int heads = a.cache.heads * a.group;
+    const int rows = (int64_t)a.batch.n_tokens * heads > 2048 ? a.group : 1;
+    hipLaunchKernelGGL((attn_join_kernel<E, D>), dim3((unsigned)a.batch.n_tokens, (unsigned)(heads / rows)), dim3(256), 0,
+                       stream, a, rows);
     return hipGetLastError();
 }
 

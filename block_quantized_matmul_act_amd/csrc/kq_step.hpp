@@ -44,7 +44,8 @@ hipError_t launch_rope_append(const RopeArgs &a, int type, int dim, int q_type, 
 constexpr int ATTN_UNIT = 128;
 struct AttnPlan {
     int waves, rows_wg, row_blocks, slot_rows, grid;
-    int64_t o_bytes, bytes;  // workspace: sums, then their maxima and weights
+    // workspace: sums, their maxima and weights (to ml_end), 16 bytes to a sequence
+    int64_t o_bytes, ml_end, bytes;
 };
 AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len);
 
@@ -62,6 +63,7 @@ struct AttnArgs {
     int out_f32;
     char *out;
     float *ws_o, *ws_ml;
+    int32_t *ws_seq;
     int rows_wg, slot_rows, grid;
 };
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int type, int dim, int q_type, hipStream_t stream);

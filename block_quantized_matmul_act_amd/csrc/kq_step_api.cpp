@@ -99,7 +99,8 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, in
     p.grid = (int)std::min<int64_t>(units, p.waves == 8 ? 256 : 512);
     const int64_t slots = max_len > ATTN_UNIT ? 2 * (int64_t)p.grid * p.slot_rows : 0;
     p.o_bytes = slots * dim * 4;
-    p.bytes = p.o_bytes + slots * 8;
+    p.ml_end = p.o_bytes + (slots + (slots & 1)) * 8;
+    p.bytes = slots ? p.ml_end + n_seqs * 16 : 0;
     return p;
 }
 
@@ -204,6 +205,7 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     a.out = static_cast<char *>(out);
     a.ws_o = static_cast<float *>(workspace);
     a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.o_bytes);
+    a.ws_seq = p.bytes ? reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + p.ml_end) : nullptr;
     a.rows_wg = p.rows_wg;
     a.slot_rows = p.slot_rows;
     a.grid = p.grid;

@@ -103,7 +103,9 @@ int main() {
                             const int64_t units = seqs * 2 * plan.row_blocks * ((len + 127) / 128);
                             EXPECT(units <= INT32_MAX && plan.grid >= 1 && plan.grid <= units && plan.grid <= 512);
                             const int64_t rows = len > 128 ? 2 * (int64_t)plan.grid * plan.slot_rows : 0;
-                            EXPECT((int64_t)bytes == rows * (dim * 4 + 8) && plan.o_bytes == rows * dim * 4);
+                            EXPECT((int64_t)bytes == (rows ? rows * (dim * 4 + 8) + (rows & 1) * 8 + seqs * 16 : 0));
+                            EXPECT(plan.o_bytes == rows * dim * 4);
+                            EXPECT((char *)attn.ws_seq == (bytes ? A + bytes - seqs * 16 : nullptr) && plan.ml_end % 16 == 0);
                             EXPECT((char *)attn.ws_ml == A + plan.o_bytes && (char *)attn.ws_o == A);
                             EXPECT(1 << attn.cache.page_shift == page && attn.group == G && attn.grid == plan.grid);
                             EXPECT(attn.rows_wg == plan.rows_wg && attn.slot_rows == plan.slot_rows && attn.max_len == len);

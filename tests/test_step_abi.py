@@ -160,7 +160,7 @@ def test_attn_workspace(kq):
             last = 0
             for m in (1, 128, 129, 1000, 8191, 131072, 1 << 20):
                 s = size(n, t, 16, m)
-                assert last <= s <= 2 * 512 * 256 * (128 * 4 + 8)
+                assert last <= s <= 2 * 512 * 256 * (128 * 4 + 8) + 16 * n
                 last = s
     for bad in (size(1, 65, 4, 10), size(-1, 1, 4, 10), size(1, 1, 5, 10), size(1, 1, 4, 0), size(1, 1, 4, 1 << 31)):
         assert bad == 0
