@@ -334,269 +334,26 @@ __device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane,
     }
 }
 
-// Up to 16 rows: one wave's worth, so the 4 waves of a workgroup cut the keys
-// (32 at a time in turn) and their sums are joined in LDS.
-template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
-    constexpr int RW = 16;
-    typedef Mfma<E, RW> MM;
-    typedef typename MM::op op_t;
-    typedef typename MM::acc acc_t;
-    typedef Frag<E, F8> FR;
-    typedef typename FR::raw raw_t;
-    constexpr int U = D * FR::BYTES <= 128 ? 2 : 1;
-    constexpr int NK = D / 32;  // steps of the first product
-    constexpr int ND = D / RW;  // results of the second product
-    constexpr int ES = FR::BYTES;
+// ---------------------------------------------------------------- tiles
 
-    __shared__ float lo[4 * RW * (D + 4)];  // sums of the waves: [wave][row][dim]
-    __shared__ float lm[4 * RW], ll[4 * RW];
-
-    Share share = share_of(a);
-    const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
-    if ((int)blockIdx.x >= groups) return;
-    const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 15, g = lane >> 4;
-    const int G = a.group;
-    // Key of this lane's row of the first product's two results (of 16 keys each;
-    // the second: 4 on): see the head of the file.
-    const int krow = 8 * (n >> 2) + (n & 3);
-    const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
-    const int64_t head_bytes = (int64_t)D * ES << page_shift;
-
-    for (int u = begin; u < end;) {
-        const Piece pc = piece_at(a, share, u, end);
-        const int h = pc.h;
-        const Seq sq = seq_of(a, pc.b);
-        const int len = sq.len, total = sq.total, R = sq.T * G, to = min(pc.to, total);
-        const bool used = n < R;
-        const int tok = used ? n / G : 0;
-        const int64_t q_row = (int64_t)(sq.first + tok) * ((int64_t)heads * G) + h * G + (used ? n % G : 0);
-
-        op_t qf[NK];
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk) {
-            v4u w = {0u, 0u, 0u, 0u};
-            if (used) w = (*reinterpret_cast<const v4u *>(a.q + (q_row * D + 32 * kk + 8 * g) * 2) & a.q_keep) ^ a.q_flip;
-            qf[kk] = __builtin_bit_cast(op_t, w);
-        }
-        uint64_t sees = 0;
-        if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(total - len);
-
-        // Addresses: 16 consecutive slots from a multiple of 16 lie in one page, so a
-        // tile of 32 has two runs whose addresses are the same for the whole wave
-        // (scalar registers); a lane adds its place in its run, which never changes.
-        const int last_run = (total - 1) & ~15;
-        struct Runs {
-            int64_t page[2];  // offset of the head's page
-            int slot[2];      // place in it
-        };
-        auto runs = [&](int key) {
-            Runs r;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int slot = min(key + 16 * i, last_run);  // (a run past the end: the last one again, masked)
-                r.page[i] = ((int64_t)slot_page(a.cache, a.batch, pc.b, slot) * heads + h) * head_bytes;
-                r.slot[i] = slot & page_mask;
-            }
-            return r;
-        };
-        // (both of a lane's keys lie in the same run)
-        auto load_k = [&](const Runs &ru, raw_t(&kf)[2][NK]) {
-            const int64_t at = n >> 3 ? ru.page[1] + ru.slot[1] * (D * ES) : ru.page[0] + ru.slot[0] * (D * ES);
-            const char *p = a.cache.k + at + ((krow & 15) * (D * ES) + 8 * g * ES);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) kf[t][kk] = *reinterpret_cast<const raw_t *>(p + (4 * t * D + 32 * kk) * ES);
-        };
-        auto load_v = [&](const Runs &ru, raw_t(&vf)[ND]) {
-            const int64_t at = g >> 1 ? ru.page[1] + ru.slot[1] * ES : ru.page[0] + ru.slot[0] * ES;
-            const char *p = a.cache.v + at + ((n << page_shift) + 8 * (g & 1)) * ES;
-            const int step = (RW * ES) << page_shift;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) vf[d] = *reinterpret_cast<const raw_t *>(p + d * step);
-        };
-
-        acc_t o[ND];
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] = acc_t{};
-        float m = M_START, l = 0.f;
-
-        // A turn of a wave is U tiles of 32 keys, 128 apart (the waves take tiles in
-        // turn); the second may lie past the piece.  Keys are loaded a turn ahead,
-        // values at the turn's begin, where the registers hold both (at dim 256 and
-        // 16 bits they do not: there each is loaded when the other is done with).
-        constexpr bool AHEAD = D * ES <= 256;
-        int key0 = pc.from + 32 * wave;
-        raw_t kf[U][2][NK];
-        Runs ru[U];
-        auto find = [&](int key) {
-#pragma unroll
-            for (int x = 0; x < U; ++x) ru[x] = runs(key + 128 * x);
-        };
-        auto keys = [&](int key) {
-#pragma unroll
-            for (int x = 0; x < U; ++x)
-                if (key + 128 * x < to) load_k(ru[x], kf[x]);
-        };
-        find(key0);
-        if (AHEAD) keys(key0);
-        for (; key0 < to; key0 += 128 * U) {
-            raw_t vf[U][ND];
-            auto values = [&] {
-#pragma unroll
-                for (int x = 0; x < U; ++x) {
-                    if (key0 + 128 * x < to) {
-                        load_v(ru[x], vf[x]);
-                    } else {
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) vf[x][d] = raw_t{};
-                    }
-                }
-            };
-            const int next = key0 + 128 * U;
-            if constexpr (AHEAD) {
-                values();
-                find(next);
-            } else {
-                keys(key0);
-            }
-
-            // p[8 x + e]: key key0 + 128 x + 8 g + e of this lane's row
-            float p[8 * U];
-#pragma unroll
-            for (int x = 0; x < U; ++x)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    acc_t sc = acc_t{};
-#pragma unroll
-                    for (int kk = 0; kk < NK; ++kk) sc = MM::mul(FR::template op<op_t>(kf[x][t][kk]), qf[kk], sc);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) p[8 * x + 4 * t + r] = sc[r];
-                }
-            if constexpr (AHEAD) {
-                keys(next);
-            } else {
-                values();
-                find(next);
-            }
-
-            const bool ragged = key0 + 128 * (U - 1) + 32 > min(len, to);
-            if (ragged) {
-#pragma unroll
-                for (int x = 0; x < U; ++x) {
-                    const uint32_t on = key0 + 128 * x < to ? seen8(sees, key0 + 128 * x + 8 * g - len) : 0u;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) p[8 * x + r] = on >> r & 1u ? p[8 * x + r] : -__builtin_inff();
-                }
-            }
-            float top = p[0];
-#pragma unroll
-            for (int r = 1; r < 8 * U; ++r) top = fmaxf(top, p[r]);
-            top *= a.score_scale;
-            if (__any(top > m + M_SLACK)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float up = fmaxf(m, top);
-                const float f = __builtin_amdgcn_exp2f(m - up);
-                m = up;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] *= f;
-            }
-            bool odd = false;
-            if (ragged) {
-                // slots past the end hold anything: zeros
-#pragma unroll
-                for (int x = 0; x < U; ++x)
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) {
-                        FR::first(vf[x][d], min(max(total - (key0 + 128 * x + 8 * g), 0), 8));
-                        odd |= FR::drop_odd(vf[x][d]);
-                    }
-            }
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-                v4u w;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * x + 2 * j], a.score_scale, -m));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * x + 2 * j + 1], a.score_scale, -m));
-                    l += p0 + p1;
-                    w[j] = pack2<E>(p0, p1);
-                }
-                const op_t pf = __builtin_bit_cast(op_t, w);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(vf[x][d]), pf, o[d]);
-            }
-            if (__any(odd)) {
-#pragma nounroll
-                for (int x = 0; x < U; ++x)
-                    if (key0 + 128 * x < to)
-                        add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, pc.b, h, len, total}, key0 + 128 * x, lane, sees, o);
-            }
-        }
-
-        // Join the waves.
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
-        if (u != begin) __syncthreads();  // the piece before has been read
-#pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f *>(lo + (wave * RW + n) * (D + 4) + d * RW + 4 * g) = o[d];
-        if (g == 0) {
-            lm[wave * RW + n] = m;
-            ll[wave * RW + n] = l;
-        }
-        __syncthreads();
-        const int out_row = threadIdx.x >> 4, jt = threadIdx.x & 15;  // 16 threads to a row
-        if (out_row < R) {
-            float mm = M_START;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mm = fmaxf(mm, lm[out_row + k * RW]);
-            float f[4], sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f[k] = __builtin_amdgcn_exp2f(lm[out_row + k * RW] - mm);
-                sum += f[k] * ll[out_row + k * RW];
-            }
-            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + out_row;
-            const float norm = pc.whole ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
-            const int64_t o_row = ((int64_t)(sq.first + out_row / G) * ((int64_t)heads * G) + h * G + out_row % G) * D;
-#pragma unroll
-            for (int v = 0; v < D; v += 64) {
-                const int dim = v + jt * 4;
-                v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    acc += f[k] * *reinterpret_cast<const v4f *>(lo + (out_row + k * RW) * (D + 4) + dim);
-                put4<E>(a, pc.whole, acc * norm, o_row + dim, slot_row * D + dim);
-            }
-            if (!pc.whole && jt == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{mm, sum};
-        }
-        u += pc.units;
-    }
-}
-
-// The same sums for sequences that bring more rows: WAVES waves of RW rows share
-// tiles of KEYS keys staged in LDS (two tiles: one in use, one being written; the
-// registers hold the one after).  Memory is read a line at a time, and once for
-// all the rows of the workgroup.
+// A tile of KEYS keys and values in LDS, staged by THREADS threads through
+// registers.  MFMA operands straight from memory would make the 16 lanes of a
+// quarter wave read 16 different rows, one cache access each (measured: 63
+// accesses to an 8-byte load of a wave, and 4 TB/s); staged, the lanes of a load
+// read whole runs of rows.
 // LDS holds 16-byte pieces; a row's pieces are permuted by an XOR with bits of
 // the row, so that the lanes of a read, which want one piece of many rows, meet
 // different banks.
-template <class E, bool F8, int D, int WAVES>
+template <class E, bool F8, int D, int KEYS, int THREADS>
 struct Tile {
-    static constexpr int ES = F8 ? 1 : 2;
-    static constexpr int KEYS = D == 256 ? 32 : 64;
+    typedef Frag<E, F8> FR;
+    typedef typename FR::raw raw_t;
+    static constexpr int ES = FR::BYTES;
     static constexpr int KB = D * ES, VB = KEYS * ES;  // bytes of a key row and of a feature row
     static constexpr int KP = KB / 16, VP = VB / 16;   // their 16-byte pieces
-    static constexpr int THREADS = WAVES * 64;
     static constexpr int PIECES = KEYS * KP;           // of the keys, and as many of the values
     static constexpr int N = (PIECES + THREADS - 1) / THREADS;  // loads of a thread for each
+    static constexpr int KSTEP = THREADS / KP, VSTEP = THREADS / VP;  // rows between a thread's loads
     static constexpr int K_BYTES = KEYS * KB, BYTES = 2 * K_BYTES;
 
     static __device__ __forceinline__ int k_pos(int key, int piece) {
@@ -604,27 +361,311 @@ struct Tile {
         return key * KB + (piece ^ f) * 16;
     }
     static __device__ __forceinline__ int v_pos(int d, int piece) {
-        const int f = VP == 8 ? d & 7 : VP == 4 ? (d >> 1) & 3 : (d >> 2) & 1;
+        const int f = VP >= 8 ? d & 7 : VP == 4 ? (d >> 1) & 3 : (d >> 2) & 1;
         return K_BYTES + d * VB + (piece ^ f) * 16;
+    }
+
+    // A thread's part: piece t (+ i * THREADS) of the keys and of the values
+    const AttnArgs &a;
+    int t, k_row, k_piece, v_row, v_piece;
+    bool stages;
+    int page_shift, page_mask;
+    // the sequence and head
+    int b, h, len, total, last_run;
+    v4u stage[2 * N];
+
+    __device__ __forceinline__ Tile(const AttnArgs &a_, int t_) : a(a_), t(t_) {
+        k_row = t / KP;
+        k_piece = t % KP;
+        v_row = t / VP;
+        v_piece = t % VP;
+        stages = PIECES >= THREADS || t < PIECES;
+        page_shift = a.cache.page_shift;
+        page_mask = (1 << page_shift) - 1;
+    }
+    __device__ __forceinline__ void aim(int b_, int h_, const Seq &q) {
+        b = b_;
+        h = h_;
+        len = q.len;
+        total = q.total;
+        last_run = (total - 1) & ~15;
+    }
+    // byte offset of the head's page of a slot
+    __device__ __forceinline__ int64_t page_of(int slot) const {
+        return ((int64_t)slot_page(a.cache, a.batch, b, slot) * a.cache.heads + h) * ((int64_t)D * ES << page_shift);
+    }
+    // Addresses: 16 consecutive slots from a multiple of 16 lie in one page, and a
+    // wave's load of keys in one such run, whose address is then a scalar; a run
+    // past the sequence's end is the last one again (masked later).
+    __device__ __forceinline__ void load(int key0) {
+        if (!stages) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int run = __builtin_amdgcn_readfirstlane((k_row + i * KSTEP) & ~15);
+            const int slot = min(key0 + run, last_run);
+            const char *p = a.cache.k + page_of(slot) + (slot & page_mask) * KB;
+            stage[i] = *reinterpret_cast<const v4u *>(p + ((k_row + i * KSTEP) & 15) * KB + k_piece * 16);
+        }
+        int64_t at = 0;
+#pragma unroll
+        for (int r = 0; r < KEYS / 16; ++r) {
+            const int slot = min(key0 + 16 * r, last_run);
+            const int64_t o = page_of(slot) + (slot & page_mask) * ES;
+            at = r == v_piece * (16 / ES) >> 4 ? o : at;
+        }
+        const char *p = a.cache.v + at + ((v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1)));
+#pragma unroll
+        for (int i = 0; i < N; ++i) stage[N + i] = *reinterpret_cast<const v4u *>(p + (i * VSTEP << page_shift) * ES);
+    }
+    // To LDS.  In a tile that reaches past the cached slots: zeros for the values of
+    // slots past the end, which may hold anything, and for infinite and NaN values
+    // of drafted tokens; whether this thread met any of those.
+    __device__ __forceinline__ bool store(char *lds, int key0) {
+        bool found = false;
+        if (!stages) return false;
+        if (key0 + KEYS > len) {
+            const int left = total - (key0 + v_piece * (16 / ES));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v4u &r = stage[N + i];
+                if constexpr (F8) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        raw_t half = {r[2 * j], r[2 * j + 1]};
+                        FR::first(half, min(max(left - 8 * j, 0), 8));
+                        found |= FR::drop_odd(half);
+                        r[2 * j] = half[0];
+                        r[2 * j + 1] = half[1];
+                    }
+                } else {
+                    FR::first(r, min(max(left, 0), 8));
+                    found |= FR::drop_odd(r);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            *reinterpret_cast<v4u *>(lds + k_pos(k_row + i * KSTEP, k_piece)) = stage[i];
+            *reinterpret_cast<v4u *>(lds + v_pos(v_row + i * VSTEP, v_piece)) = stage[N + i];
+        }
+        return found;
     }
 };
 
-template <class E, bool F8, int D, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs a) {
-    constexpr int RW = D == 256 ? 16 : 32;
+// The softmax sums of RW rows of a wave over tiles of KEYS keys.
+template <class E, bool F8, int D, int KEYS, int RW>
+struct Attend {
     typedef Mfma<E, RW> MM;
     typedef typename MM::op op_t;
     typedef typename MM::acc acc_t;
     typedef Frag<E, F8> FR;
     typedef typename FR::raw raw_t;
-    typedef Tile<E, F8, D, WAVES> TL;
-    constexpr int ES = TL::ES, KEYS = TL::KEYS;
-    constexpr int NG = 64 / RW;                    // lane groups: 8 of a step's keys, 8 of a step's features to each
-    constexpr int NK = D / (8 * NG), ND = D / RW;  // steps of the first product, results of the second
-    constexpr int NT = KEYS / RW, NS = KEYS / (8 * NG);  // results of the first, steps of the second
-    constexpr int NR = RW * RW / 64;
+    typedef Tile<E, F8, D, KEYS, 64> TL;           // (for the places in LDS alone)
+    static constexpr int NG = 64 / RW;             // lane groups: 8 of a step's keys, 8 of a step's features to each
+    static constexpr int NK = D / (8 * NG), ND = D / RW;         // steps of the first product, results of the second
+    static constexpr int NT = KEYS / RW, NS = KEYS / (8 * NG);   // results of the first, steps of the second
+    static constexpr int NR = RW * RW / 64;
 
-    __shared__ __align__(16) char tile[2 * TL::BYTES];
+    const AttnArgs &a;
+    int lane, n, g, krow;
+    bool used;
+    int64_t q_row;  // of q and out
+    uint64_t sees;
+    op_t qf[NK];
+    acc_t o[ND];
+    float m, l;
+
+    __device__ __forceinline__ Attend(const AttnArgs &a_) : a(a_) {
+        lane = threadIdx.x & 63;
+        n = lane & (RW - 1);
+        g = lane / RW;
+        // this lane's row of the first product's results: see the head of the file
+        krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+    }
+    // 8 values from an even or odd half piece
+    __device__ __forceinline__ raw_t k_frag(const char *at, int t, int kk) const {
+        const int key = RW == 16 ? krow + 32 * (t >> 1) + 4 * (t & 1) : krow + 32 * t;
+        const int half = NG * kk + g;
+        return *reinterpret_cast<const raw_t *>(at + TL::k_pos(key, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
+    }
+    __device__ __forceinline__ raw_t v_frag(const char *at, int d, int s) const {
+        const int half = NG * s + g;
+        return *reinterpret_cast<const raw_t *>(at + TL::v_pos(RW * d + n, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
+    }
+    // begin rows row0 .. of key head h
+    __device__ __forceinline__ void begin(const Seq &sq, int h, int row0) {
+        const int G = a.group, row = row0 + n;
+        used = row < sq.T * G;
+        const int tok = used ? row / G : 0;
+        q_row = (int64_t)(sq.first + tok) * ((int64_t)a.cache.heads * G) + h * G + (used ? row % G : 0);
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            v4u w = {0u, 0u, 0u, 0u};
+            if (used) w = (*reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (NG * kk + g)) * 2) & a.q_keep) ^ a.q_flip;
+            qf[kk] = __builtin_bit_cast(op_t, w);
+        }
+        sees = 0;
+        if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(sq.total - sq.len);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] = acc_t{};
+        m = M_START;
+        l = 0.f;
+    }
+    // add the tile of keys from key0
+    __device__ __forceinline__ void tile(const char *at, int key0, int len) {
+        // p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's row
+        float p[NT * NR];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            acc_t sc = acc_t{};
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) sc = MM::mul(FR::template op<op_t>(k_frag(at, t, kk)), qf[kk], sc);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) p[t * NR + r] = sc[r];
+        }
+        if (key0 + KEYS > len) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t on = seen8(sees, key0 + 8 * NG * s + 8 * g - len);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
+            }
+        }
+        float top = p[0];
+#pragma unroll
+        for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
+        top *= a.score_scale;
+        if (__any(top > m + M_SLACK)) {
+#pragma unroll
+            for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+            const float up = fmaxf(m, top);
+            const float f = __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= f;
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            v4u w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], a.score_scale, -m));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], a.score_scale, -m));
+                l += p0 + p1;
+                w[j] = pack2<E>(p0, p1);
+            }
+            const op_t pf = __builtin_bit_cast(op_t, w);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(v_frag(at, d, s)), pf, o[d]);
+        }
+    }
+    // what infinite and NaN values of the tile's drafted tokens add
+    __device__ __forceinline__ void odd_values(int b, int h, const Seq &sq, int key0) {
+#pragma nounroll
+        for (int s = 0; s < NS; ++s)
+            add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, sq.len, sq.total}, key0 + 8 * NG * s, lane, sees, o);
+    }
+    // the whole rows' weights (the lane groups hold parts of them)
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
+    }
+};
+
+// Up to 16 rows: one wave's worth, so the 4 waves of a workgroup take tiles in
+// turn, each its own in LDS without a barrier, and their sums are joined in LDS.
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
+    constexpr int RW = 16;
+    constexpr int KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
+    typedef Tile<E, F8, D, KEYS, 64> TL;
+    typedef Attend<E, F8, D, KEYS, RW> AT;
+    constexpr int O_FLOATS = RW * (D + 4);
+    constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : O_FLOATS * 4;
+
+    __shared__ __align__(16) char lds[4 * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
+    __shared__ float lm[4 * RW], ll[4 * RW];
+
+    Share share = share_of(a);
+    const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
+    if ((int)blockIdx.x >= groups) return;
+    const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char *mine = lds + wave * WAVE_BYTES;
+    TL tl(a, threadIdx.x & 63);
+    AT at(a);
+
+    for (int u = begin; u < end;) {
+        const Piece pc = piece_at(a, share, u, end);
+        const Seq sq = seq_of(a, pc.b);
+        const int R = sq.T * a.group, to = min(pc.to, sq.total);
+        tl.aim(pc.b, pc.h, sq);
+        int key0 = pc.from + KEYS * wave;
+        if (key0 < to) tl.load(key0);
+        at.begin(sq, pc.h, 0);
+        if (u != begin) __syncthreads();  // the piece before has been joined
+        for (; key0 < to; key0 += 4 * KEYS) {
+            const bool odd = tl.store(mine, key0);
+            const int next = key0 + 4 * KEYS;
+            if (next < to) tl.load(next);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            at.tile(mine, key0, sq.len);
+            if (__any(odd)) at.odd_values(pc.b, pc.h, sq, key0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        at.end();
+
+        // Join the waves.
+        float *lo = reinterpret_cast<float *>(mine);
+#pragma unroll
+        for (int d = 0; d < AT::ND; ++d) *reinterpret_cast<v4f *>(lo + at.n * (D + 4) + d * RW + 4 * at.g) = at.o[d];
+        if (at.g == 0) {
+            lm[wave * RW + at.n] = at.m;
+            ll[wave * RW + at.n] = at.l;
+        }
+        __syncthreads();
+        const int row = threadIdx.x >> 4, jt = threadIdx.x & 15;  // 16 threads to a row
+        if (row < R) {
+            float mm = M_START;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mm = fmaxf(mm, lm[row + k * RW]);
+            float f[4], sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f[k] = __builtin_amdgcn_exp2f(lm[row + k * RW] - mm);
+                sum += f[k] * ll[row + k * RW];
+            }
+            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + row;
+            const float norm = pc.whole ? (sum == 0.f ? 0.f : a.v_scale / sum) : 1.f;
+            const int64_t o_row =
+                (int64_t)(sq.first + row / a.group) * ((int64_t)heads * a.group) + pc.h * a.group + row % a.group;
+#pragma unroll
+            for (int v = 0; v < D; v += 64) {
+                const int dim = v + jt * 4;
+                v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc += f[k] * *reinterpret_cast<const v4f *>(lds + k * WAVE_BYTES + (row * (D + 4) + dim) * 4);
+                put4<E>(a, pc.whole, acc * norm, o_row * D + dim, slot_row * D + dim);
+            }
+            if (!pc.whole && jt == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{mm, sum};
+        }
+        u += pc.units;
+    }
+}
+
+// More rows: WAVES waves of RW rows share the tiles (two in LDS: one in use, one
+// being written; the registers hold the one after), so memory is read once for
+// all the rows of the workgroup.
+template <class E, bool F8, int D, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs a) {
+    constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
+    typedef Tile<E, F8, D, KEYS, WAVES * 64> TL;
+    typedef Attend<E, F8, D, KEYS, RW> AT;
+
+    __shared__ __align__(16) char lds[2 * TL::BYTES];
     __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
 
     Share share = share_of(a);
@@ -632,200 +673,48 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs
     if ((int)blockIdx.x >= groups) return;
     const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
 
-    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & (RW - 1), g = lane / RW;
-    const int G = a.group;
-    const int page_shift = a.cache.page_shift, page_mask = (1 << page_shift) - 1;
-    const int64_t head_bytes = (int64_t)D * ES << page_shift;
-    // staging: piece threadIdx.x (+ i * THREADS) of the keys and of the values
-    const int k_row = threadIdx.x / TL::KP, k_piece = threadIdx.x % TL::KP;
-    const int v_row = threadIdx.x / TL::VP, v_piece = threadIdx.x % TL::VP;
-    const int v_run = v_piece * (16 / ES) >> 4;
-    const int v_off = (v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1));
-    const bool stages = TL::PIECES >= TL::THREADS || (int)threadIdx.x < TL::PIECES;
-    // where this lane reads: its row of the first product's results (see the head
-    // of the file) and of the second's, 8 values from an even or odd half piece
-    const int krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
-    auto k_frag = [&](const char *at, int t, int kk) {
-        const int key = RW == 16 ? krow + 32 * (t >> 1) + 4 * (t & 1) : krow + 32 * t;
-        const int half = NG * kk + g;  // in units of 8 values
-        return *reinterpret_cast<const raw_t *>(at + TL::k_pos(key, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
-    };
-    auto v_frag = [&](const char *at, int d, int s) {
-        const int half = NG * s + g;
-        return *reinterpret_cast<const raw_t *>(at + TL::v_pos(RW * d + n, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
-    };
+    TL tl(a, threadIdx.x);
+    AT at(a);
     if (threadIdx.x == 0) odd = 0;
 
     for (int u = begin; u < end;) {
         const Piece pc = piece_at(a, share, u, end);
-        const int h = pc.h;
         const Seq sq = seq_of(a, pc.b);
-        const int len = sq.len, total = sq.total, R = sq.T * G, to = min(pc.to, total);
-        const int row = pc.rb * a.rows_wg + wave * RW + n;
-        const bool used = row < R;
-        const int tok = used ? row / G : 0;
-        const int64_t q_row = (int64_t)(sq.first + tok) * ((int64_t)heads * G) + h * G + (used ? row % G : 0);
-
-        op_t qf[NK];
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk) {
-            v4u w = {0u, 0u, 0u, 0u};
-            if (used)
-                w = (*reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (NG * kk + g)) * 2) & a.q_keep) ^ a.q_flip;
-            qf[kk] = __builtin_bit_cast(op_t, w);
-        }
-        uint64_t sees = 0;
-        if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(total - len);
-
-        const int last_run = (total - 1) & ~15;
-        v4u stage[2 * TL::N];
-        auto run_at = [&](int slot) { return ((int64_t)slot_page(a.cache, a.batch, pc.b, slot) * heads + h) * head_bytes; };
-        auto load = [&](int key0) {
-            if (!stages) return;
-#pragma unroll
-            for (int i = 0; i < TL::N; ++i) {  // a wave's pieces lie in one run of 16 slots (from a multiple of 16)
-                const int run = __builtin_amdgcn_readfirstlane((k_row + i * (TL::THREADS / TL::KP)) & ~15);
-                const int slot = min(key0 + run, last_run);  // (a run past the end: the last one again, masked)
-                const char *p = a.cache.k + run_at(slot) + (slot & page_mask) * TL::KB;
-                stage[i] = *reinterpret_cast<const v4u *>(p + ((k_row + i * (TL::THREADS / TL::KP)) & 15) * TL::KB + k_piece * 16);
-            }
-            int64_t at = 0;
-#pragma unroll
-            for (int r = 0; r < KEYS / 16; ++r) {
-                const int slot = min(key0 + 16 * r, last_run);
-                const int64_t o = run_at(slot) + (slot & page_mask) * ES;
-                at = r == v_run ? o : at;
-            }
-            const char *p = a.cache.v + at + v_off;
-#pragma unroll
-            for (int i = 0; i < TL::N; ++i)
-                stage[TL::N + i] = *reinterpret_cast<const v4u *>(p + (i * (TL::THREADS / TL::VP) << page_shift) * ES);
-        };
-        auto store = [&](char *to_lds, int key0) {
-            if (!stages) return;
-            if (key0 + KEYS > len) {
-                // slots past the end hold anything: zeros; infinite and NaN values of
-                // drafted tokens: zeros here, and noted
-                const int left = total - (key0 + v_piece * (16 / ES));
-                bool found = false;
-#pragma unroll
-                for (int i = 0; i < TL::N; ++i) {
-                    v4u &r = stage[TL::N + i];
-                    if constexpr (F8) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            raw_t half = {r[2 * j], r[2 * j + 1]};
-                            FR::first(half, min(max(left - 8 * j, 0), 8));
-                            found |= FR::drop_odd(half);
-                            r[2 * j] = half[0];
-                            r[2 * j + 1] = half[1];
-                        }
-                    } else {
-                        FR::first(r, min(max(left, 0), 8));
-                        found |= FR::drop_odd(r);
-                    }
-                }
-                if (found) odd = 1;
-            }
-#pragma unroll
-            for (int i = 0; i < TL::N; ++i) {
-                *reinterpret_cast<v4u *>(to_lds + TL::k_pos(k_row + i * (TL::THREADS / TL::KP), k_piece)) = stage[i];
-                *reinterpret_cast<v4u *>(to_lds + TL::v_pos(v_row + i * (TL::THREADS / TL::VP), v_piece)) = stage[TL::N + i];
-            }
-        };
-
-        acc_t o[ND];
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] = acc_t{};
-        float m = M_START, l = 0.f;
-
-        load(pc.from);
+        const int to = min(pc.to, sq.total);
+        tl.aim(pc.b, pc.h, sq);
+        tl.load(pc.from);
+        at.begin(sq, pc.h, pc.rb * a.rows_wg + wave * RW);
         __syncthreads();  // the piece before has been read
-        store(tile, pc.from);
-        load(pc.from + KEYS);
+        if (tl.store(lds, pc.from)) odd = 1;
+        tl.load(pc.from + KEYS);
         int second = 0;
         for (int key0 = pc.from; key0 < to; key0 += KEYS) {
             __syncthreads();
-            const char *at = tile + second * TL::BYTES;
-            acc_t sc[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                sc[t] = acc_t{};
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) sc[t] = MM::mul(FR::template op<op_t>(k_frag(at, t, kk)), qf[kk], sc[t]);
-            }
-            // p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's row
-            float p[NT * NR];
-#pragma unroll
-            for (int r = 0; r < NT * NR; ++r) p[r] = sc[r / NR][r % NR];
-            const bool ragged = key0 + KEYS > len;
-            if (ragged) {
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    const uint32_t on = seen8(sees, key0 + 8 * NG * s + 8 * g - len);
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
-                }
-            }
-            float top = p[0];
-#pragma unroll
-            for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
-            top *= a.score_scale;
-            if (__any(top > m + M_SLACK)) {
-#pragma unroll
-                for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-                const float up = fmaxf(m, top);
-                const float f = __builtin_amdgcn_exp2f(m - up);
-                m = up;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] *= f;
-            }
-            op_t pf[NS];
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                v4u w;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], a.score_scale, -m));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], a.score_scale, -m));
-                    l += p0 + p1;
-                    w[j] = pack2<E>(p0, p1);
-                }
-                pf[s] = __builtin_bit_cast(op_t, w);
-            }
-#pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(v_frag(at, d, s)), pf[s], o[d]);
-            if (ragged && odd) {
-#pragma nounroll
-                for (int s = 0; s < NS; ++s)
-                    add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, pc.b, h, len, total}, key0 + 8 * NG * s, lane, sees, o);
+            at.tile(lds + second * TL::BYTES, key0, sq.len);
+            if (key0 + KEYS > sq.len) {
+                if (odd) at.odd_values(pc.b, pc.h, sq, key0);
             }
             second ^= 1;
             if (key0 + KEYS < to) {
-                store(tile + second * TL::BYTES, key0 + KEYS);
-                load(key0 + 2 * KEYS);
+                if (tl.store(lds + second * TL::BYTES, key0 + KEYS)) odd = 1;
+                tl.load(key0 + 2 * KEYS);
             }
         }
+        at.end();
 
+        if (at.used) {
+            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + wave * RW + at.n;
+            const float norm = pc.whole ? (at.l == 0.f ? 0.f : a.v_scale / at.l) : 1.f;
 #pragma unroll
-        for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
-        if (used) {
-            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + wave * RW + n;
-            const float norm = pc.whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
+            for (int d = 0; d < AT::ND; ++d)
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < NR; r += 4) {
-                    const int dim = RW * d + 2 * r + 4 * g;
-                    put4<E>(a, pc.whole, v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * norm, q_row * D + dim,
-                            slot_row * D + dim);
+                for (int r = 0; r < AT::NR; r += 4) {
+                    const int dim = RW * d + 2 * r + 4 * at.g;
+                    put4<E>(a, pc.whole, v4f{at.o[d][r], at.o[d][r + 1], at.o[d][r + 2], at.o[d][r + 3]} * norm,
+                            at.q_row * D + dim, slot_row * D + dim);
                 }
-            if (!pc.whole && g == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{m, l};
+            if (!pc.whole && at.g == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{at.m, at.l};
         }
         u += pc.units;
     }
