@@ -250,8 +250,20 @@ __device__ __forceinline__ Share share_of(const AttnArgs &a) {
     }
     return s;
 }
-// The run of workgroup w of `groups` (at least as many units as groups).
-__device__ __forceinline__ int run_begin(int w, int groups, int units) { return (int)((int64_t)w * units / groups); }
+// Equal runs of `units` for `groups` workgroups (at least as many units as groups):
+// the first `more` have one unit more than the others.
+struct Runs {
+    int size, more;
+    __device__ __forceinline__ Runs(int units, int groups) {
+        size = units / groups;
+        more = units - size * groups;
+    }
+    __device__ __forceinline__ int begin(int w) const { return w * size + min(w, more); }
+    __device__ __forceinline__ int holder(int u) const {  // the workgroup that has unit u
+        const int longer = more * (size + 1);
+        return u < longer ? u / (size + 1) : more + (u - longer) / size;
+    }
+};
 
 // One block's share of a run: keys [from, to) of a row block of a head; `whole`
 // if that is all of its keys, else the workspace slot of its sums.
@@ -341,10 +353,13 @@ __device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane,
 // quarter wave read 16 different rows, one cache access each (measured: 63
 // accesses to an 8-byte load of a wave, and 4 TB/s); staged, the lanes of a load
 // read whole runs of rows.
+// ONCE: the keys are read by this workgroup alone, and pass the caches by, which
+// leaves these to the values, whose lines (one feature of a page) several waves
+// share: 257 -> 234 us for 1.4 GB; the values too: up to 291 us.
 // LDS holds 16-byte pieces; a row's pieces are permuted by an XOR with bits of
 // the row, so that the lanes of a read, which want one piece of many rows, meet
 // different banks.
-template <class E, bool F8, int D, int KEYS, int THREADS>
+template <class E, bool F8, int D, int KEYS, int RW, int THREADS, bool ONCE>
 struct Tile {
     typedef Frag<E, F8> FR;
     typedef typename FR::raw raw_t;
@@ -356,12 +371,16 @@ struct Tile {
     static constexpr int KSTEP = THREADS / KP, VSTEP = THREADS / VP;  // rows between a thread's loads
     static constexpr int K_BYTES = KEYS * KB, BYTES = 2 * K_BYTES;
 
+    // The 16 lanes that a read serves together are 0-3, 12-15, 20-23 and 24-27 of a
+    // half wave, or the others; the XORs give them 16 different places of 256 bytes.
     static __device__ __forceinline__ int k_pos(int key, int piece) {
-        const int f = KP >= 8 ? (key & 3) | ((key >> 1) & 4) : (key >> 1) & (KP - 1);
+        const int f = KP >= 16  ? (RW == 32 ? key & 15 : (key & 3) | ((key >> 1) & 12))
+                      : KP == 8 ? (RW == 32 ? (key >> 1) & 7 : ((key >> 1) & 1) | ((key >> 2) & 6))
+                                : (key >> 3) & 3;
         return key * KB + (piece ^ f) * 16;
     }
     static __device__ __forceinline__ int v_pos(int d, int piece) {
-        const int f = VP >= 8 ? d & 7 : VP == 4 ? (d >> 1) & 3 : (d >> 2) & 1;
+        const int f = VP >= 8 ? (d >> 1) & 7 : VP == 4 ? -(d >> 2) & 3 : (d >> 3) & 1;
         return K_BYTES + d * VB + (piece ^ f) * 16;
     }
 
@@ -404,7 +423,11 @@ struct Tile {
             const int run = __builtin_amdgcn_readfirstlane((k_row + i * KSTEP) & ~15);
             const int slot = min(key0 + run, last_run);
             const char *p = a.cache.k + page_of(slot) + (slot & page_mask) * KB;
-            stage[i] = *reinterpret_cast<const v4u *>(p + ((k_row + i * KSTEP) & 15) * KB + k_piece * 16);
+            const v4u *at = reinterpret_cast<const v4u *>(p + ((k_row + i * KSTEP) & 15) * KB + k_piece * 16);
+            if constexpr (ONCE)
+                stage[i] = __builtin_nontemporal_load(at);
+            else
+                stage[i] = *at;
         }
         int64_t at = 0;
 #pragma unroll
@@ -460,7 +483,7 @@ struct Attend {
     typedef typename MM::acc acc_t;
     typedef Frag<E, F8> FR;
     typedef typename FR::raw raw_t;
-    typedef Tile<E, F8, D, KEYS, 64> TL;           // (for the places in LDS alone)
+    typedef Tile<E, F8, D, KEYS, RW, 64, true> TL;  // (for the places in LDS alone)
     static constexpr int NG = 64 / RW;             // lane groups: 8 of a step's keys, 8 of a step's features to each
     static constexpr int NK = D / (8 * NG), ND = D / RW;         // steps of the first product, results of the second
     static constexpr int NT = KEYS / RW, NS = KEYS / (8 * NG);   // results of the first, steps of the second
@@ -524,9 +547,11 @@ struct Attend {
             for (int r = 0; r < NR; ++r) p[t * NR + r] = sc[r];
         }
         if (key0 + KEYS > len) {
+            int k0 = key0;
+            asm volatile("" : "+s"(k0));  // (the masks are not worked out ahead of this branch)
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                const uint32_t on = seen8(sees, key0 + 8 * NG * s + 8 * g - len);
+                const uint32_t on = seen8(sees, k0 + 8 * NG * s + 8 * g - len);
 #pragma unroll
                 for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
             }
@@ -579,7 +604,7 @@ template <class E, bool F8, int D>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
     constexpr int RW = 16;
     constexpr int KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
-    typedef Tile<E, F8, D, KEYS, 64> TL;
+    typedef Tile<E, F8, D, KEYS, RW, 64, true> TL;
     typedef Attend<E, F8, D, KEYS, RW> AT;
     constexpr int O_FLOATS = RW * (D + 4);
     constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : O_FLOATS * 4;
@@ -590,7 +615,8 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
     Share share = share_of(a);
     const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
     if ((int)blockIdx.x >= groups) return;
-    const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
+    const Runs runs(units, groups);
+    const int begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     char *mine = lds + wave * WAVE_BYTES;
@@ -662,7 +688,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
 template <class E, bool F8, int D, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs a) {
     constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
-    typedef Tile<E, F8, D, KEYS, WAVES * 64> TL;
+    typedef Tile<E, F8, D, KEYS, RW, WAVES * 64, WAVES == 4> TL;
     typedef Attend<E, F8, D, KEYS, RW> AT;
 
     __shared__ __align__(16) char lds[2 * TL::BYTES];
@@ -671,7 +697,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs
     Share share = share_of(a);
     const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
     if ((int)blockIdx.x >= groups) return;
-    const int begin = run_begin(blockIdx.x, groups, units), end = run_begin(blockIdx.x + 1, groups, units);
+    const Runs runs(units, groups);
+    const int begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     TL tl(a, threadIdx.x);
@@ -736,7 +763,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int ro
     const int i = tok - sq.first;
     if (i < 0 || i >= sq.T) return;
     const v4i sh = reinterpret_cast<const v4i *>(a.ws_seq)[b];  // units before, tiles, blocks, all units
-    const int units = sh[3] * heads, groups = min(a.grid, units), tiles = sh[1];
+    const int units = sh[3] * heads, tiles = sh[1];
+    const Runs runs(units, min(a.grid, units));
     int sets = 1;  // sets of threads to a row
     while (2 * sets * rows <= SETS) sets *= 2;
     const int lane = threadIdx.x % TPP, set = threadIdx.x / TPP, sub = set % sets;
@@ -745,13 +773,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int ro
         const int row = i * G + head0 % G + min(j, rows - 1), rb = row / a.rows_wg;
         const int from = heads * sh[0] + h * tiles * sh[2] + rb * tiles;
         // the workgroups that hold the block's first and last unit
-        const int w0 = (int)(((int64_t)(from + 1) * groups - 1) / units);
-        const int w1 = (int)(((int64_t)(from + tiles) * groups - 1) / units);
+        const int w0 = runs.holder(from), w1 = runs.holder(from + tiles - 1);
         float m = M_START, l = 0.f;
         v4f o = {0.f, 0.f, 0.f, 0.f};
         for (int w = w0 == w1 ? w1 + 1 : w0 + sub; w <= w1; w += sets) {  // (one workgroup: finished there)
             // a workgroup's first piece lies in its first slot
-            const int second = run_begin(w, groups, units) < from;
+            const int second = runs.begin(w) < from;
             const int64_t r = (2 * (int64_t)w + second) * a.slot_rows + (row - rb * a.rows_wg);
             const v2f ml = *reinterpret_cast<const v2f *>(a.ws_ml + 2 * r);
             const v4f po = *reinterpret_cast<const v4f *>(a.ws_o + r * D + 4 * lane);
