@@ -390,7 +390,9 @@ struct Tile {
     bool stages;
     int page_shift, page_mask;
     // the sequence and head
-    int b, h, len, total, last_run;
+    int b, h, len, total, last;  // last: a slot of the sequence's last run
+    // of the tile to load next: the pages of its runs of 16 slots
+    int key, pages[KEYS / 16];
     v4u stage[2 * N];
 
     __device__ __forceinline__ Tile(const AttnArgs &a_, int t_) : a(a_), t(t_) {
@@ -407,38 +409,61 @@ struct Tile {
         h = h_;
         len = q.len;
         total = q.total;
-        last_run = (total - 1) & ~15;
+        last = (total - 1) & ~15;
     }
-    // byte offset of the head's page of a slot
-    __device__ __forceinline__ int64_t page_of(int slot) const {
-        return ((int64_t)slot_page(a.cache, a.batch, b, slot) * a.cache.heads + h) * ((int64_t)D * ES << page_shift);
-    }
-    // Addresses: 16 consecutive slots from a multiple of 16 lie in one page, and a
-    // wave's load of keys in one such run, whose address is then a scalar; a run
-    // past the sequence's end is the last one again (masked later).
-    __device__ __forceinline__ void load(int key0) {
-        if (!stages) return;
+    // The pages of the tile from key0, a turn before its load needs them: 16
+    // consecutive slots from a multiple of 16 lie in one page, often the tile does.
+    // A run past the sequence's end is taken to be its last one (masked later).
+    __device__ __forceinline__ void find(int key0) {
+        key = key0;
+        pages[0] = slot_page(a.cache, a.batch, b, min(key0, last));
+        if ((1 << page_shift) < KEYS) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int run = __builtin_amdgcn_readfirstlane((k_row + i * KSTEP) & ~15);
-            const int slot = min(key0 + run, last_run);
-            const char *p = a.cache.k + page_of(slot) + (slot & page_mask) * KB;
-            const v4u *at = reinterpret_cast<const v4u *>(p + ((k_row + i * KSTEP) & 15) * KB + k_piece * 16);
-            if constexpr (ONCE)
-                stage[i] = __builtin_nontemporal_load(at);
-            else
-                stage[i] = *at;
+            for (int r = 1; r < KEYS / 16; ++r) pages[r] = slot_page(a.cache, a.batch, b, min(key0 + 16 * r, last));
         }
-        int64_t at = 0;
+    }
+    __device__ __forceinline__ int64_t page_at(int page) const {
+        return ((int64_t)page * a.cache.heads + h) * ((int64_t)D * ES << page_shift);
+    }
+    // That tile (to the registers).  A wave's load of keys lies in one run.
+    __device__ __forceinline__ void load() {
+        if (!stages) return;
+        if ((1 << page_shift) >= KEYS) {
+            const int slot = min(key, last & -KEYS) & page_mask;  // (pages are whole in memory, past the end too)
+            const int64_t at = page_at(pages[0]);
+            const char *pk = a.cache.k + at + slot * KB + t * 16;
+            const char *pv = a.cache.v + at + slot * ES + ((v_row << page_shift) * ES + v_piece * 16);
+#pragma unroll
+            for (int i = 0; i < N; ++i) get(stage[i], pk + i * (THREADS * 16));
+#pragma unroll
+            for (int i = 0; i < N; ++i) stage[N + i] = *reinterpret_cast<const v4u *>(pv + (i * VSTEP << page_shift) * ES);
+            return;
+        }
+        int64_t run_k[KEYS / 16], at_v = 0;
 #pragma unroll
         for (int r = 0; r < KEYS / 16; ++r) {
-            const int slot = min(key0 + 16 * r, last_run);
-            const int64_t o = page_of(slot) + (slot & page_mask) * ES;
-            at = r == v_piece * (16 / ES) >> 4 ? o : at;
+            const int64_t at = page_at(pages[r]);
+            const int in = min(key + 16 * r, last) & page_mask;
+            run_k[r] = at + in * KB;
+            at_v = r == v_piece * (16 / ES) >> 4 ? at + in * ES : at_v;
         }
-        const char *p = a.cache.v + at + ((v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1)));
 #pragma unroll
-        for (int i = 0; i < N; ++i) stage[N + i] = *reinterpret_cast<const v4u *>(p + (i * VSTEP << page_shift) * ES);
+        for (int i = 0; i < N; ++i) {
+            const int mine = __builtin_amdgcn_readfirstlane(k_row + i * KSTEP) >> 4;
+            int64_t at = run_k[0];
+#pragma unroll
+            for (int r = 1; r < KEYS / 16; ++r) at = r == mine ? run_k[r] : at;
+            get(stage[i], a.cache.k + at + (((k_row + i * KSTEP) & 15) * KB + k_piece * 16));
+        }
+        const char *pv = a.cache.v + at_v + ((v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1)));
+#pragma unroll
+        for (int i = 0; i < N; ++i) stage[N + i] = *reinterpret_cast<const v4u *>(pv + (i * VSTEP << page_shift) * ES);
+    }
+    static __device__ __forceinline__ void get(v4u &r, const char *p) {
+        if constexpr (ONCE)
+            r = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(p));
+        else
+            r = *reinterpret_cast<const v4u *>(p);
     }
     // To LDS.  In a tile that reaches past the cached slots: zeros for the values of
     // slots past the end, which may hold anything, and for infinite and NaN values
@@ -629,13 +654,17 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
         const int R = sq.T * a.group, to = min(pc.to, sq.total);
         tl.aim(pc.b, pc.h, sq);
         int key0 = pc.from + KEYS * wave;
-        if (key0 < to) tl.load(key0);
+        tl.find(key0);
+        tl.load();
+        tl.find(key0 + 4 * KEYS);
         at.begin(sq, pc.h, 0);
         if (u != begin) __syncthreads();  // the piece before has been joined
         for (; key0 < to; key0 += 4 * KEYS) {
             const bool odd = tl.store(mine, key0);
-            const int next = key0 + 4 * KEYS;
-            if (next < to) tl.load(next);
+            if (key0 + 4 * KEYS < to) {
+                tl.load();
+                tl.find(key0 + 8 * KEYS);
+            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             at.tile(mine, key0, sq.len);
             if (__any(odd)) at.odd_values(pc.b, pc.h, sq, key0);
@@ -710,11 +739,14 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs
         const Seq sq = seq_of(a, pc.b);
         const int to = min(pc.to, sq.total);
         tl.aim(pc.b, pc.h, sq);
-        tl.load(pc.from);
+        tl.find(pc.from);
+        tl.load();
+        tl.find(pc.from + KEYS);
         at.begin(sq, pc.h, pc.rb * a.rows_wg + wave * RW);
         __syncthreads();  // the piece before has been read
         if (tl.store(lds, pc.from)) odd = 1;
-        tl.load(pc.from + KEYS);
+        tl.load();
+        tl.find(pc.from + 2 * KEYS);
         int second = 0;
         for (int key0 = pc.from; key0 < to; key0 += KEYS) {
             __syncthreads();
@@ -725,7 +757,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs
             second ^= 1;
             if (key0 + KEYS < to) {
                 if (tl.store(lds + second * TL::BYTES, key0 + KEYS)) odd = 1;
-                tl.load(key0 + 2 * KEYS);
+                tl.load();
+                tl.find(key0 + 3 * KEYS);
             }
         }
         at.end();
