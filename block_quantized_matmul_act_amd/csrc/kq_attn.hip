@@ -39,6 +39,46 @@ constexpr float M_SLACK = 8.f;
 
 typedef float v2f __attribute__((ext_vector_type(2)));
 
+// A lane's value and that of the lane 32 (16) away, in both, in no order.
+__device__ __forceinline__ v2f across32(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return v2f{__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __forceinline__ v2f across16(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return v2f{__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+// Over the lane groups of RW lanes: the largest, the sum.
+template <int RW>
+__device__ __forceinline__ float groups_max(float x) {
+    v2f r = across32(x);
+    x = fmaxf(r[0], r[1]);
+    if constexpr (RW == 16) {
+        r = across16(x);
+        x = fmaxf(r[0], r[1]);
+    }
+    return x;
+}
+template <int RW>
+__device__ __forceinline__ float groups_sum(float x) {
+    v2f r = across32(x);
+    x = r[0] + r[1];
+    if constexpr (RW == 16) {
+        r = across16(x);
+        x = r[0] + r[1];
+    }
+    return x;
+}
+// A constant that stays where it is used (hoisted out of a path that is hardly
+// ever taken, it would cost the loops a register).
+__device__ __forceinline__ uint32_t here(uint32_t c) {
+    uint32_t r;
+    asm volatile("v_mov_b32 %0, %1" : "=v"(r) : "i"(c));
+    return r;
+}
+
 // 4 neighbouring sums: finished ones to the output, a part's to the workspace.
 template <class E>
 __device__ __forceinline__ void put4(const AttnArgs &a, bool whole, v4f x, int64_t out, int64_t slot) {
@@ -97,9 +137,18 @@ __device__ __forceinline__ uint32_t seen8(uint64_t sees, int node) {
     return node >= 0 ? drafted : both;
 }
 
-// Marks of infinite and NaN values: whole numbers that both 16-bit types hold,
-// set so far apart that sums of 32 do not run into the next.
-constexpr float MARK_POS = 1.f, MARK_NEG = 128.f, MARK_NAN = 16384.f;
+// Marks of infinite and NaN values: 1, 128 and 16384, whole numbers that both
+// 16-bit types hold, set so far apart that sums of 32 do not run into the next.
+template <class E>
+struct Marks {
+    uint32_t pos, neg, nan;
+    __device__ __forceinline__ Marks() {
+        constexpr bool bf = std::is_same_v<E, __bf16>;
+        pos = here(bf ? 0x3F80u : 0x3C00u);
+        neg = here(bf ? 0x4300u : 0x5800u);
+        nan = here(bf ? 0x4680u : 0x7400u);
+    }
+};
 
 // Eight cached values as they lie in memory, and as an operand.
 template <class E, bool F8>
@@ -128,11 +177,11 @@ struct Frag<E, false> {
         }
         return any;
     }
-    // a value's mark: see add_odd
-    static __device__ __forceinline__ float mark(raw r, int i) {
+    // value i's mark: see add_odd
+    static __device__ __forceinline__ uint32_t mark(raw r, int i, const Marks<E> &m) {
         constexpr uint32_t e = std::is_same_v<E, __bf16> ? 0x7F80u : 0x7C00u;
         const uint32_t x = r[i >> 1] >> (16 * (i & 1)) & 0xFFFFu;
-        return (x & 0x7FFFu) < e ? 0.f : (x & 0x7FFFu) > e ? MARK_NAN : x >> 15 ? MARK_NEG : MARK_POS;
+        return (x & 0x7FFFu) < e ? 0u : (x & 0x7FFFu) > e ? m.nan : x >> 15 ? m.neg : m.pos;
     }
     template <class OP>
     static __device__ __forceinline__ OP op(raw r) {
@@ -161,8 +210,8 @@ struct Frag<E, true> {
         }
         return any != 0;
     }
-    static __device__ __forceinline__ float mark(raw r, int i) {
-        return ((r[i >> 2] >> (8 * (i & 3))) & 0x7Fu) == 0x7Fu ? MARK_NAN : 0.f;
+    static __device__ __forceinline__ uint32_t mark(raw r, int i, const Marks<E> &m) {
+        return ((r[i >> 2] >> (8 * (i & 3))) & 0x7Fu) == 0x7Fu ? m.nan : 0u;
     }
     static __device__ __forceinline__ uint32_t pair(uint32_t r, bool hi) {
         if constexpr (std::is_same_v<E, __bf16>)
@@ -211,11 +260,12 @@ __device__ __forceinline__ void share_chunk(const AttnArgs &a, Share &s, int chu
         blocks = (q.T * a.group + a.rows_wg - 1) / a.rows_wg;
     }
     int incl = tiles * blocks;
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-        const int left = __shfl_up(incl, x);
-        incl += lane >= x ? left : 0;
-    }
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);  // in rows of 16: from 1, 2, 4, 8 to the left
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);  // lane 15 of rows 0 and 2 to rows 1 and 3
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);  // lane 31 to the upper half
     s.chunk = chunk;
     s.incl = incl;
     s.tiles = tiles;
@@ -317,10 +367,12 @@ __device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane,
     constexpr int ES = FR::BYTES;
     const int n = lane & (RW - 1), g = lane / RW;
     const int key = key0 + 8 * g;  // the first of this lane's 8
+    const Marks<E> marks;
+    const float inf = __builtin_bit_cast(float, here(0x7F800000u));
     const uint32_t on = seen8(sees, key - va.len);
     v4u w = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 1] |= (on >> e & 1u) * (pack2<E>(1.f, 0.f) << (16 * (e & 1)));
+    for (int e = 0; e < 8; ++e) w[e >> 1] |= (on >> e & 1u) * (marks.pos << (16 * (e & 1)));
     const typename MM::op seen = __builtin_bit_cast(typename MM::op, w);
     const int shift = va.cache.page_shift;
     const int slot = min(key & ~15, (va.total - 1) & ~15);
@@ -332,15 +384,15 @@ __device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane,
         typename FR::raw r = *reinterpret_cast<const typename FR::raw *>(p + ((d * RW + n) << shift) * ES);
         FR::first(r, min(max(va.total - key, 0), 8));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack2<E>(FR::mark(r, 2 * j), FR::mark(r, 2 * j + 1));
+        for (int j = 0; j < 4; ++j) w[j] = FR::mark(r, 2 * j, marks) | FR::mark(r, 2 * j + 1, marks) << 16;
         const typename MM::acc count =
             MM::mul(__builtin_bit_cast(typename MM::op, w), seen, typename MM::acc{});
 #pragma unroll
         for (int i = 0; i < RW * RW / 64; ++i) {
             const int c = (int)count[i];
-            float x = (c & 127) ? __builtin_inff() : 0.f;
-            x = c & (127 << 7) ? x - __builtin_inff() : x;
-            o[d][i] += c >> 14 ? __builtin_nanf("") : x;
+            float x = (c & 127) ? inf : 0.f;
+            x = c & (127 << 7) ? x - inf : x;
+            o[d][i] += c >> 14 ? inf - inf : x;
         }
         __builtin_amdgcn_sched_barrier(0);  // one at a time: this path must not cost the others registers
     }
@@ -373,26 +425,27 @@ struct Tile {
 
     // The 16 lanes that a read serves together are 0-3, 12-15, 20-23 and 24-27 of a
     // half wave, or the others; the XORs give them 16 different places of 256 bytes.
-    static __device__ __forceinline__ int k_pos(int key, int piece) {
-        const int f = KP >= 16  ? (RW == 32 ? key & 15 : (key & 3) | ((key >> 1) & 12))
-                      : KP == 8 ? (RW == 32 ? (key >> 1) & 7 : ((key >> 1) & 1) | ((key >> 2) & 6))
-                                : (key >> 3) & 3;
-        return key * KB + (piece ^ f) * 16;
+    // They take bits of the row, so the place of row x | y is that of x with a
+    // constant XORed and one added.
+    static __device__ __forceinline__ constexpr int k_xor(int key) {
+        return KP >= 16  ? (RW == 32 ? key & 15 : (key & 3) | ((key >> 1) & 12))
+               : KP == 8 ? (RW == 32 ? (key >> 1) & 7 : ((key >> 1) & 1) | ((key >> 2) & 6))
+                         : (key >> 3) & 3;
     }
-    static __device__ __forceinline__ int v_pos(int d, int piece) {
-        const int f = VP >= 8 ? (d >> 1) & 7 : VP == 4 ? -(d >> 2) & 3 : (d >> 3) & 1;
-        return K_BYTES + d * VB + (piece ^ f) * 16;
+    static __device__ __forceinline__ constexpr int v_xor(int d) {
+        return VP >= 8 ? (d >> 1) & 7 : VP == 4 ? -(d >> 2) & 3 : (d >> 3) & 1;
     }
+    static __device__ __forceinline__ int k_pos(int key, int piece) { return key * KB + (piece ^ k_xor(key)) * 16; }
+    static __device__ __forceinline__ int v_pos(int d, int piece) { return d * VB + (piece ^ v_xor(d)) * 16; }
 
     // A thread's part: piece t (+ i * THREADS) of the keys and of the values
     const AttnArgs &a;
     int t, k_row, k_piece, v_row, v_piece;
+    int k_to, v_to;  // places in a tile
     bool stages;
     int page_shift, page_mask;
     // the sequence and head
     int b, h, len, total, last;  // last: a slot of the sequence's last run
-    // of the tile to load next: the pages of its runs of 16 slots
-    int key, pages[KEYS / 16];
     v4u stage[2 * N];
 
     __device__ __forceinline__ Tile(const AttnArgs &a_, int t_) : a(a_), t(t_) {
@@ -400,6 +453,8 @@ struct Tile {
         k_piece = t % KP;
         v_row = t / VP;
         v_piece = t % VP;
+        k_to = k_pos(k_row, k_piece);
+        v_to = v_pos(v_row, v_piece);
         stages = PIECES >= THREADS || t < PIECES;
         page_shift = a.cache.page_shift;
         page_mask = (1 << page_shift) - 1;
@@ -411,53 +466,68 @@ struct Tile {
         total = q.total;
         last = (total - 1) & ~15;
     }
-    // The pages of the tile from key0, a turn before its load needs them: 16
-    // consecutive slots from a multiple of 16 lie in one page, often the tile does.
-    // A run past the sequence's end is taken to be its last one (masked later).
-    __device__ __forceinline__ void find(int key0) {
-        key = key0;
-        pages[0] = slot_page(a.cache, a.batch, b, min(key0, last));
+    // Where a tile lies: the pages of its runs of 16 slots, looked up a turn before
+    // the load needs them.  16 consecutive slots from a multiple of 16 lie in one
+    // page, often the tile does.  A run past the sequence's end is taken to be its
+    // last one (masked later).
+    struct Place {
+        int key, entries[KEYS / 16];  // of the page table as they are: nothing waits for them here
+    };
+    __device__ __forceinline__ Place find(int key0) const {
+        Place p;
+        p.key = key0;
+        p.entries[0] = slot_entry(a.cache, a.batch, b, min(key0, last));
         if ((1 << page_shift) < KEYS) {
 #pragma unroll
-            for (int r = 1; r < KEYS / 16; ++r) pages[r] = slot_page(a.cache, a.batch, b, min(key0 + 16 * r, last));
+            for (int r = 1; r < KEYS / 16; ++r) p.entries[r] = slot_entry(a.cache, a.batch, b, min(key0 + 16 * r, last));
         }
+        return p;
     }
-    __device__ __forceinline__ int64_t page_at(int page) const {
-        return ((int64_t)page * a.cache.heads + h) * ((int64_t)D * ES << page_shift);
+    __device__ __forceinline__ int64_t page_at(int entry) const {
+        return ((int64_t)page_inside(a.cache, entry) * a.cache.heads + h) * ((int64_t)D * ES << page_shift);
     }
-    // That tile (to the registers).  A wave's load of keys lies in one run.
-    __device__ __forceinline__ void load() {
+    // Its keys to the registers.  A wave's load lies in one run.
+    __device__ __forceinline__ void load_k(const Place &pl) {
         if (!stages) return;
         if ((1 << page_shift) >= KEYS) {
-            const int slot = min(key, last & -KEYS) & page_mask;  // (pages are whole in memory, past the end too)
-            const int64_t at = page_at(pages[0]);
-            const char *pk = a.cache.k + at + slot * KB + t * 16;
-            const char *pv = a.cache.v + at + slot * ES + ((v_row << page_shift) * ES + v_piece * 16);
+            // (pages are whole in memory, past the sequence's end too)
+            const char *p = a.cache.k + page_at(pl.entries[0]) + (min(pl.key, last & -KEYS) & page_mask) * KB + t * 16;
 #pragma unroll
-            for (int i = 0; i < N; ++i) get(stage[i], pk + i * (THREADS * 16));
-#pragma unroll
-            for (int i = 0; i < N; ++i) stage[N + i] = *reinterpret_cast<const v4u *>(pv + (i * VSTEP << page_shift) * ES);
+            for (int i = 0; i < N; ++i) get(stage[i], p + i * (THREADS * 16));
             return;
         }
-        int64_t run_k[KEYS / 16], at_v = 0;
+        int64_t run[KEYS / 16];
 #pragma unroll
-        for (int r = 0; r < KEYS / 16; ++r) {
-            const int64_t at = page_at(pages[r]);
-            const int in = min(key + 16 * r, last) & page_mask;
-            run_k[r] = at + in * KB;
-            at_v = r == v_piece * (16 / ES) >> 4 ? at + in * ES : at_v;
-        }
+        for (int r = 0; r < KEYS / 16; ++r) run[r] = page_at(pl.entries[r]) + (min(pl.key + 16 * r, last) & page_mask) * KB;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int mine = __builtin_amdgcn_readfirstlane(k_row + i * KSTEP) >> 4;
-            int64_t at = run_k[0];
+            int64_t at = run[0];
 #pragma unroll
-            for (int r = 1; r < KEYS / 16; ++r) at = r == mine ? run_k[r] : at;
+            for (int r = 1; r < KEYS / 16; ++r) at = r == mine ? run[r] : at;
             get(stage[i], a.cache.k + at + (((k_row + i * KSTEP) & 15) * KB + k_piece * 16));
         }
-        const char *pv = a.cache.v + at_v + ((v_row << page_shift) * ES + (v_piece * 16 & (16 * ES - 1)));
+    }
+    // Its values.
+    __device__ __forceinline__ void load_v(const Place &pl) {
+        if (!stages) return;
+        const char *p = a.cache.v + (v_row << page_shift) * ES;
+        if ((1 << page_shift) >= KEYS) {
+            p += page_at(pl.entries[0]) + (min(pl.key, last & -KEYS) & page_mask) * ES + v_piece * 16;
+        } else {
+            int64_t at = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) stage[N + i] = *reinterpret_cast<const v4u *>(pv + (i * VSTEP << page_shift) * ES);
+            for (int r = 0; r < KEYS / 16; ++r) {
+                const int64_t o = page_at(pl.entries[r]) + (min(pl.key + 16 * r, last) & page_mask) * ES;
+                at = r == v_piece * (16 / ES) >> 4 ? o : at;
+            }
+            p += at + (v_piece * 16 & (16 * ES - 1));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            stage[N + i] = *reinterpret_cast<const v4u *>(p);
+            p += VSTEP * ES << page_shift;
+        }
     }
     static __device__ __forceinline__ void get(v4u &r, const char *p) {
         if constexpr (ONCE)
@@ -465,10 +535,17 @@ struct Tile {
         else
             r = *reinterpret_cast<const v4u *>(p);
     }
-    // To LDS.  In a tile that reaches past the cached slots: zeros for the values of
+    // The keys to LDS (the tile at byte `buf`, a multiple of 1024).
+    __device__ __forceinline__ void store_k(char *lds, int buf) const {
+        if (!stages) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<v4u *>(lds + ((k_to + buf) ^ (k_xor(i * KSTEP) * 16)) + i * KSTEP * KB) = stage[i];
+    }
+    // The values to LDS.  In a tile that reaches past the cached slots: zeros for
     // slots past the end, which may hold anything, and for infinite and NaN values
     // of drafted tokens; whether this thread met any of those.
-    __device__ __forceinline__ bool store(char *lds, int key0) {
+    __device__ __forceinline__ bool store_v(char *lds, int buf, int key0) {
         bool found = false;
         if (!stages) return false;
         if (key0 + KEYS > len) {
@@ -492,10 +569,8 @@ struct Tile {
             }
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            *reinterpret_cast<v4u *>(lds + k_pos(k_row + i * KSTEP, k_piece)) = stage[i];
-            *reinterpret_cast<v4u *>(lds + v_pos(v_row + i * VSTEP, v_piece)) = stage[N + i];
-        }
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<v4u *>(lds + ((v_to + buf) ^ (v_xor(i * VSTEP) * 16)) + i * VSTEP * VB) = stage[N + i];
         return found;
     }
 };
@@ -515,7 +590,8 @@ struct Attend {
     static constexpr int NR = RW * RW / 64;
 
     const AttnArgs &a;
-    int lane, n, g, krow;
+    int lane, n, g;
+    int k_from, v_from;  // places in a tile
     bool used;
     int64_t q_row;  // of q and out
     uint64_t sees;
@@ -528,17 +604,17 @@ struct Attend {
         n = lane & (RW - 1);
         g = lane / RW;
         // this lane's row of the first product's results: see the head of the file
-        krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+        const int krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+        k_from = TL::k_pos(krow, F8 ? g >> 1 : g) + (F8 ? 8 * (g & 1) : 0);
+        v_from = TL::v_pos(n, F8 ? g >> 1 : g) + (F8 ? 8 * (g & 1) : 0);
     }
-    // 8 values from an even or odd half piece
-    __device__ __forceinline__ raw_t k_frag(const char *at, int t, int kk) const {
-        const int key = RW == 16 ? krow + 32 * (t >> 1) + 4 * (t & 1) : krow + 32 * t;
-        const int half = NG * kk + g;
-        return *reinterpret_cast<const raw_t *>(at + TL::k_pos(key, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
+    // 8 values of this lane: row t (and step kk) of the keys, row d (step s) of the values
+    __device__ __forceinline__ raw_t k_frag(const char *lds, int at, int t, int kk) const {
+        const int row = RW == 16 ? 32 * (t >> 1) + 4 * (t & 1) : 32 * t;
+        return *reinterpret_cast<const raw_t *>(lds + (at ^ (kk * NG * 8 * FR::BYTES)) + row * TL::KB);
     }
-    __device__ __forceinline__ raw_t v_frag(const char *at, int d, int s) const {
-        const int half = NG * s + g;
-        return *reinterpret_cast<const raw_t *>(at + TL::v_pos(RW * d + n, F8 ? half >> 1 : half) + (F8 ? 8 * (half & 1) : 0));
+    __device__ __forceinline__ raw_t v_frag(const char *lds, int at, int d, int s) const {
+        return *reinterpret_cast<const raw_t *>(lds + (at ^ (s * NG * 8 * FR::BYTES)) + RW * d * TL::VB);
     }
     // begin rows row0 .. of key head h
     __device__ __forceinline__ void begin(const Seq &sq, int h, int row0) {
@@ -559,18 +635,51 @@ struct Attend {
         m = M_START;
         l = 0.f;
     }
-    // add the tile of keys from key0
-    __device__ __forceinline__ void tile(const char *at, int key0, int len) {
-        // p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's row
-        float p[NT * NR];
+    // Matrix products of one stream: with VALUES the probabilities pf times the values
+    // at byte v of the LDS are added to the sums, with SCORES p gets the scores of
+    // the keys at byte k; p[r]: key key0 + 8 NG (r / 8) + 8 g + r % 8 of this lane's
+    // row.  The operands are read AHEAD products before they are used (left to itself
+    // the compiler reads each right before its product, and waits for it).
+    template <bool VALUES, bool SCORES, int AHEAD>
+    __device__ __forceinline__ void products(const char *lds, int v, const op_t (&pf)[NS], int k, float (&p)[NT * NR]) {
+        constexpr int NV = VALUES ? NS * ND : 0, ALL = NV + (SCORES ? NT * NK : 0), RING = AHEAD + 2;
+        const int from_v = v_from + v, from_k = k_from + k;
+        raw_t ring[RING];
+        acc_t sc[NT];
+        auto read = [&](auto X) {
+            constexpr int x = decltype(X)::value;
+            if constexpr (x < NV)
+                ring[x % RING] = v_frag(lds, from_v, x % ND, x / ND);
+            else if constexpr (x < ALL)
+                ring[x % RING] = k_frag(lds, from_k, (x - NV) % NT, (x - NV) / NT);
+        };
+        if constexpr (SCORES) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            acc_t sc = acc_t{};
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) sc = MM::mul(FR::template op<op_t>(k_frag(at, t, kk)), qf[kk], sc);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) p[t * NR + r] = sc[r];
+            for (int t = 0; t < NT; ++t) sc[t] = acc_t{};
         }
+        static_for<0, AHEAD>(read);
+        static_for<0, ALL / 2>([&](auto X) {
+            constexpr int x = 2 * decltype(X)::value;
+            read(IC<x + AHEAD>{});
+            read(IC<x + AHEAD + 1>{});
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<x, x + 2>([&](auto Y) {
+                constexpr int y = decltype(Y)::value;
+                const op_t w = FR::template op<op_t>(ring[y % RING]);
+                if constexpr (y < NV)
+                    o[y % ND] = MM::mul(w, pf[y / ND], o[y % ND]);
+                else
+                    sc[(y - NV) % NT] = MM::mul(w, qf[(y - NV) / NT], sc[(y - NV) % NT]);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (SCORES) {
+#pragma unroll
+            for (int r = 0; r < NT * NR; ++r) p[r] = sc[r / NR][r % NR];
+        }
+    }
+    // Masks the scores, and raises m and rescales the sums where it must.
+    __device__ __forceinline__ void raise(int key0, int len, float (&p)[NT * NR]) {
         if (key0 + KEYS > len) {
             int k0 = key0;
             asm volatile("" : "+s"(k0));  // (the masks are not worked out ahead of this branch)
@@ -586,8 +695,7 @@ struct Attend {
         for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
         top *= a.score_scale;
         if (__any(top > m + M_SLACK)) {
-#pragma unroll
-            for (int x = RW; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+            top = groups_max<RW>(top);
             const float up = fmaxf(m, top);
             const float f = __builtin_amdgcn_exp2f(m - up);
             m = up;
@@ -595,46 +703,69 @@ struct Attend {
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] *= f;
         }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            v4u w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], a.score_scale, -m));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], a.score_scale, -m));
-                l += p0 + p1;
-                w[j] = pack2<E>(p0, p1);
-            }
-            const op_t pf = __builtin_bit_cast(op_t, w);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] = MM::mul(FR::template op<op_t>(v_frag(at, d, s)), pf, o[d]);
-        }
     }
-    // what infinite and NaN values of the tile's drafted tokens add
-    __device__ __forceinline__ void odd_values(int b, int h, const Seq &sq, int key0) {
+    // The probabilities of step s of the second product.
+    __device__ __forceinline__ op_t probabilities(const float (&p)[NT * NR], int s) {
+        v4u w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], a.score_scale, -m));
+            const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], a.score_scale, -m));
+            l += p0 + p1;
+            w[j] = pack2<E>(p0, p1);
+        }
+        return __builtin_bit_cast(op_t, w);
+    }
+    __device__ __forceinline__ void tile(const char *lds, int buf, int key0, int len) {
+        float p[NT * NR];
+        op_t pf[NS];
+        products<false, true, 4>(lds, 0, pf, buf, p);
+        raise(key0, len, p);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) pf[s] = probabilities(p, s);
+        products<true, false, 4>(lds, buf + TL::K_BYTES, pf, 0, p);
+    }
+    // What infinite and NaN values of drafted tokens among keys [from, to) add; at a
+    // piece's end, where the loop's registers are free.
+    __device__ __forceinline__ void odd_values(int b, int h, const Seq &sq, int from, int to) {
 #pragma nounroll
-        for (int s = 0; s < NS; ++s)
-            add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, sq.len, sq.total}, key0 + 8 * NG * s, lane, sees, o);
+        for (int key = max(from, sq.len & -KEYS); key < to; key += 8 * NG)
+            add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, sq.len, sq.total}, key, lane, sees, o);
     }
     // the whole rows' weights (the lane groups hold parts of them)
     __device__ __forceinline__ void end() {
+        l = groups_sum<RW>(l);
+    }
+    // end, and the rows to the output or to the workspace from row slot_row
+    __device__ __forceinline__ void put(bool whole, int64_t slot_row) {
+        end();
+        if (!used) return;
+        slot_row += n;
+        const float norm = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
 #pragma unroll
-        for (int x = RW; x < 64; x <<= 1) l += __shfl_xor(l, x);
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < NR; r += 4) {
+                const int dim = RW * d + 2 * r + 4 * g;
+                put4<E>(a, whole, v4f{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * norm, q_row * D + dim,
+                        slot_row * D + dim);
+            }
+        if (!whole && g == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{m, l};
     }
 };
 
 // Up to 16 rows: one wave's worth, so the 4 waves of a workgroup take tiles in
 // turn, each its own in LDS without a barrier, and their sums are joined in LDS.
 template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const AttnArgs a) {
     constexpr int RW = 16;
     constexpr int KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
     typedef Tile<E, F8, D, KEYS, RW, 64, true> TL;
     typedef Attend<E, F8, D, KEYS, RW> AT;
     constexpr int O_FLOATS = RW * (D + 4);
-    constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : O_FLOATS * 4;
+    constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : (O_FLOATS * 4 + 1023) / 1024 * 1024;
 
-    __shared__ __align__(16) char lds[4 * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
+    __shared__ __align__(1024) char lds[4 * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
     __shared__ float lm[4 * RW], ll[4 * RW];
 
     Share share = share_of(a);
@@ -644,7 +775,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
     const int begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    char *mine = lds + wave * WAVE_BYTES;
+    const int mine = wave * WAVE_BYTES;
     TL tl(a, threadIdx.x & 63);
     AT at(a);
 
@@ -654,26 +785,33 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
         const int R = sq.T * a.group, to = min(pc.to, sq.total);
         tl.aim(pc.b, pc.h, sq);
         int key0 = pc.from + KEYS * wave;
-        tl.find(key0);
-        tl.load();
-        tl.find(key0 + 4 * KEYS);
+        typename TL::Place next = tl.find(key0);
+        tl.load_k(next);
+        tl.load_v(next);
+        next = tl.find(key0 + 4 * KEYS);
         at.begin(sq, pc.h, 0);
         if (u != begin) __syncthreads();  // the piece before has been joined
+        bool odd = false;
         for (; key0 < to; key0 += 4 * KEYS) {
-            const bool odd = tl.store(mine, key0);
+            tl.store_k(lds, mine);
+            odd |= tl.store_v(lds, mine + TL::K_BYTES, key0);
             if (key0 + 4 * KEYS < to) {
-                tl.load();
-                tl.find(key0 + 8 * KEYS);
+                tl.load_k(next);
+                tl.load_v(next);
+                next = tl.find(key0 + 8 * KEYS);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            at.tile(mine, key0, sq.len);
-            if (__any(odd)) at.odd_values(pc.b, pc.h, sq, key0);
+            at.tile(lds, mine, key0, sq.len);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        if (__any(odd)) {
+            for (key0 = pc.from + KEYS * wave; key0 < to; key0 += 4 * KEYS)
+                at.odd_values(pc.b, pc.h, sq, key0, min(key0 + KEYS, to));
         }
         at.end();
 
         // Join the waves.
-        float *lo = reinterpret_cast<float *>(mine);
+        float *lo = reinterpret_cast<float *>(lds + mine);
 #pragma unroll
         for (int d = 0; d < AT::ND; ++d) *reinterpret_cast<v4f *>(lo + at.n * (D + 4) + d * RW + 4 * at.g) = at.o[d];
         if (at.g == 0) {
@@ -711,16 +849,16 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs a) {
     }
 }
 
-// More rows: WAVES waves of RW rows share the tiles (two in LDS: one in use, one
-// being written; the registers hold the one after), so memory is read once for
-// all the rows of the workgroup.
-template <class E, bool F8, int D, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs a) {
-    constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
-    typedef Tile<E, F8, D, KEYS, RW, WAVES * 64, WAVES == 4> TL;
+// More rows, up to 4 waves' worth: the waves share the tiles (two in LDS: one in
+// use, one being written; the registers hold the one after), so memory is read
+// once for all the rows.
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
+    constexpr int RW = 32, KEYS = D == 128 ? 32 : 64;  // (64 at dim 128 would not fit the registers)
+    typedef Tile<E, F8, D, KEYS, RW, 256, true> TL;
     typedef Attend<E, F8, D, KEYS, RW> AT;
 
-    __shared__ __align__(16) char lds[2 * TL::BYTES];
+    __shared__ __align__(1024) char lds[2 * TL::BYTES];
     __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
 
     Share share = share_of(a);
@@ -739,43 +877,127 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_tile_kernel(const AttnArgs
         const Seq sq = seq_of(a, pc.b);
         const int to = min(pc.to, sq.total);
         tl.aim(pc.b, pc.h, sq);
-        tl.find(pc.from);
-        tl.load();
-        tl.find(pc.from + KEYS);
+        typename TL::Place next = tl.find(pc.from);
+        tl.load_k(next);
+        tl.load_v(next);
+        next = tl.find(pc.from + KEYS);
         at.begin(sq, pc.h, pc.rb * a.rows_wg + wave * RW);
         __syncthreads();  // the piece before has been read
-        if (tl.store(lds, pc.from)) odd = 1;
-        tl.load();
-        tl.find(pc.from + 2 * KEYS);
-        int second = 0;
+        tl.store_k(lds, 0);
+        if (tl.store_v(lds, TL::K_BYTES, pc.from)) odd = 1;
+        tl.load_k(next);
+        tl.load_v(next);
+        next = tl.find(pc.from + 2 * KEYS);
+        int buf = 0;
         for (int key0 = pc.from; key0 < to; key0 += KEYS) {
             __syncthreads();
-            at.tile(lds + second * TL::BYTES, key0, sq.len);
-            if (key0 + KEYS > sq.len) {
-                if (odd) at.odd_values(pc.b, pc.h, sq, key0);
-            }
-            second ^= 1;
+            at.tile(lds, buf, key0, sq.len);
+            buf = TL::BYTES - buf;
             if (key0 + KEYS < to) {
-                if (tl.store(lds + second * TL::BYTES, key0 + KEYS)) odd = 1;
-                tl.load();
-                tl.find(key0 + 3 * KEYS);
+                tl.store_k(lds, buf);
+                if (tl.store_v(lds, buf + TL::K_BYTES, key0 + KEYS)) odd = 1;
+                tl.load_k(next);
+                tl.load_v(next);
+                next = tl.find(key0 + 3 * KEYS);
             }
         }
-        at.end();
+        if (odd) at.odd_values(pc.b, pc.h, sq, pc.from, to);
+        at.put(pc.whole, (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + wave * RW);
+        u += pc.units;
+    }
+}
 
-        if (at.used) {
-            const int64_t slot_row = (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + wave * RW + at.n;
-            const float norm = pc.whole ? (at.l == 0.f ? 0.f : a.v_scale / at.l) : 1.f;
+// Still more rows: 8 waves, two to a SIMD, share the tiles, and the second four
+// run half a turn behind the first.  A turn has a half of matrix products (the
+// values of the tile before, the scores of this one) and a half of vector work
+// (softmax, staging), as long as each other, so that one wave of a SIMD keeps its
+// matrix unit busy while the other has its vector unit; a barrier ends every half
+// (the later waves meet one more at the begin, the earlier ones at the end).
+// Times in halves: the early waves multiply tile i at 2 i, the late ones at 2 i + 1.
+// Each wave stages its share of keys i + 2 and values i + 1 after scores i, so
+// early or late they are in LDS by 2 i + 3, before anyone's products at 2 i + 4; what
+// they overwrite, keys i - 1 and values i - 2 (three of each in LDS), was last read at
+// 2 i - 1.
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs a) {
+    constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
+    typedef Tile<E, F8, D, KEYS, RW, 512, false> TL;
+    typedef Attend<E, F8, D, KEYS, RW> AT;
+
+    __shared__ __align__(1024) char lds[3 * TL::BYTES];  // keys and values by turns
+    __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
+
+    Share share = share_of(a);
+    const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
+    if ((int)blockIdx.x >= groups) return;
+    const Runs runs(units, groups);
+    const int begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool late = wave >= 4;
+    TL tl(a, threadIdx.x);
+    AT at(a);
+    if (threadIdx.x == 0) odd = 0;
+
+    for (int u = begin; u < end;) {
+        const Piece pc = piece_at(a, share, u, end);
+        const Seq sq = seq_of(a, pc.b);
+        const int to = min(pc.to, sq.total), tiles = (to - pc.from + KEYS - 1) / KEYS;
+        tl.aim(pc.b, pc.h, sq);
+        // keys 0, 1 and values 0 to LDS; keys 2 and values 1 on their way
+        typename TL::Place p0 = tl.find(pc.from), p1 = tl.find(pc.from + KEYS), p2 = tl.find(pc.from + 2 * KEYS);
+        tl.load_k(p0);
+        tl.load_v(p0);
+        at.begin(sq, pc.h, pc.rb * a.rows_wg + wave * RW);
+        __syncthreads();  // the piece before has been read
+        tl.store_k(lds, 0);
+        if (tl.store_v(lds, TL::K_BYTES, pc.from)) odd = 1;
+        tl.load_k(p1);
+        tl.store_k(lds, TL::BYTES);
+        tl.load_v(p1);
+        tl.load_k(p2);
+        p1 = p2;
+        p2 = tl.find(pc.from + 3 * KEYS);
+        float p[AT::NT * AT::NR];
+        typename AT::op_t pf[AT::NS];
+        int key0 = pc.from, buf = 0;  // buf: where tile i is (i % 3)
+        __syncthreads();
+        if (late) __syncthreads();
+        auto vector_half = [&](int i, int before, int after) {
+            at.raise(key0, sq.len, p);
 #pragma unroll
-            for (int d = 0; d < AT::ND; ++d)
-#pragma unroll
-                for (int r = 0; r < AT::NR; r += 4) {
-                    const int dim = RW * d + 2 * r + 4 * at.g;
-                    put4<E>(a, pc.whole, v4f{at.o[d][r], at.o[d][r + 1], at.o[d][r + 2], at.o[d][r + 3]} * norm,
-                            at.q_row * D + dim, slot_row * D + dim);
-                }
-            if (!pc.whole && at.g == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * slot_row) = v2f{at.m, at.l};
+            for (int s = 0; s < AT::NS; ++s) {
+                v4u w = __builtin_bit_cast(v4u, at.probabilities(p, s));
+                asm volatile("" : "+v"(w));  // (now, while the loads for the staging below arrive)
+                pf[s] = __builtin_bit_cast(typename AT::op_t, w);
+            }
+            if (i + 1 < tiles) {
+                tl.store_k(lds, before);  // keys i + 2
+                if (tl.store_v(lds, after + TL::K_BYTES, key0 + KEYS)) odd = 1;
+                tl.load_v(p1);
+                tl.load_k(p2);
+                p1 = p2;
+                p2 = tl.find(key0 + 4 * KEYS);
+            }
+        };
+        at.template products<false, true, 6>(lds, 0, pf, 0, p);
+        __syncthreads();
+        vector_half(0, 2 * TL::BYTES, TL::BYTES);
+        __syncthreads();
+        for (int i = 1; i < tiles; ++i) {
+            key0 += KEYS;
+            const int before = buf;
+            buf = buf == 2 * TL::BYTES ? 0 : buf + TL::BYTES;
+            at.template products<true, true, 6>(lds, before + TL::K_BYTES, pf, buf, p);
+            __syncthreads();
+            vector_half(i, before, buf == 2 * TL::BYTES ? 0 : buf + TL::BYTES);
+            __syncthreads();
         }
+        at.template products<true, false, 6>(lds, buf + TL::K_BYTES, pf, 0, p);
+        __syncthreads();
+        if (!late) __syncthreads();
+        if (odd) at.odd_values(pc.b, pc.h, sq, pc.from, to);
+        at.put(pc.whole, (2 * (int64_t)blockIdx.x + (u != begin)) * a.slot_rows + wave * RW);
         u += pc.units;
     }
 }
@@ -849,10 +1071,10 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) 
     const dim3 grid((unsigned)p.grid);
     if (p.waves == 0)
         hipLaunchKernelGGL((attn_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, a);
-    else if (p.waves == 4)
-        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D, 4>), grid, dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D, 8>), grid, dim3(512), 0, stream, a);
+    else if (p.waves == 8)
+        hipLaunchKernelGGL((attn_wide_kernel<E, F8, D>), grid, dim3(512), 0, stream, a);
+    else if constexpr (D < 256)
+        hipLaunchKernelGGL((attn_tile_kernel<E, F8, D>), grid, dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.bytes == 0) return e;  // no workspace: nothing is cut
     // many rows: the heads of a group together, which find their parts once

@@ -86,10 +86,11 @@ namespace kq {
 AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len) {
     AttnPlan p;
     // Waves of 32 rows, at dim 256 of 16 (whose sums and operands fit the
-    // registers); 8 of them where there are rows for more than 4.
+    // registers); 8 of them where there are rows for more than 4 (96 rows: 103 us
+    // with 4, 124 with 8), and at dim 256.
     const int64_t rows = max_tokens * group;
     const int rows_wave = dim == 256 ? 16 : 32;
-    p.waves = rows <= 16 ? 0 : rows <= 4 * rows_wave ? 4 : 8;
+    p.waves = rows <= 16 ? 0 : rows <= 4 * rows_wave && dim < 256 ? 4 : 8;
     p.rows_wg = p.waves ? p.waves * rows_wave : 16;
     p.row_blocks = (int)((rows + p.rows_wg - 1) / p.rows_wg);
     p.slot_rows = (int)std::min<int64_t>(rows, p.rows_wg);

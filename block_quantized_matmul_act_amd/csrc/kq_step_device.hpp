@@ -42,15 +42,21 @@ __device__ __forceinline__ void batch_rows(const BatchArgs &s, int b, int &first
     count = min(max(s.offsets[b + 1], first), s.n_tokens) - first;
 }
 
-// The page of slot `slot` of sequence b; a page outside the cache or a slot
-// past the table gives a wrong page, never one outside the cache.
+// The page of slot `slot` of sequence b: its entry in the table, held inside the
+// cache; a page outside the cache or a slot past the table gives a wrong page,
+// never one outside the cache.
 // The arrays of a step are read as constants: where b and slot are the same for
 // a wave, the load is a scalar one.
 typedef const int32_t __attribute__((address_space(4))) *const_ints;
-__device__ __forceinline__ int slot_page(const CacheArgs &c, const BatchArgs &s, int b, int slot) {
+__device__ __forceinline__ int slot_entry(const CacheArgs &c, const BatchArgs &s, int b, int slot) {
     const int col = min(max(slot, 0) >> c.page_shift, s.max_pages - 1);
-    const int page = ((const_ints)s.pages)[(int64_t)b * s.max_pages + col];
-    return (int)min((int64_t)max(page, 0), c.n_pages - 1);
+    return ((const_ints)s.pages)[(int64_t)b * s.max_pages + col];
+}
+__device__ __forceinline__ int page_inside(const CacheArgs &c, int entry) {
+    return (int)min((int64_t)max(entry, 0), c.n_pages - 1);
+}
+__device__ __forceinline__ int slot_page(const CacheArgs &c, const BatchArgs &s, int b, int slot) {
+    return page_inside(c, slot_entry(c, s, b, slot));
 }
 
 // The sequence of token row `row`, found by a whole wave together: the last b

@@ -95,7 +95,7 @@ int main() {
                             if (rc == KQ_ERR_UNSUPPORTED) continue;
                             EXPECT(rc == KQ_OK && attns == before + 1);
                             const int wave = dim == 256 ? 16 : 32;
-                            EXPECT(plan.waves == (T * G <= 16 ? 0 : T * G <= 4 * wave ? 4 : 8));
+                            EXPECT(plan.waves == (T * G <= 16 ? 0 : T * G <= 4 * wave && dim < 256 ? 4 : 8));
                             EXPECT(plan.rows_wg == (plan.waves ? plan.waves * wave : 16));
                             EXPECT((int64_t)plan.rows_wg * plan.row_blocks >= T * G);
                             EXPECT((int64_t)plan.rows_wg * (plan.row_blocks - 1) < T * G);
