@@ -348,54 +348,69 @@ def gemm_id(fmt, W, n_experts, a_q8, M, N, K, expert_offsets, rows, out=None, st
 
 
 # ------------------------------- the step between two products (cache, attention, answer)
+#
+# These calls are a few microseconds of GPU work where one token is decoded, so
+# their checks are written to cost little: a tensor that is as it should be takes
+# one test each of device, type, shape and layout, and the message is worked out
+# only for one that is not.
 
-_types = None
-
-
-def _type(t, where):
-    """KQ_T_* of a tensor's element type."""
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: KQ_T_F32, torch.bfloat16: KQ_T_BF16, torch.float16: KQ_T_F16,
-                  torch.float8_e4m3fn: KQ_T_F8}
-    kind = _types.get(t.dtype)
-    if kind is None:
-        raise ValueError(f"{where}: element type {t.dtype} not taken")
-    return kind
+_types = _current_stream = _step = None
 
 
-def _tensor(t, dtype, shape, where, contiguous=True):
-    """Check one tensor argument (None in a shape: any size); its pointer."""
+def _step_lib():
+    """The library's entry points of the step, and torch's types, once."""
+    global _types, _current_stream, _step
+    import torch
+    _types = {torch.float32: KQ_T_F32, torch.bfloat16: KQ_T_BF16, torch.float16: KQ_T_F16,
+              torch.float8_e4m3fn: KQ_T_F8}
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _step = lib()
+    return _step
+
+
+def _refuse(t, dtype, shape, device, where):
+    """Raise what is wrong with a tensor argument (None in a shape: any size)."""
     if not t.is_cuda:
         raise ValueError(f"{where}: expected a device tensor")
-    if dtype is not None and t.dtype is not dtype:
+    if t.get_device() != device:
+        raise ValueError(f"{where}: expected a tensor on device {device}, got {t.device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{where}: expected dtype {dtype}, got {t.dtype}")
-    have = t.shape
-    if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
-        raise ValueError(f"{where}: expected shape {shape}, got {tuple(have)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{where}: expected a contiguous tensor")
-    return t.data_ptr()
+    if t.dim() != len(shape) or any(n is not None and n != h for n, h in zip(shape, t.shape)):
+        raise ValueError(f"{where}: expected shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{where}: expected a contiguous tensor")
 
 
-def _rows(t, shape, where):
-    """Check a [rows][n] tensor whose rows may lie apart; (pointer, row stride)."""
-    p = _tensor(t, None, shape, where, contiguous=False)
+def _tensor(t, dtype, shape, device, where):
+    """The address of a tensor argument after its checks."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, device, where)
+
+
+def _rows(t, n, device, where):
+    """(address, row stride) of a [rows][n] tensor whose rows may lie apart."""
+    if device < 0:
+        raise ValueError(f"{where}: expected a device tensor")
+    if t.dim() != 2 or (n is not None and t.shape[1] != n):
+        raise ValueError(f"{where}: expected shape (None, {n}), got {tuple(t.shape)}")
     rows, n = t.shape
-    if n > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = max(n, 1)
+    if one != 1 and n > 1:
         raise ValueError(f"{where}: expected rows of neighbouring elements")
-    ld = t.stride(0) if rows > 1 else max(n, 1)
     if ld < n:
         raise ValueError(f"{where}: rows overlap (stride {ld}, {n} elements)")
-    return p, ld
+    return t.data_ptr(), ld
 
 
-def _same_device(first, others, where):
-    at = first.device
-    for t in others:
-        if t is not None and t.device != at:
-            raise ValueError(f"{where}: tensors on {at} and {t.device}")
+def _type(dtype, where):
+    kind = (_types or _step_lib() and _types).get(dtype)
+    if kind is None:
+        raise ValueError(f"{where}: element type {dtype} not taken")
+    return kind
 
 
 def _on(stream, device):
@@ -412,37 +427,46 @@ class PagedCache:
     """Keys [n_pages][heads][page][dim] and values [n_pages][heads][dim][page]
     of one layer (bfloat16, float16 or float8_e4m3fn device tensors); what is
     stored times k_scale / v_scale is the key / value."""
+    __slots__ = ("k", "v", "dtype", "device", "c", "at")
 
     def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
-        where = "PagedCache"
         if k.dim() != 4:
-            raise ValueError(f"{where} k: expected [n_pages][heads][page][dim], got {tuple(k.shape)}")
-        n, heads, page, dim = k.shape
+            raise ValueError(f"PagedCache k: expected [n_pages][heads][page][dim], got {tuple(k.shape)}")
+        n, heads, page, dim = shape = k.shape
         self.k, self.v, self.dtype = k, v, k.dtype
-        self.c = kq_cache(_tensor(k, None, (n, heads, page, dim), where + " k"),
-                          _tensor(v, k.dtype, (n, heads, dim, page), where + " v"), n, _type(k, where), heads, dim,
-                          page, k_scale, v_scale)
-        _same_device(k, (v,), where)
+        self.device = device = k.get_device()
+        pk, pv = k.data_ptr(), v.data_ptr()
+        if device < 0 or not k.is_contiguous():
+            _refuse(k, k.dtype, shape, device, "PagedCache k")
+        if v.dtype is not k.dtype or v.shape != (n, heads, dim, page) or v.get_device() != device or not v.is_contiguous():
+            _refuse(v, k.dtype, (n, heads, dim, page), device, "PagedCache v")
+        self.c = c = kq_cache(pk, pv, n, _type(k.dtype, "PagedCache k"), heads, dim, page, k_scale, v_scale)
+        self.at = ctypes.addressof(c)
 
 
 class Batch:
     """The sequences of one step (int32 device tensors): offsets [n_seqs + 1] of
     their token rows, lens [n_seqs] tokens already cached, pages [n_seqs][max_pages]."""
+    __slots__ = ("offsets", "lens", "pages", "device", "c", "at")
 
     def __init__(self, offsets, lens, pages):
         import torch
-        where, i32 = "Batch", torch.int32
-        n = lens.numel()
+        i32 = torch.int32
+        n = lens.shape[0]
+        wide = pages.shape[-1]
         self.offsets, self.lens, self.pages = offsets, lens, pages
-        self.c = kq_batch(_tensor(offsets, i32, (n + 1,), where + " offsets"), _tensor(lens, i32, (n,), where + " lens"),
-                          _tensor(pages, i32, (n, None), where + " pages"), n, 0, pages.shape[1])
-        _same_device(offsets, (lens, pages), where)
+        self.device = device = lens.get_device()
+        self.c = c = kq_batch(_tensor(offsets, i32, (n + 1,), device, "Batch offsets"),
+                              _tensor(lens, i32, (n,), device, "Batch lens"),
+                              _tensor(pages, i32, (n, wide), device, "Batch pages"), n, 0, wide)
+        self.at = ctypes.addressof(c)
+        if device < 0:
+            raise ValueError("Batch: expected device tensors")
 
-    def rows(self, n):
-        """The step's descriptor for n token rows (which the first tensor with a
-        row to each token tells: the offsets themselves stay on the device)."""
-        self.c.n_tokens = n
-        return self.c
+
+def _together(device, cache, batch, where):
+    if cache.device != device or batch.device != device:
+        raise ValueError(f"{where}: tensors on devices {device}, {cache.device} and {batch.device}")
 
 
 def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None, k_norm=None, eps=1e-6, pairs=False,
@@ -455,25 +479,32 @@ def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None
     if stream is not None:
         with _on(stream, x.device):
             return rope_append(cache, batch, x, q_heads, rope, positions, q_norm, k_norm, eps, pairs, q_dtype, out)
-    where, f32, c = "rope_append", torch.float32, cache.c
-    px, ldx = _rows(x, (None, (q_heads + 2 * c.heads) * c.dim), where + " x")
+    f32, c, device = torch.float32, cache.c, x.get_device()
+    heads, dim = c.heads, c.dim
+    px, ldx = _rows(x, (q_heads + 2 * heads) * dim, device, "rope_append x")
     if x.dtype is not f32:
-        raise ValueError(f"{where} x: expected dtype {f32}, got {x.dtype}")
+        _refuse(x, f32, x.shape, device, "rope_append x")
+    _together(device, cache, batch, "rope_append")
     M = x.shape[0]
-    if q_dtype is None:
-        q_dtype = out.dtype if out is not None else torch.bfloat16 if c.type == KQ_T_F8 else cache.dtype
     if out is None:
-        out = torch.empty((M, q_heads, c.dim), dtype=q_dtype, device=x.device)
-    pq = _tensor(out, q_dtype, (M, q_heads, c.dim), where + " out")
+        if q_dtype is None:
+            q_dtype = torch.bfloat16 if c.type == KQ_T_F8 else cache.dtype
+        out = torch.empty((M, q_heads, dim), dtype=q_dtype, device=x.device)
+        pq = out.data_ptr()
+    else:
+        q_dtype = q_dtype or out.dtype
+        pq = _tensor(out, q_dtype, (M, q_heads, dim), device, "rope_append out")
     pr, n_pos, rot = None, 0, 0
     if rope is not None:
-        pr = _tensor(rope, f32, (None, None), where + " rope")
-        n_pos, rot = rope.shape
-    pn = [None if w is None else _tensor(w, f32, (c.dim,), where + " norm") for w in (q_norm, k_norm)]
-    pp = None if positions is None else _tensor(positions, torch.int32, (M,), where + " positions")
-    _same_device(x, (cache.k, batch.lens, out, rope, q_norm, k_norm, positions), where)
-    kq_rope_append(c, batch.rows(M), px, ldx, q_heads, pn[0], pn[1], eps, pr, n_pos, rot, pairs, pp, _type(out, where),
-                   pq)
+        n_pos, rot = rope.shape if rope.dim() == 2 else (None, None)
+        pr = _tensor(rope, f32, (n_pos, rot), device, "rope_append rope")
+    pqn = None if q_norm is None else _tensor(q_norm, f32, (dim,), device, "rope_append q_norm")
+    pkn = None if k_norm is None else _tensor(k_norm, f32, (dim,), device, "rope_append k_norm")
+    pp = None if positions is None else _tensor(positions, torch.int32, (M,), device, "rope_append positions")
+    batch.c.n_tokens = M
+    _check((_step or _step_lib()).kq_rope_append(cache.at, batch.at, px, ldx, q_heads, pqn, pkn, eps, pr, n_pos, rot,
+                                                 1 if pairs else 0, pp, _type(q_dtype, "rope_append out"), pq,
+                                                 _current_stream(device)), "kq_rope_append")
     return out
 
 
@@ -488,22 +519,32 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
     if stream is not None:
         with _on(stream, q.device):
             return attn_tree(cache, batch, q, mask, scale, max_tokens, max_len, out_dtype, out)
-    where, c = "attn_tree", cache.c
-    pq = _tensor(q, None, (None, None, c.dim), where + " q")
-    M, heads, dim = q.shape
+    c, device, q_dtype = cache.c, q.get_device(), q.dtype
+    dim = c.dim
+    if device < 0 or q.dim() != 3 or q.shape[2] != dim or not q.is_contiguous():
+        _refuse(q, q_dtype, (None, None, dim), device, "attn_tree q")
+    M, heads, _ = shape = q.shape
+    _together(device, cache, batch, "attn_tree")
     if out is None:
-        out = torch.empty((M, heads, dim), dtype=out_dtype or q.dtype, device=q.device)
-    po = _tensor(out, out_dtype, (M, heads, dim), where + " out")
-    pm = None if mask is None else _tensor(mask, torch.int64, (M,), where + " mask")
+        out = torch.empty_like(q) if out_dtype is None else torch.empty(shape, dtype=out_dtype, device=q.device)
+        po = out.data_ptr()
+    else:
+        po = _tensor(out, out_dtype or out.dtype, shape, device, "attn_tree out")
+    pm = None if mask is None else _tensor(mask, torch.int64, (M,), device, "attn_tree mask")
     if max_len is None:
         max_len = batch.c.max_pages * c.page
     if scale is None:
         scale = dim ** -0.5
-    _same_device(q, (cache.k, batch.lens, out, mask), where)
-    b = batch.rows(M)
-    need = kq_attn_tree_workspace(c, b, heads, max_tokens, max_len)
-    work = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    kq_attn_tree(c, b, _type(q, where), pq, heads, pm, scale, max_tokens, max_len, _type(out, where), po, work, need)
+    batch.c.n_tokens = M
+    step = _step or _step_lib()
+    need = step.kq_attn_tree_workspace(cache.at, batch.at, heads, max_tokens, max_len)
+    work = pw = None
+    if need:
+        work = torch.empty(need, dtype=torch.uint8, device=q.device)
+        pw = work.data_ptr()
+    _check(step.kq_attn_tree(cache.at, batch.at, _type(q_dtype, "attn_tree q"), q.data_ptr(), heads, pm, scale, max_tokens,
+                             max_len, _type(out.dtype, "attn_tree out"), po, pw, need, _current_stream(device)),
+           "kq_attn_tree")
     return out
 
 
@@ -512,12 +553,25 @@ def cache_keep(caches, batch, path, counts, stream=None):
     lens[b] + j takes what slot lens[b] + path[offsets[b] + j] held, j < counts[b]
     (int32 [n_tokens] and [n_seqs])."""
     import torch
-    where, i32 = "cache_keep", torch.int32
-    pp = _tensor(path, i32, (None,), where + " path")
-    pc = _tensor(counts, i32, (batch.c.n_seqs,), where + " counts")
-    n = len(caches)
-    _same_device(path, (batch.lens, counts, *(c.k for c in caches)), where)
-    kq_cache_keep((kq_cache * n)(*(c.c for c in caches)), n, batch.rows(path.shape[0]), pp, pc, stream)
+    i32, device, n = torch.int32, path.get_device(), len(caches)
+    if device < 0 or path.dim() != 1:
+        _refuse(path, i32, (None,), device, "cache_keep path")
+    pp = _tensor(path, i32, path.shape, device, "cache_keep path")
+    pc = _tensor(counts, i32, (batch.c.n_seqs,), device, "cache_keep counts")
+    for c in caches:
+        if c.device != device:
+            _together(device, c, batch, "cache_keep")
+    if batch.device != device:
+        raise ValueError(f"cache_keep: tensors on devices {device} and {batch.device}")
+    batch.c.n_tokens = path.shape[0]
+    if n == 1:
+        at = caches[0].at
+    else:
+        every = (kq_cache * n)(*[c.c for c in caches])
+        at = ctypes.addressof(every)
+    step = _step or _step_lib()
+    _check(step.kq_cache_keep(at, n, batch.at, pp, pc, _current_stream(device) if stream is None else _stream(stream)),
+           "kq_cache_keep")
 
 
 class LogProbs:
@@ -534,25 +588,33 @@ def logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     if stream is not None:
         with _on(stream, logits.device):
             return logprobs(logits, tokens, n_top, entropy)
-    where, f32 = "logprobs", torch.float32
-    px, ldx = _rows(logits, (None, None), where + " logits")
+    device = logits.get_device()
+    px, ldx = _rows(logits, None, device, "logprobs logits")
     M, V = logits.shape
-    kind, dev = _type(logits, where), logits.device
-    if kind == KQ_T_F8:
-        raise ValueError(f"{where}: element type {logits.dtype} not taken")
+    kind, dev = _type(logits.dtype, "logprobs logits"), logits.device
+    step = _step or _step_lib()
+    given, pt = 0, None
+    if tokens is not None:
+        given = tokens.shape[-1]
+        pt = _tensor(tokens, torch.int32, (M, given), device, "logprobs tokens")
+    n_top = max(int(n_top), 0)
+    # one allocation: the floats [M][n_given], [M], [M][n_top], the ids, the workspace
+    lens = (M * given, M if entropy else 0, M * n_top)
+    need = step.kq_logprobs_workspace(M, V, n_top)
+    floats = lens[0] + lens[1] + lens[2]
+    at = (floats + lens[2] + 3) // 4 * 4
+    block = torch.empty(at + (need + 3) // 4, dtype=torch.float32, device=dev)
+    p = block.data_ptr()
     r = LogProbs()
     r.logprob = r.entropy = r.top_ids = r.top_logprobs = None
-    pt, given = None, 0
+    p_given = p_entropy = p_ids = p_tops = None
     if tokens is not None:
-        pt, given = _tensor(tokens, torch.int32, (M, None), where + " tokens"), tokens.shape[1]
-        _same_device(logits, (tokens,), where)
-        r.logprob = torch.empty((M, given), dtype=f32, device=dev)
+        r.logprob, p_given = block.as_strided((M, given), (given, 1), 0), p
     if entropy:
-        r.entropy = torch.empty((M,), dtype=f32, device=dev)
+        r.entropy, p_entropy = block.as_strided((M,), (1,), lens[0]), p + 4 * lens[0]
     if n_top:
-        r.top_ids = torch.empty((M, max(n_top, 0)), dtype=torch.int32, device=dev)
-        r.top_logprobs = torch.empty((M, max(n_top, 0)), dtype=f32, device=dev)
-    need = kq_logprobs_workspace(M, V, n_top)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    kq_logprobs(kind, px, M, V, ldx, pt, given, n_top, r.logprob, r.entropy, r.top_ids, r.top_logprobs, work, need)
+        r.top_logprobs, p_tops = block.as_strided((M, n_top), (n_top, 1), lens[0] + lens[1]), p + 4 * (lens[0] + lens[1])
+        r.top_ids, p_ids = block.view(torch.int32).as_strided((M, n_top), (n_top, 1), floats), p + 4 * floats
+    _check(step.kq_logprobs(kind, px, M, V, ldx, pt, given, n_top, p_given, p_entropy, p_ids, p_tops,
+                            p + 4 * at if need else None, need, _current_stream(device)), "kq_logprobs")
     return r

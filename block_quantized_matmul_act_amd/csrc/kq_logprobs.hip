@@ -5,12 +5,18 @@
 //   lse = m + log s,  logprob = x - lse,  entropy = log s - t / s
 //
 // Every lane keeps its own (m, s, t) in fp32 over 16 values at a time: when m
-// rises by u, s and t become s e^-u and (t - u s) e^-u.  The n largest live
-// sorted in the lanes of each wave (lane i: the i-th); a value enters only if
-// it beats the last of them, which after the first 1024 values of a wave is
-// rare, so the search costs one comparison per 16 values.  Ties go to the
-// lower index, so the order is total and the result does not depend on how
-// the row is cut.
+// rises by u, s and t become s e^-u and (t - u s) e^-u.
+//
+// The largest values live sorted in the lanes of each wave (lane i: the i-th), as
+// 64-bit keys: the value's bits in an order of whole numbers, then the
+// complement of its index, so that ties go to the lower index, the order is total
+// and the result does not depend on how the row is cut.  A value is a candidate if
+// it beats the n-th of them; candidates gather in LDS, and up to 64 at a time
+// are sorted by a network over the lanes and merged (the larger of list i and
+// candidate 63 - i are the 64 largest of both, in an order that 6 steps sort).
+// Before the first values the n-th largest of the lanes' largest bounds the n-th
+// from below, so even they bring few candidates; later a candidate is rare, and
+// the search costs one comparison per 16 values.
 //
 // A row is cut into parts where there are too few rows to fill the chip; each
 // part leaves (m, s, t) and its n largest, and a second kernel joins them.
@@ -46,42 +52,119 @@ __device__ __forceinline__ void join(Stat &a, Stat b) {
     a.t += b.t;
 }
 
-// The n largest (value, index) seen by a wave, lane i holding the i-th;
-// last_v / last_i (uniform): the n-th.
-struct Top {
-    float v = -__builtin_inff();
-    int i = INT32_MAX;
-    float last_v = -__builtin_inff();
-    int last_i = INT32_MAX;
-};
-__device__ __forceinline__ bool beats(float v, int i, float v2, int i2) { return v > v2 || (v == v2 && i < i2); }
-__device__ __forceinline__ float lane_f(float v, int lane) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
-// every lane's (v, i) that beats the n-th enters; a lane without a value passes on = false
-__device__ __forceinline__ void enter(Top &top, float v, int i, bool on, int n) {
+// v of lane (this ^ D)
+template <int D>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+    auto dpp = [](uint32_t x, auto C) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(C)::value, 0xF, 0xF, false);
+    };
     const int lane = threadIdx.x & 63;
-    uint64_t todo = __ballot(on && beats(v, i, top.last_v, top.last_i));
-    while (todo) {
-        const int src = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        const float nv = lane_f(v, src);
-        const int ni = __builtin_amdgcn_readlane(i, src);
-        if (!beats(nv, ni, top.last_v, top.last_i)) continue;
-        const int at = __popcll(__ballot(beats(top.v, top.i, nv, ni)));
-        const float pv = __shfl_up(top.v, 1);
-        const int pi = __shfl_up(top.i, 1);
-        if (lane > at) {
-            top.v = pv;
-            top.i = pi;
-        } else if (lane == at) {
-            top.v = nv;
-            top.i = ni;
-        }
-        top.last_v = lane_f(top.v, n - 1);
-        top.last_i = __builtin_amdgcn_readlane(top.i, n - 1);
+    if constexpr (D == 1) return dpp(v, IC<0xB1>{});
+    if constexpr (D == 2) return dpp(v, IC<0x4E>{});
+    if constexpr (D == 4) return dpp(dpp(v, IC<0x141>{}), IC<0x1B>{});  // ^ 7, ^ 3
+    if constexpr (D == 8) return dpp(v, IC<0x128>{});
+    if constexpr (D == 15) return dpp(v, IC<0x140>{});
+    if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return lane & 16 ? r[0] : r[1];
+    }
+    if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return lane & 32 ? r[0] : r[1];
     }
 }
+typedef uint64_t Key;
+template <int D>
+__device__ __forceinline__ Key key_xor(Key k) {
+    return (Key)lane_xor<D>((uint32_t)(k >> 32)) << 32 | lane_xor<D>((uint32_t)k);
+}
+// One step of a sorting network: the larger key to the lane with bit D clear, or
+// in lanes with bit UP set the other way round.
+template <int D, int UP>
+__device__ __forceinline__ void order(Key &k) {
+    const int lane = threadIdx.x & 63;
+    const Key o = key_xor<D>(k);
+    const bool larger = ((lane & D) == 0) != ((lane & UP) != 0);
+    k = (k > o) == larger ? k : o;
+}
+// a bitonic sequence of 64 keys to a falling one
+__device__ __forceinline__ void merge64(Key &k) {
+    order<32, 0>(k);
+    order<16, 0>(k);
+    order<8, 0>(k);
+    order<4, 0>(k);
+    order<2, 0>(k);
+    order<1, 0>(k);
+}
+__device__ __forceinline__ void sort64(Key &k) {
+    order<1, 2>(k);
+    order<2, 4>(k), order<1, 4>(k);
+    order<4, 8>(k), order<2, 8>(k), order<1, 8>(k);
+    order<8, 16>(k), order<4, 16>(k), order<2, 16>(k), order<1, 16>(k);
+    order<16, 32>(k), order<8, 32>(k), order<4, 32>(k), order<2, 32>(k), order<1, 32>(k);
+    merge64(k);
+}
+// the 64 largest of two falling sequences, falling
+__device__ __forceinline__ Key join64(Key a, Key b) {
+    b = key_xor<15>(key_xor<16>(key_xor<32>(b)));  // reversed
+    a = a > b ? a : b;
+    merge64(a);
+    return a;
+}
+
+// -inf < ... < -0 = 0 < ... < inf as whole numbers, and back.
+__device__ __forceinline__ uint32_t rank_of(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v + 0.f);  // (-0 becomes 0)
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t r) {
+    return __builtin_bit_cast(float, r ^ ((int)r < 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ Key key_of(float v, int i) { return (Key)rank_of(v) << 32 | ~(uint32_t)i; }
+__device__ __forceinline__ uint32_t lane_u(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// The largest keys a wave has seen (0: none), and what candidates must beat: the
+// n-th of them, or a bound below it.
+struct Top {
+    Key list = 0, last = 0;
+    float last_v = -__builtin_inff();  // last's value (its rank 0 is below all)
+    int held = 0;                      // candidates in LDS
+    __device__ __forceinline__ void bound(Key k) {
+        last = k;
+        last_v = k ? value_of((uint32_t)(k >> 32)) : -__builtin_inff();
+    }
+    __device__ __forceinline__ void add(Key falling, int n) {
+        list = join64(list, falling);
+        const Key k = (Key)lane_u((uint32_t)(list >> 32), n - 1) << 32 | lane_u((uint32_t)list, n - 1);
+        if (k > last) bound(k);
+    }
+    __device__ __forceinline__ void flush(const Key *mine, int n) {
+        const int lane = threadIdx.x & 63;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        Key k = lane < held ? mine[lane] : 0;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        sort64(k);
+        add(k, n);
+        held = 0;
+    }
+    // each lane's (v, i), where `on`
+    __device__ __forceinline__ void offer(Key *mine, float v, int i, bool on, int n) {
+        const Key k = key_of(v, i);
+        uint64_t better = __ballot(on && k > last);
+        if (!better) return;
+        if (held + __popcll(better) > 64) {
+            flush(mine, n);
+            better = __ballot(on && k > last);
+        }
+        if (on && k > last) {
+            const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(better >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)better, 0));
+            mine[held + before] = k;
+        }
+        held += __popcll(better);
+    }
+};
 
 // 16 consecutive-by-pieces values of the row for one lane; rows need only the
 // alignment of their type.
@@ -92,7 +175,7 @@ struct Load<float> {
     static constexpr int PIECE = 4;
     static __device__ __forceinline__ void get(const float *p, float *x) {
         typedef v4f __attribute__((aligned(4))) u4;
-        const v4f w = *reinterpret_cast<const u4 *>(p);
+        const v4f w = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p));
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = w[e];
     }
@@ -102,16 +185,10 @@ struct Load {
     static constexpr int PIECE = 8;
     static __device__ __forceinline__ void get(const T *p, float *x) {
         typedef v4u __attribute__((aligned(2))) u4;
-        const v4u w = *reinterpret_cast<const u4 *>(p);
+        const v4u w = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p));
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (float)__builtin_bit_cast(T, (unsigned short)(w[e >> 1] >> (16 * (e & 1))));
     }
-};
-
-// What a part leaves in the workspace: [M][parts] Stat, then [M][parts][n] pairs.
-struct Pair {
-    float v;
-    int i;
 };
 
 __device__ __forceinline__ Stat wave_join(Stat a) {
@@ -126,27 +203,24 @@ __device__ __forceinline__ Stat wave_join(Stat a) {
     return a;
 }
 
-// The workgroup's waves -> one Stat (in every thread of wave 0) and the n
-// largest (in wave 0's Top).
+// The workgroup's waves -> one Stat (in every thread of wave 0) and the largest
+// keys (in wave 0's list).  keys: LDS, 64 for each wave.
 template <bool TOP>
-__device__ __forceinline__ void workgroup_join(Stat &st, Top &top, int n) {
+__device__ __forceinline__ void workgroup_join(Stat &st, Top &top, Key *keys, int n) {
     __shared__ Stat stats[WG / 64];
-    __shared__ Pair pairs[WG / 64][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     st = wave_join(st);
     if (lane == 0) stats[wave] = st;
     if constexpr (TOP) {
-        if (lane < n) pairs[wave][lane] = Pair{top.v, top.i};
+        if (top.held) top.flush(keys + wave * 64, n);
+        keys[wave * 64 + lane] = top.list;
     }
     __syncthreads();
     if (wave) return;
 #pragma unroll
     for (int w = 1; w < WG / 64; ++w) {
         join(st, stats[w]);
-        if constexpr (TOP) {
-            const Pair p = lane < n ? pairs[w][lane] : Pair{0.f, 0};
-            enter(top, p.v, p.i, lane < n && p.i != INT32_MAX, n);
-        }
+        if constexpr (TOP) top.list = join64(top.list, keys[w * 64 + lane]);
     }
 }
 
@@ -163,8 +237,8 @@ __device__ __forceinline__ void finish(const LogprobsArgs &a, int64_t row, const
     if constexpr (TOP) {
         if (lane < a.n_top) {
             // (a row with NaNs may have found fewer: any index will do)
-            a.top_ids[row * a.n_top + lane] = min(max(top.i, 0), a.V - 1);
-            a.top_logprobs[row * a.n_top + lane] = top.v - lse;
+            a.top_ids[row * a.n_top + lane] = min(max((int)~(uint32_t)top.list, 0), a.V - 1);
+            a.top_logprobs[row * a.n_top + lane] = value_of((uint32_t)(top.list >> 32)) - lse;
         }
     }
 }
@@ -178,6 +252,8 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const T *x = reinterpret_cast<const T *>(a.x) + row * a.ldx;
     const int n = a.n_top;
+    __shared__ Key keys[TOP ? WG : 1];
+    Key *mine = keys + (TOP ? wave * 64 : 0);
     Stat st = STAT_0;
     Top top;
     for (int at = from + wave * BATCH; at < to; at += WG / 64 * BATCH) {
@@ -203,8 +279,16 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
             st.t = fmaf(e, fmaxf(z, -1000.f), st.t);  // (e = 0 where z is below: never 0 * -inf)
         }
         if constexpr (TOP) {
+            if (at == from + wave * BATCH) {
+                // the n-th largest of the lanes' largest: at least n values reach it
+                // (of a lane past the end: none, so the bound is none, too)
+                Key k = at + lane * PIECE < to ? key_of(best, INT32_MAX) : 0;
+                sort64(k);
+                const uint32_t r = lane_u((uint32_t)(k >> 32), n - 1);
+                if (r) top.bound((Key)r << 32);
+            }
             const int i0 = at + lane * PIECE;  // the lowest index of this lane's values
-            if (__any(best > top.last_v || (best == top.last_v && i0 < top.last_i))) {
+            if (__any(best > top.last_v || (best == top.last_v && ~(uint32_t)i0 > (uint32_t)top.last))) {
 #pragma nounroll
                 for (int p = 0; p < PIECES; ++p)
 #pragma unroll
@@ -213,12 +297,13 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
 #pragma unroll
                         for (int q = 1; q < PIECES; ++q) w = p == q ? v[q * PIECE + e] : w;
                         const int i = at + (p * 64 + lane) * PIECE + e;
-                        enter(top, w, i, i < to, n);
+                        top.offer(mine, w, i, i < to, n);
                     }
+                if (top.held >= 16) top.flush(mine, n);
             }
         }
     }
-    workgroup_join<TOP>(st, top, n);
+    workgroup_join<TOP>(st, top, keys, n);
     if (wave) return;
     if (a.parts == 1) {
         finish<T, TOP>(a, row, x, st, top);
@@ -227,8 +312,8 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
     Stat *stats = reinterpret_cast<Stat *>(a.ws);
     if (lane == 0) stats[blockIdx.x] = st;
     if constexpr (TOP) {
-        Pair *pairs = reinterpret_cast<Pair *>(stats + (int64_t)gridDim.x);
-        if (lane < n) pairs[(int64_t)blockIdx.x * n + lane] = Pair{top.v, top.i};
+        Key *lists = reinterpret_cast<Key *>(a.ws + (12 * (int64_t)gridDim.x + 7) / 8 * 8);
+        if (lane < n) lists[(int64_t)blockIdx.x * n + lane] = top.list;
     }
 }
 
@@ -241,16 +326,18 @@ __global__ __launch_bounds__(WG) void logprobs_join_kernel(const LogprobsArgs a)
     Stat st = STAT_0;
     Top top;
     for (int p = threadIdx.x; p < a.parts; p += WG) join(st, stats[row * a.parts + p]);
+    __shared__ Key keys[TOP ? WG : 1];
     if constexpr (TOP) {
-        const Pair *pairs = reinterpret_cast<const Pair *>(stats + items) + row * a.parts * a.n_top;
-        const int all = a.parts * a.n_top;
-        for (int p0 = wave * 64; p0 < all; p0 += WG) {
-            const bool on = p0 + lane < all;
-            const Pair p = on ? pairs[p0 + lane] : Pair{0.f, 0};
-            enter(top, p.v, p.i, on && p.i != INT32_MAX, a.n_top);
+        const int n = a.n_top;
+        const Key *lists = reinterpret_cast<const Key *>(a.ws + (12 * items + 7) / 8 * 8) + row * a.parts * n;
+        Key next = wave < a.parts && lane < n ? lists[wave * n + lane] : 0;
+        for (int p = wave; p < a.parts; p += WG / 64) {
+            const Key now = next;
+            next = p + WG / 64 < a.parts && lane < n ? lists[(p + WG / 64) * n + lane] : 0;
+            top.list = join64(top.list, now);
         }
     }
-    workgroup_join<TOP>(st, top, a.n_top);
+    workgroup_join<TOP>(st, top, keys, a.n_top);
     if (wave == 0)
         finish<T, TOP>(a, row, reinterpret_cast<const T *>(a.x) + row * a.ldx, st, top);
 }

@@ -114,7 +114,7 @@ LogprobsPlan logprobs_plan(int64_t M, int64_t V, int64_t n_top) {
     part = std::max<int64_t>(4096, (part + 4095) / 4096 * 4096);
     p.part = (int)std::min<int64_t>(part, kMaxInt / 2 + 1);
     p.parts = (int)std::max<int64_t>(1, (V + p.part - 1) / p.part);
-    p.bytes = p.parts > 1 ? M * p.parts * (12 + 8 * n_top) : 0;
+    p.bytes = p.parts > 1 ? (M * p.parts * 12 + 7) / 8 * 8 + M * p.parts * 8 * n_top : 0;
     return p;
 }
 

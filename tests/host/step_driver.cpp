@@ -127,7 +127,7 @@ int main() {
             const size_t bytes = kq_logprobs_workspace(M, V, V < 7 ? 1 : 7);
             EXPECT(kq_logprobs(KQ_T_BF16, A, M, V, V, I, 2, V < 7 ? 1 : 7, F, nullptr, I, F, A, bytes, nullptr) == KQ_OK);
             EXPECT((int64_t)lp.part * lp.parts >= V && (int64_t)lp.part * (lp.parts - 1) < V);
-            EXPECT(bytes == (lp.parts > 1 ? (size_t)(M * lp.parts * (12 + 8 * 7)) : 0));
+            EXPECT(bytes == (lp.parts > 1 ? (size_t)((M * lp.parts * 12 + 7) / 8 * 8 + M * lp.parts * 8 * 7) : 0));
             if (bytes) EXPECT(kq_logprobs(KQ_T_BF16, A, M, V, V, I, 2, 7, F, nullptr, I, F, A, bytes - 1, nullptr) == KQ_ERR_SHAPE);
         }
     EXPECT(ropes == counted[kq::V_ROPE_APPEND] && keeps == counted[kq::V_CACHE_KEEP]);

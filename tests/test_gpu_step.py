@@ -100,7 +100,7 @@ def test_attn_long_sequences_in_parts(kq, tokens, group, dim):
     step = Step(5, lens, new, 32)
     batch = step.batch(kq)
     c = kq.PagedCache(*(t.to(DEV) for t in ref.empty_cache(2, 1, 32, dim, F16)))
-    batch.rows(step.M)
+    batch.c.n_tokens = step.M
     assert kq.kq_attn_tree_workspace(c.c, batch.c, group, tokens, step.max_len) > 0
     rng = np.random.default_rng(1)
     mask = np.concatenate([ref.tree_mask(rng, n) for n in new])
