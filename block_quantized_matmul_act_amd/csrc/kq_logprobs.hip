@@ -169,25 +169,25 @@ struct Top {
 // 16 consecutive-by-pieces values of the row for one lane; rows need only the
 // alignment of their type.
 template <class T>
-struct Load;
-template <>
-struct Load<float> {
-    static constexpr int PIECE = 4;
-    static __device__ __forceinline__ void get(const float *p, float *x) {
-        typedef v4f __attribute__((aligned(4))) u4;
-        const v4f w = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = w[e];
-    }
-};
-template <class T>
 struct Load {
-    static constexpr int PIECE = 8;
-    static __device__ __forceinline__ void get(const T *p, float *x) {
-        typedef v4u __attribute__((aligned(2))) u4;
-        const v4u w = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p));
+    typedef v4u raw;
+    static constexpr int PIECE = 16 / sizeof(T);
+    static __device__ __forceinline__ raw get(const T *p) {
+        typedef v4u __attribute__((aligned(4))) at4;
+        typedef v4u __attribute__((aligned(2))) at2;
+        if constexpr (sizeof(T) == 4)
+            return __builtin_nontemporal_load(reinterpret_cast<const at4 *>(p));
+        else
+            return __builtin_nontemporal_load(reinterpret_cast<const at2 *>(p));
+    }
+    static __device__ __forceinline__ void open(raw w, float *x) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (float)__builtin_bit_cast(T, (unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+        for (int e = 0; e < PIECE; ++e) {
+            if constexpr (sizeof(T) == 4)
+                x[e] = __builtin_bit_cast(float, w[e]);
+            else
+                x[e] = (float)__builtin_bit_cast(T, (unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+        }
     }
 };
 
@@ -256,11 +256,21 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
     Key *mine = keys + (TOP ? wave * 64 : 0);
     Stat st = STAT_0;
     Top top;
-    for (int at = from + wave * BATCH; at < to; at += WG / 64 * BATCH) {
+    // whole batches are loaded a turn ahead
+    constexpr int STEP = WG / 64 * BATCH;
+    typename Load<T>::raw next[PIECES];
+    auto load = [&](int at) {
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) next[p] = Load<T>::get(x + at + (p * 64 + lane) * PIECE);
+    };
+    int at = from + wave * BATCH;
+    if (at + BATCH <= to) load(at);
+    for (; at < to; at += STEP) {
         float v[16];
         if (at + BATCH <= to) {
 #pragma unroll
-            for (int p = 0; p < PIECES; ++p) Load<T>::get(x + at + (p * 64 + lane) * PIECE, v + p * PIECE);
+            for (int p = 0; p < PIECES; ++p) Load<T>::open(next[p], v + p * PIECE);
+            if (at + STEP + BATCH <= to) load(at + STEP);
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {

@@ -10,7 +10,7 @@
 // transposed in their page, so a workgroup stages a tile of rows in LDS and
 // stores, feature by feature, 8 consecutive slots at once where 8 rows of the
 // tile are an aligned run of one page; rows outside such runs (the ends of a
-// sequence, single tokens) go value by value.
+// sequence, single tokens) go value by value.  x is read once, past the caches.
 //
 // Bound: HBM bandwidth (4 bytes read, 2 or 1 written per value); a call of few
 // rows is bound by its launch and two dependent loads (row -> sequence -> page).
@@ -61,46 +61,60 @@ struct Rope {
         return r;
     }
 
-    // One wave: HPW consecutive query / key heads of one row.
-    static __device__ __forceinline__ void heads(const RopeArgs &a, int row, int group) {
+    // One wave: GROUPS times HPW consecutive query / key heads of one row, from
+    // `head0`.  The row's place and its cosines are found once.
+    template <int GROUPS>
+    static __device__ __forceinline__ void heads(const RopeArgs &a, int row, int head0) {
         const int lane = threadIdx.x & 63;
-        const int i = lane % LPH, hd = group * HPW + lane / LPH;
+        const int i = lane % LPH, hd0 = head0 + lane / LPH;
         const int kv = a.cache.heads, n_heads = a.q_heads + kv;
-        const bool on = hd < n_heads;
-        const bool is_q = hd < a.q_heads;
-        const float *xp = a.x + (int64_t)row * a.ldx + (int64_t)(on ? hd : 0) * D;
-        v4f lo = at(xp + 4 * i), hi = at(xp + D / 2 + 4 * i);
-
+        const float *xr = a.x + (int64_t)row * a.ldx;
+        v4f lo[GROUPS], hi[GROUPS];
+#pragma unroll
+        for (int j = 0; j < GROUPS; ++j) {
+            const int hd = min(hd0 + j * HPW, n_heads - 1);
+            lo[j] = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(xr + hd * D + 4 * i));
+            hi[j] = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(xr + hd * D + D / 2 + 4 * i));
+        }
         // the slot is needed by keys and by positions that follow it
         int slot = 0, page = 0;
-        const bool any_k = (group + 1) * HPW > a.q_heads;
-        if (any_k || !a.positions) {
+        if (head0 + GROUPS * HPW > a.q_heads || !a.positions) {
             const int b = batch_seq(a.batch, row);
             int first, count;
             batch_rows(a.batch, b, first, count);
             slot = max(a.batch.lens[b], 0) + (row - first);
             page = slot_page(a.cache, a.batch, b, slot);
         }
-        const float *w = is_q ? a.q_norm : a.k_norm;
-        float rs = 1.f;
-        if (a.q_norm || a.k_norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
-#pragma unroll
-            for (int x = 1; x < LPH; x <<= 1) ss += __shfl_xor(ss, x);
-            if (w) rs = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        }
-        v4f ylo = lo * rs, yhi = hi * rs;
-        if (w) {
-            ylo *= at(w + 4 * i);
-            yhi *= at(w + D / 2 + 4 * i);
-        }
+        const float *cs = a.rope;
+        v4f c = {0.f, 0.f, 0.f, 0.f}, s = c;
+        const bool whole = a.rot == D && !a.pairs;  // the halves that lo and hi are
         if (a.rot) {
-            const int pos = min(max(a.positions ? a.positions[row] : slot, 0), a.n_pos - 1);
-            const float *cs = a.rope + (int64_t)pos * a.rot;
-            if (a.rot == D && !a.pairs) {
-                const v4f c = at(cs + 4 * i), s = at(cs + D / 2 + 4 * i);
+            cs += (int64_t)min(max(a.positions ? a.positions[row] : slot, 0), a.n_pos - 1) * a.rot;
+            if (whole) {
+                c = at(cs + 4 * i);
+                s = at(cs + D / 2 + 4 * i);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < GROUPS; ++j) {
+            const int hd = hd0 + j * HPW;
+            const bool is_q = hd < a.q_heads;
+            const float *w = is_q ? a.q_norm : a.k_norm;
+            float rs = 1.f;
+            if (a.q_norm || a.k_norm) {
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ss = fmaf(lo[j][e], lo[j][e], fmaf(hi[j][e], hi[j][e], ss));
+#pragma unroll
+                for (int x = 1; x < LPH; x <<= 1) ss += __shfl_xor(ss, x);
+                if (w) rs = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+            }
+            v4f ylo = lo[j] * rs, yhi = hi[j] * rs;
+            if (w) {
+                ylo *= at(w + 4 * i);
+                yhi *= at(w + D / 2 + 4 * i);
+            }
+            if (whole) {
                 v4f z;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -108,22 +122,22 @@ struct Rope {
                     yhi[e] = fmaf(yhi[e], c[e], ylo[e] * s[e]);
                 }
                 ylo = z;
-            } else {
+            } else if (a.rot) {
+                const float *xp = xr + min(hd, n_heads - 1) * D;
                 ylo = rotate(a, ylo, 4 * i, xp, w, rs, cs);
                 yhi = rotate(a, yhi, D / 2 + 4 * i, xp, w, rs, cs);
             }
-        }
-        if (!on) return;
-        if (is_q) {
-            char *p = a.q + (((int64_t)row * a.q_heads + hd) * D + 4 * i) * 2;
-            *reinterpret_cast<v2u *>(p) = v2u{pack2<E>(ylo[0], ylo[1]), pack2<E>(ylo[2], ylo[3])};
-            *reinterpret_cast<v2u *>(p + D) = v2u{pack2<E>(yhi[0], yhi[1]), pack2<E>(yhi[2], yhi[3])};
-        } else {
-            const int shift = a.cache.page_shift;
-            char *p = a.cache.k + ((((int64_t)page * kv + (hd - a.q_heads)) << shift) + (slot & ((1 << shift) - 1))) * (D * ES) +
-                      4 * i * ES;
-            store4(p, ylo * a.k_inv);
-            store4(p + D / 2 * ES, yhi * a.k_inv);
+            if (is_q) {
+                char *p = a.q + (((int64_t)row * a.q_heads + hd) * D + 4 * i) * 2;
+                *reinterpret_cast<v2u *>(p) = v2u{pack2<E>(ylo[0], ylo[1]), pack2<E>(ylo[2], ylo[3])};
+                *reinterpret_cast<v2u *>(p + D) = v2u{pack2<E>(yhi[0], yhi[1]), pack2<E>(yhi[2], yhi[3])};
+            } else if (hd < n_heads) {
+                const int shift = a.cache.page_shift;
+                char *p = a.cache.k + 4 * i * ES +
+                          ((((int64_t)page * kv + (hd - a.q_heads)) << shift) + (slot & ((1 << shift) - 1))) * (D * ES);
+                store4(p, ylo * a.k_inv);
+                store4(p + D / 2 * ES, yhi * a.k_inv);
+            }
         }
     }
 
@@ -132,32 +146,64 @@ struct Rope {
     static __device__ __forceinline__ void values(const RopeArgs &a, int row0, int h) {
         constexpr int PITCH = D * ES + 4;  // 4 bytes past a row: feature-wise reads of 8 rows miss no bank twice
         __shared__ __align__(16) char tile[TT * PITCH];
-        __shared__ int64_t where[TT];  // byte offset of the row's slot in v for feature 0
-        __shared__ int place[TT];      // its place in the page, -1 for no row
+        __shared__ int64_t where[TT];      // byte offset of the row's slot in v for feature 0
+        __shared__ int runs[TT], ones[TT];  // rows that lead 8 of a page, rows that go alone
+        __shared__ int n_runs, n_ones;
         const int rows = min(TT, a.batch.n_tokens - row0);
         const int shift = a.cache.page_shift, kv = a.cache.heads;
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        for (int r = wave; r < TT; r += 4) {
-            if (r >= rows) {
-                if (lane == 0) place[r] = -1;
-                continue;
+        const int lane = threadIdx.x & 63;
+        if (threadIdx.x < 64) {
+            // a lane to a row: its sequence (the first row's, and those that begin
+            // up to it), its slot, its place
+            const int b0 = batch_seq(a.batch, row0);
+            const int next = b0 + 1 + lane;
+            const int begins = next < a.batch.n_seqs ? a.batch.offsets[next] : INT32_MAX;
+            int b = b0;
+            for (int r = 0; r < rows; ++r) {
+                const int more = __popcll(__ballot(begins <= row0 + r));
+                if (lane == r) b = b0 + more;
             }
-            const int b = batch_seq(a.batch, row0 + r);
-            int first, count;
-            batch_rows(a.batch, b, first, count);
-            const int slot = max(a.batch.lens[b], 0) + (row0 + r - first);
-            const int page = slot_page(a.cache, a.batch, b, slot);
-            const int in = slot & ((1 << shift) - 1);
+            if (__any(b == b0 + 64)) {  // (more than 64 sequences in the tile: some have no rows)
+                for (int r = 0; r < rows; ++r) {
+                    const int each = batch_seq(a.batch, row0 + r);
+                    if (lane == r) b = each;
+                }
+            }
+            const bool row = lane < rows;
+            int64_t at = -1;
+            int in = 1;
+            if (row) {
+                int first, count;
+                batch_rows(a.batch, b, first, count);
+                const int slot = max(a.batch.lens[b], 0) + (row0 + lane - first);
+                in = slot & ((1 << shift) - 1);
+                at = ((((int64_t)slot_page(a.cache, a.batch, b, slot) * kv + h) * D << shift) + in) * ES;
+                where[lane] = at;
+            }
+            // A row leads a run if its place is a multiple of 8 and it and the 7 after
+            // it lie one after another; it then stores for all 8.
+            const int64_t then = __shfl_down(at, 1);
+            const uint64_t joined = __ballot(lane + 1 < rows && then == at + ES);
+            const uint64_t leads = __ballot(row && (in & 7) == 0 && ((joined >> lane) & 127ull) == 127ull);
+            uint64_t led = leads;
+            led |= led << 1;
+            led |= led << 2;
+            led |= led << 4;
+            const uint64_t alone = __ballot(row) & ~led;
+            const uint64_t below = (1ull << lane) - 1ull;
+            if (leads >> lane & 1ull) runs[__popcll(leads & below)] = lane;
+            if (alone >> lane & 1ull) ones[__popcll(alone & below)] = lane;
             if (lane == 0) {
-                where[r] = ((((int64_t)page * kv + h) * D << shift) + in) * ES;
-                place[r] = in;
+                n_runs = __popcll(leads);
+                n_ones = __popcll(alone);
             }
         }
         constexpr int RPP = 256 / LPH;  // rows to a pass
         const int i = threadIdx.x % LPH;
         for (int r = threadIdx.x / LPH; r < rows; r += RPP) {
             const float *xp = a.x + (int64_t)(row0 + r) * a.ldx + (int64_t)(a.q_heads + kv + h) * D + 4 * i;
-            const v4f lo = at(xp) * a.v_inv, hi = at(xp + D / 2) * a.v_inv;
+            const v4f lo = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(xp)) * a.v_inv;
+            const v4f hi = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(xp + D / 2)) * a.v_inv;
             char *p = tile + r * PITCH + 4 * i * ES;
             if constexpr (F8) {
                 *reinterpret_cast<uint32_t *>(p) = pack4_f8(lo[0], lo[1], lo[2], lo[3]);
@@ -171,49 +217,44 @@ struct Rope {
             }
         }
         __syncthreads();
-        // Row r leads a run if its place is a multiple of 8 and rows r .. r + 7
-        // lie one after another in its page; it then stores for all 8.
-        auto leads = [&](int r) {
-            if (r < 0 || r + 7 >= rows || (place[r] & 7)) return false;
-            bool run = true;
-#pragma unroll
-            for (int j = 1; j < 8; ++j) run = run && where[r + j] == where[r] + j * ES;
-            return run;
-        };
         char *v = a.cache.v;
-        for (int t = threadIdx.x; t < TT * D; t += 256) {
-            // consecutive lanes: rows of one feature, so that the stores of a
-            // page's run lie next to one another
-            const int r = t % TT, d = t / TT;
-            if (r >= rows) continue;
-            const char *s = tile + r * PITCH + d * ES;
-            char *p = v + where[r] + ((int64_t)d << shift) * ES;
-            if (leads(r)) {
+        constexpr int RUNS = TT / 8;  // at most: the runs of a feature to neighbouring lanes, whose stores adjoin
+        const int n = n_runs, alone = n_ones;
+        if ((int)threadIdx.x % RUNS < n) {
+            const int r = runs[threadIdx.x % RUNS];
+            const char *s = tile + r * PITCH;
+            char *p = v + where[r];
+            for (int d = threadIdx.x / RUNS; d < D; d += 256 / RUNS) {
+                char *to = p + ((int64_t)d << shift) * ES;
                 if constexpr (F8) {
                     v2u w = {0u, 0u};
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        w[j >> 2] |= (uint32_t) * reinterpret_cast<const uint8_t *>(s + j * PITCH) << (8 * (j & 3));
-                    *reinterpret_cast<v2u *>(p) = w;
+                        w[j >> 2] |= (uint32_t) * reinterpret_cast<const uint8_t *>(s + d + j * PITCH) << (8 * (j & 3));
+                    *reinterpret_cast<v2u *>(to) = w;
                 } else {
                     v4u w = {0u, 0u, 0u, 0u};
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        w[j >> 1] |= (uint32_t) * reinterpret_cast<const uint16_t *>(s + j * PITCH) << (16 * (j & 1));
-                    *reinterpret_cast<v4u *>(p) = w;
+                        w[j >> 1] |= (uint32_t) * reinterpret_cast<const uint16_t *>(s + d * 2 + j * PITCH) << (16 * (j & 1));
+                    *reinterpret_cast<v4u *>(to) = w;
                 }
-            } else if (!leads(r - (place[r] & 7))) {
-                if constexpr (F8)
-                    *p = *s;
-                else
-                    *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(s);
             }
+        }
+        for (int t = threadIdx.x; t < alone * D; t += 256) {
+            const int r = ones[t / D], d = t % D;
+            const char *s = tile + r * PITCH + d * ES;
+            char *p = v + where[r] + ((int64_t)d << shift) * ES;
+            if constexpr (F8)
+                *p = *s;
+            else
+                *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(s);
         }
     }
 };
 
 // Blocks [0, value_blocks): tiles of value rows; then 4 waves of heads each.
-template <class E, bool F8, int D, int TT>
+template <class E, bool F8, int D, int TT, int GROUPS>
 __global__ __launch_bounds__(256) void rope_append_kernel(const RopeArgs a, int value_blocks) {
     typedef Rope<E, F8, D> RO;
     const int kv = a.cache.heads;
@@ -221,22 +262,31 @@ __global__ __launch_bounds__(256) void rope_append_kernel(const RopeArgs a, int 
         RO::template values<TT>(a, (int)(blockIdx.x / kv) * TT, blockIdx.x % kv);
         return;
     }
-    const int groups = (a.q_heads + kv + RO::HPW - 1) / RO::HPW;
-    const int64_t item = (int64_t)(blockIdx.x - value_blocks) * 4 + (threadIdx.x >> 6);
-    const int64_t row = item / groups;
-    if (row < a.batch.n_tokens) RO::heads(a, (int)row, (int)(item % groups));
+    constexpr int HEADS = RO::HPW * GROUPS;
+    const int waves = (a.q_heads + kv + HEADS - 1) / HEADS;  // to a row
+    const int item = (blockIdx.x - value_blocks) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = item / waves;
+    if (row < a.batch.n_tokens) RO::template heads<GROUPS>(a, row, (item - row * waves) * HEADS);
+}
+
+template <class E, bool F8, int D, int TT, int GROUPS>
+hipError_t launch_sized(const RopeArgs &a, hipStream_t stream) {
+    const int kv = a.cache.heads;
+    constexpr int HEADS = Rope<E, F8, D>::HPW * GROUPS;
+    const int64_t value_blocks = (int64_t)((a.batch.n_tokens + TT - 1) / TT) * kv;
+    const int64_t waves = (a.q_heads + kv + HEADS - 1) / HEADS;
+    const int64_t blocks = value_blocks + (waves * a.batch.n_tokens + 3) / 4;
+    hipLaunchKernelGGL((rope_append_kernel<E, F8, D, TT, GROUPS>), dim3((unsigned)blocks), dim3(256), 0, stream, a,
+                       (int)value_blocks);
+    return hipGetLastError();
 }
 
 template <class E, bool F8, int D>
 hipError_t launch(const RopeArgs &a, hipStream_t stream) {
-    constexpr int TT = 16;
-    const int kv = a.cache.heads;
-    const int64_t value_blocks = (int64_t)((a.batch.n_tokens + TT - 1) / TT) * kv;
-    const int64_t groups = (a.q_heads + kv + Rope<E, F8, D>::HPW - 1) / Rope<E, F8, D>::HPW;
-    const int64_t blocks = value_blocks + (groups * a.batch.n_tokens + 3) / 4;
-    hipLaunchKernelGGL((rope_append_kernel<E, F8, D, TT>), dim3((unsigned)blocks), dim3(256), 0, stream, a,
-                       (int)value_blocks);
-    return hipGetLastError();
+    // Few rows: as many waves and tiles as there can be.  Many: tiles of 64 rows, of
+    // which all but the ends are whole runs, and more heads to a wave.
+    const int64_t heads = (int64_t)a.batch.n_tokens * (a.q_heads + a.cache.heads) * D;
+    return heads < (1 << 21) ? launch_sized<E, F8, D, 16, 1>(a, stream) : launch_sized<E, F8, D, 64, 2>(a, stream);
 }
 
 template <class E, bool F8>
