@@ -283,10 +283,11 @@ hipError_t launch_sized(const RopeArgs &a, hipStream_t stream) {
 
 template <class E, bool F8, int D>
 hipError_t launch(const RopeArgs &a, hipStream_t stream) {
-    // Few rows: as many waves and tiles as there can be.  Many: tiles of 64 rows, of
-    // which all but the ends are whole runs, and more heads to a wave.
-    const int64_t heads = (int64_t)a.batch.n_tokens * (a.q_heads + a.cache.heads) * D;
-    return heads < (1 << 21) ? launch_sized<E, F8, D, 16, 1>(a, stream) : launch_sized<E, F8, D, 64, 2>(a, stream);
+    // Fewer values: as many waves and tiles as there can be.  More: tiles of 64 rows,
+    // of which all but the ends are whole runs, and two groups of heads to a wave
+    // (1k rows of 48 heads of 128: 11 us and 14; 2k of 40: 18 and 16; 12k of 40: 105 and 93).
+    const int64_t values = (int64_t)a.batch.n_tokens * (a.q_heads + a.cache.heads) * D;
+    return values < (1 << 23) ? launch_sized<E, F8, D, 16, 1>(a, stream) : launch_sized<E, F8, D, 64, 2>(a, stream);
 }
 
 template <class E, bool F8>
