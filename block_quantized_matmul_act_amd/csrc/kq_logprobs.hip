@@ -2,7 +2,7 @@
 // largest of each row of logits, in one pass over the logits (gfx950).
 //
 //   m = max x,  s = sum e^(x - m),  t = sum e^(x - m) (x - m)
-//   lse = m + log s,  logprob = x - lse,  entropy = log s - t / s
+//   logprob = (x - m) - log s,  entropy = log s - t / s
 //
 // Every lane keeps its own (m, s, t) in fp32 over 16 values at a time: when m
 // rises by u, s and t become s e^-u and (t - u s) e^-u.
@@ -27,7 +27,8 @@ namespace kq {
 
 namespace {
 
-constexpr float M_START = -3e38f;  // finite, so that x - m is never inf - inf for x = -inf
+// finite, so that x - m is never inf - inf for x = -inf, and above no finite x
+constexpr float M_START = -3.402823466e38f;
 constexpr int BATCH = 1024;        // values of one step of a wave: 16 to a lane
 constexpr int WG = 256;
 
@@ -38,9 +39,9 @@ constexpr Stat STAT_0 = {M_START, 0.f, 0.f};
 __device__ __forceinline__ float exp_of(float z) { return __builtin_amdgcn_exp2f(z * 1.44269504088896340736f); }
 
 __device__ __forceinline__ void rise(Stat &a, float m) {
-    const float u = a.m - m, f = exp_of(u);
+    // (-1000 is as good as any u below it, and s = 0 times it is 0 where -inf were NaN)
+    const float u = fmaxf(a.m - m, -1000.f), f = exp_of(u);
     a.t = (a.t + u * a.s) * f;
-    // (s = 0 and u = -inf where a row holds +inf: the NaN is the result wanted)
     a.s *= f;
     a.m = m;
 }
@@ -183,10 +184,12 @@ struct Load {
     static __device__ __forceinline__ void open(raw w, float *x) {
 #pragma unroll
         for (int e = 0; e < PIECE; ++e) {
+            // the element as a value first: a bit cast of the element itself reads element 0
+            const unsigned word = w[sizeof(T) == 4 ? e : e >> 1];
             if constexpr (sizeof(T) == 4)
-                x[e] = __builtin_bit_cast(float, w[e]);
+                x[e] = __builtin_bit_cast(float, word);
             else
-                x[e] = (float)__builtin_bit_cast(T, (unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+                x[e] = (float)__builtin_bit_cast(T, (unsigned short)(word >> (16 * (e & 1))));
         }
     }
 };
@@ -208,7 +211,7 @@ __device__ __forceinline__ Stat wave_join(Stat a) {
 template <bool TOP>
 __device__ __forceinline__ void workgroup_join(Stat &st, Top &top, Key *keys, int n) {
     __shared__ Stat stats[WG / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     st = wave_join(st);
     if (lane == 0) stats[wave] = st;
     if constexpr (TOP) {
@@ -228,17 +231,17 @@ __device__ __forceinline__ void workgroup_join(Stat &st, Top &top, Key *keys, in
 template <class T, bool TOP>
 __device__ __forceinline__ void finish(const LogprobsArgs &a, int64_t row, const T *x, Stat st, const Top &top) {
     const int lane = threadIdx.x & 63;
-    const float log_s = logf(st.s), lse = st.m + log_s;
+    const float log_s = logf(st.s);
     for (int i = lane; i < a.n_given; i += 64) {
         const int t = a.tokens[row * a.n_given + i];
-        a.logprob[row * a.n_given + i] = t >= 0 && t < a.V ? (float)x[t] - lse : -__builtin_inff();
+        a.logprob[row * a.n_given + i] = t >= 0 && t < a.V ? ((float)x[t] - st.m) - log_s : -__builtin_inff();
     }
     if (a.entropy && lane == 0) a.entropy[row] = log_s - st.t / st.s;
     if constexpr (TOP) {
         if (lane < a.n_top) {
             // (a row with NaNs may have found fewer: any index will do)
             a.top_ids[row * a.n_top + lane] = min(max((int)~(uint32_t)top.list, 0), a.V - 1);
-            a.top_logprobs[row * a.n_top + lane] = value_of((uint32_t)(top.list >> 32)) - lse;
+            a.top_logprobs[row * a.n_top + lane] = (value_of((uint32_t)(top.list >> 32)) - st.m) - log_s;
         }
     }
 }
@@ -249,7 +252,7 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
     const int64_t row = blockIdx.x / a.parts;
     const int part = blockIdx.x % a.parts;
     const int from = part * a.part, to = min(from + a.part, a.V);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const T *x = reinterpret_cast<const T *>(a.x) + row * a.ldx;
     const int n = a.n_top;
     __shared__ Key keys[TOP ? WG : 1];
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(WG) void logprobs_kernel(const LogprobsArgs a) {
 template <class T, bool TOP>
 __global__ __launch_bounds__(WG) void logprobs_join_kernel(const LogprobsArgs a) {
     const int64_t row = blockIdx.x, items = (int64_t)gridDim.x * a.parts;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Stat *stats = reinterpret_cast<const Stat *>(a.ws);
     Stat st = STAT_0;
     Top top;

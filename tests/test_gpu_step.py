@@ -457,6 +457,26 @@ def test_logprobs_rows_without_a_distribution(kq):
         check_logprobs(kq, x[3:], t[3:], 4)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logprobs_at_the_ends_of_the_range(kq, dtype):
+    """Equal logits at the type's lowest and highest value and at a value that
+    leaves no bits for the sum's logarithm: log probability -log V and entropy log
+    V all the same; and one highest among the lowest is sure."""
+    lo, hi = torch.finfo(dtype).min, torch.finfo(dtype).max
+    for V in (70, 5000):
+        x = torch.tensor([lo, hi, 1e30, -2e38, lo], dtype=dtype)[:, None].repeat(1, V)
+        x[4, V // 2] = hi
+        t = torch.tensor([[0, V // 2]] * 5, dtype=torch.int32)
+        r = kq.logprobs(up(x), up(t), n_top=2)
+        torch.cuda.synchronize()
+        bound = 2.0 ** -24 * (V / 256 + 64) + 2.0 ** -21 * math.log(V)
+        assert ((r.logprob[:4].cpu() + math.log(V)).abs() <= bound).all()
+        assert ((r.top_logprobs[:4].cpu() + math.log(V)).abs() <= bound).all()
+        assert ((r.entropy[:4].cpu() - math.log(V)).abs() <= bound).all()
+        assert r.top_ids[:4].tolist() == [[0, 1]] * 4 and r.top_ids[4].tolist() == [V // 2, 0]
+        assert r.logprob[4].tolist() == [-math.inf, 0.0] and r.entropy[4] == 0
+
+
 def test_logprobs_past_two_gigabytes(kq):
     """Rows at 32-bit-offset ends: 2.2e9 bytes of logits; first and last rows checked."""
     M, V = 5000, 110001
