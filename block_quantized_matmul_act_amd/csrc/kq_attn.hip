@@ -21,7 +21,7 @@
 //
 // A wave holds the sums of RW query rows (16 or 32).
 //
-// How the work is shared: a unit is UNIT slots of one (sequence, key head, block
+// How the work is shared: a unit is 128 (short sequences: 1024) slots of one (sequence, key head, block
 // of rows).  The lengths are known to the device alone, so every workgroup of a
 // grid that just fills the chip adds up the units itself and takes an equal run
 // of them, whatever the mix of lengths.  A run covers parts of at most two
@@ -230,8 +230,6 @@ struct Frag<E, true> {
 
 // ---------------------------------------------------------------- sharing
 
-constexpr int UNIT = ATTN_UNIT;
-
 // A sequence as the kernels see it: rows and slots held inside the step and the
 // bounds of the call.
 struct Seq {
@@ -256,7 +254,7 @@ __device__ __forceinline__ void share_chunk(const AttnArgs &a, Share &s, int chu
     int tiles = 0, blocks = 0;
     if (b < a.batch.n_seqs) {
         const Seq q = seq_of(a, b);
-        tiles = q.T ? (q.total + UNIT - 1) / UNIT : 0;
+        tiles = q.T ? (q.total + (1 << a.unit_shift) - 1) >> a.unit_shift : 0;
         blocks = (q.T * a.group + a.rows_wg - 1) / a.rows_wg;
     }
     int incl = tiles * blocks;
@@ -341,8 +339,8 @@ __device__ __forceinline__ Piece piece_at(const AttnArgs &a, Share &s, int u, in
     p.rb = in_head / tiles;
     const int tile = in_head - p.rb * tiles;
     p.units = min(tiles - tile, end - u);
-    p.from = tile * UNIT;
-    p.to = (tile + p.units) * UNIT;  // (past the sequence's end in its last unit)
+    p.from = tile << a.unit_shift;
+    p.to = (tile + p.units) << a.unit_shift;  // (past the sequence's end in its last unit)
     p.whole = p.units == tiles;
     return p;
 }
@@ -754,10 +752,10 @@ struct Attend {
     }
 };
 
-// Up to 16 rows: one wave's worth, so the 4 waves of a workgroup take tiles in
+// Up to 16 rows: one wave's worth, so the waves of a workgroup take tiles in
 // turn, each its own in LDS without a barrier, and their sums are joined in LDS.
-template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const AttnArgs a) {
+template <class E, bool F8, int D, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, D == 256 || WAVES == 8 ? 1 : 2) void attn_few_kernel(const AttnArgs a) {
     constexpr int RW = 16;
     constexpr int KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
     typedef Tile<E, F8, D, KEYS, RW, 64, true> TL;
@@ -765,8 +763,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
     constexpr int O_FLOATS = RW * (D + 4);
     constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : (O_FLOATS * 4 + 1023) / 1024 * 1024;
 
-    __shared__ __align__(1024) char lds[4 * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
-    __shared__ float lm[4 * RW], ll[4 * RW];
+    __shared__ __align__(1024) char lds[WAVES * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
+    __shared__ float lm[WAVES * RW], ll[WAVES * RW];
 
     Share share = share_of(a);
     const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
@@ -788,24 +786,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
         typename TL::Place next = tl.find(key0);
         tl.load_k(next);
         tl.load_v(next);
-        next = tl.find(key0 + 4 * KEYS);
+        next = tl.find(key0 + WAVES * KEYS);
         at.begin(sq, pc.h, 0);
         if (u != begin) __syncthreads();  // the piece before has been joined
         bool odd = false;
-        for (; key0 < to; key0 += 4 * KEYS) {
+        for (; key0 < to; key0 += WAVES * KEYS) {
             tl.store_k(lds, mine);
             odd |= tl.store_v(lds, mine + TL::K_BYTES, key0);
-            if (key0 + 4 * KEYS < to) {
+            if (key0 + WAVES * KEYS < to) {
                 tl.load_k(next);
                 tl.load_v(next);
-                next = tl.find(key0 + 8 * KEYS);
+                next = tl.find(key0 + 2 * WAVES * KEYS);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             at.tile(lds, mine, key0, sq.len);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
         if (__any(odd)) {
-            for (key0 = pc.from + KEYS * wave; key0 < to; key0 += 4 * KEYS)
+            for (key0 = pc.from + KEYS * wave; key0 < to; key0 += WAVES * KEYS)
                 at.odd_values(pc.b, pc.h, sq, key0, min(key0 + KEYS, to));
         }
         at.end();
@@ -823,10 +821,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
         if (row < R) {
             float mm = M_START;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mm = fmaxf(mm, lm[row + k * RW]);
-            float f[4], sum = 0.f;
+            for (int k = 0; k < WAVES; ++k) mm = fmaxf(mm, lm[row + k * RW]);
+            float f[WAVES], sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < WAVES; ++k) {
                 f[k] = __builtin_amdgcn_exp2f(lm[row + k * RW] - mm);
                 sum += f[k] * ll[row + k * RW];
             }
@@ -839,7 +837,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
                 const int dim = v + jt * 4;
                 v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < WAVES; ++k)
                     acc += f[k] * *reinterpret_cast<const v4f *>(lds + k * WAVE_BYTES + (row * (D + 4) + dim) * 4);
                 put4<E>(a, pc.whole, acc * norm, o_row * D + dim, slot_row * D + dim);
             }
@@ -1069,8 +1067,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int ro
 template <class E, bool F8, int D>
 hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
     const dim3 grid((unsigned)p.grid);
+    if constexpr (D < 256) {
+        if (p.waves == 0 && p.unit_shift != ATTN_UNIT_SHIFT) {
+            hipLaunchKernelGGL((attn_few_kernel<E, F8, D, 8>), grid, dim3(512), 0, stream, a);
+            return hipGetLastError();
+        }
+    }
     if (p.waves == 0)
-        hipLaunchKernelGGL((attn_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_few_kernel<E, F8, D, 4>), grid, dim3(256), 0, stream, a);
     else if (p.waves == 8)
         hipLaunchKernelGGL((attn_wide_kernel<E, F8, D>), grid, dim3(512), 0, stream, a);
     else if constexpr (D < 256)

@@ -39,15 +39,16 @@ hipError_t launch_rope_append(const RopeArgs &a, int type, int dim, int q_type, 
 
 // How attention over the cache is shared out: `waves` waves (0: the kernel for
 // up to 16 rows) hold rows_wg query rows, `grid` workgroups take equal runs of
-// units of ATTN_UNIT slots and leave at most two cut blocks each (slot_rows rows
+// units of 2^unit_shift slots and leave at most two cut blocks each (slot_rows rows
 // of the workspace to a block).
-constexpr int ATTN_UNIT = 128;
+constexpr int ATTN_UNIT_SHIFT = 7, ATTN_UNIT = 1 << ATTN_UNIT_SHIFT;
+constexpr int ATTN_WHOLE_SHIFT = 10, ATTN_WHOLE = 1 << ATTN_WHOLE_SHIFT;  // short sequences that are not cut
 struct AttnPlan {
-    int waves, rows_wg, row_blocks, slot_rows, grid;
+    int waves, rows_wg, row_blocks, slot_rows, grid, unit_shift;
     // workspace: sums, their maxima and weights (to ml_end), 16 bytes to a sequence
     int64_t o_bytes, ml_end, bytes;
 };
-AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len);
+AttnPlan attn_plan(const kq_cache &cache, int64_t n_seqs, int64_t q_heads, int64_t max_tokens, int64_t max_len);
 
 struct AttnArgs {
     CacheArgs cache;
@@ -64,7 +65,7 @@ struct AttnArgs {
     char *out;
     float *ws_o, *ws_ml;
     int32_t *ws_seq;
-    int rows_wg, slot_rows, grid;
+    int rows_wg, slot_rows, grid, unit_shift;
 };
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int type, int dim, int q_type, hipStream_t stream);
 

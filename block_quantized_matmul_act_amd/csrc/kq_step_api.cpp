@@ -83,8 +83,9 @@ int check_attn(const kq_cache *c, const kq_batch *s, int64_t q_heads, int64_t ma
 
 namespace kq {
 
-AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, int64_t max_tokens, int64_t max_len) {
+AttnPlan attn_plan(const kq_cache &cache, int64_t n_seqs, int64_t q_heads, int64_t max_tokens, int64_t max_len) {
     AttnPlan p;
+    const int64_t heads = cache.heads, group = q_heads / heads, dim = cache.dim;
     // Waves of 32 rows, at dim 256 of 16 (whose sums and operands fit the
     // registers); 8 of them where there are rows for more than 4 (96 rows: 103 us
     // with 4, 124 with 8), and at dim 256.
@@ -96,9 +97,20 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t heads, int64_t group, int64_t dim, in
     p.slot_rows = (int)std::min<int64_t>(rows, p.rows_wg);
     // Workgroups: as many as stay on 256 compute units together (8 waves each),
     // or the units there can be.
-    const int64_t units = n_seqs * heads * p.row_blocks * ((max_len + ATTN_UNIT - 1) / ATTN_UNIT);
+    p.unit_shift = ATTN_UNIT_SHIFT;
+    // Few rows of short sequences, no more of them than compute units: a workgroup
+    // of 8 waves takes a head's keys whole, and no second kernel is launched.  The
+    // call, in parts / whole, one sequence of 8 heads of 128, bfloat16: 500 slots
+    // 15.9 / 11.2 us, 1000 slots 15.8 / 12.7, 2000 slots 15.6 / 20.1 (the rate of one
+    // compute unit); 32 sequences of 500 slots 20.0 / 14.9, of 1000 25.5 / 21.5;
+    // more than 256 heads: 200 sequences of 500 62 / 76.  (At dim 256 8 waves' sums do
+    // not fit the registers.)
+    if (p.waves == 0 && max_len > ATTN_UNIT && max_len <= ATTN_WHOLE && n_seqs * heads <= 256 && dim < 256)
+        p.unit_shift = ATTN_WHOLE_SHIFT;
+    const int unit = 1 << p.unit_shift;
+    const int64_t units = n_seqs * heads * p.row_blocks * ((max_len + unit - 1) / unit);
     p.grid = (int)std::min<int64_t>(units, p.waves == 8 ? 256 : 512);
-    const int64_t slots = max_len > ATTN_UNIT ? 2 * (int64_t)p.grid * p.slot_rows : 0;
+    const int64_t slots = max_len > unit ? 2 * (int64_t)p.grid * p.slot_rows : 0;
     p.o_bytes = slots * dim * 4;
     p.ml_end = p.o_bytes + (slots + (slots & 1)) * 8;
     p.bytes = slots ? p.ml_end + n_seqs * 16 : 0;
@@ -169,7 +181,7 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
 size_t kq_attn_tree_workspace(const kq_cache *cache, const kq_batch *batch, int64_t q_heads, int64_t max_tokens,
                               int64_t max_len) {
     if (check_attn(cache, batch, q_heads, max_tokens, max_len) <= 0) return 0;
-    return (size_t)attn_plan(batch->n_seqs, cache->heads, q_heads / cache->heads, cache->dim, max_tokens, max_len).bytes;
+    return (size_t)attn_plan(*cache, batch->n_seqs, q_heads, max_tokens, max_len).bytes;
 }
 
 int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q, int64_t q_heads,
@@ -184,8 +196,7 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     if (rc <= 0) return rc;
     rc = check_step(cache, batch);
     if (rc != KQ_OK) return rc;
-    const AttnPlan p =
-        attn_plan(batch->n_seqs, cache->heads, q_heads / cache->heads, cache->dim, max_tokens, max_len);
+    const AttnPlan p = attn_plan(*cache, batch->n_seqs, q_heads, max_tokens, max_len);
     if (!q || !out || (p.bytes && !workspace)) return KQ_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 8) || !aligned(workspace, 16)) return KQ_ERR_ALIGN;
     if (workspace_bytes < (size_t)p.bytes) return KQ_ERR_SHAPE;
@@ -210,6 +221,7 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     a.rows_wg = p.rows_wg;
     a.slot_rows = p.slot_rows;
     a.grid = p.grid;
+    a.unit_shift = p.unit_shift;
     if (launch_attn(a, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
     count_dispatch(p.waves == 0 ? V_ATTN_FEW : V_ATTN_ROWS);
     return KQ_OK;

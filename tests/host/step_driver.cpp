@@ -86,7 +86,7 @@ int main() {
             for (int64_t seqs : {1, 3, 64, 4096})
                 for (int64_t T : {1, 2, 17, 64})
                     for (int64_t G : {1, 5, 16, 64})
-                        for (int64_t len : {1, 127, 128, 129, 5000, 131075, 1 << 30}) {
+                        for (int64_t len : {1, 127, 128, 129, 1024, 1025, 5000, 131075, 1 << 30}) {
                             kq_cache c = {A, A, 100, KQ_T_F16, 2, dim, page, 1.f, 1.f};
                             kq_batch s = {I, I, I, seqs, seqs, 10};
                             const int before = attns;
@@ -100,9 +100,11 @@ int main() {
                             EXPECT((int64_t)plan.rows_wg * plan.row_blocks >= T * G);
                             EXPECT((int64_t)plan.rows_wg * (plan.row_blocks - 1) < T * G);
                             EXPECT(plan.slot_rows == (T * G < plan.rows_wg ? T * G : plan.rows_wg));
-                            const int64_t units = seqs * 2 * plan.row_blocks * ((len + 127) / 128);
+                            const int unit = plan.waves == 0 && len > 128 && len <= 1024 && seqs * 2 <= 256 && dim < 256 ? 1024 : 128;
+                            EXPECT(1 << plan.unit_shift == unit && attn.unit_shift == plan.unit_shift);
+                            const int64_t units = seqs * 2 * plan.row_blocks * ((len + unit - 1) / unit);
                             EXPECT(units <= INT32_MAX && plan.grid >= 1 && plan.grid <= units && plan.grid <= 512);
-                            const int64_t rows = len > 128 ? 2 * (int64_t)plan.grid * plan.slot_rows : 0;
+                            const int64_t rows = len > unit ? 2 * (int64_t)plan.grid * plan.slot_rows : 0;
                             EXPECT((int64_t)bytes == (rows ? rows * (dim * 4 + 8) + (rows & 1) * 8 + seqs * 16 : 0));
                             EXPECT(plan.o_bytes == rows * dim * 4);
                             EXPECT((char *)attn.ws_seq == (bytes ? A + bytes - seqs * 16 : nullptr) && plan.ml_end % 16 == 0);

@@ -92,6 +92,16 @@ def test_attn_pages(kq, page, tokens):
     check_attn(kq, step, 8, 2, 128, BF16, BF16, None)
 
 
+@pytest.mark.parametrize("dim,kv", [(64, F8), (64, F16), (128, F8), (128, F16), (256, F16)])
+@pytest.mark.parametrize("max_len", [129, 700, 1024, 1025])
+def test_attn_short_sequences_whole(kq, dim, kv, max_len):
+    """Few rows: sequences up to 1024 slots are not cut; lengths around the
+    ends of the waves' turns, masks that see nothing among them."""
+    lens = [n for n in (0, 1, 63, 255, 256, 257, 511, 512, 600, 1020) if n + 4 <= max_len]
+    step = Step(8, lens, [4] * len(lens), 64)
+    check_attn(kq, step, 4, 2, dim, F16, kv, ref.tree_mask(np.random.default_rng(2), 4 * len(lens)) & np.uint64(15), max_len=max_len)
+
+
 @pytest.mark.parametrize("tokens,group,dim", [(1, 4, 128), (1, 1, 64), (20, 4, 128), (64, 8, 64), (2, 8, 256), (30, 3, 256)])
 def test_attn_long_sequences_in_parts(kq, tokens, group, dim):
     """Long and short sequences together: the long ones are cut into parts, the
