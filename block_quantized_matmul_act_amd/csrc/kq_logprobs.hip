@@ -20,7 +20,9 @@
 //
 // A row is cut into parts where there are too few rows to fill the chip; each
 // part leaves (m, s, t) and its n largest, and a second kernel joins them.
-// Bound: HBM bandwidth (each logit is read once).
+// Bound: HBM bandwidth (each logit is read once): 1537 rows of 100277 fp32 logits with 8
+// alternatives in 109 us, 5.6 TB/s (a batch loaded a turn ahead: 118 us without).  One
+// row of 128256 with 20 alternatives: 8 us and 7 for the join, bound by latency.
 #include "kq_step_device.hpp"
 
 namespace kq {
