@@ -56,6 +56,10 @@ SIGNATURES = {
     "kq_variant_name": (ctypes.c_char_p, [_I]),
     "kq_dispatch_count": (ctypes.c_uint64, [_I]),
     "kq_dispatch_reset": (None, []),
+    "kq_num_step_variants": (_I, []),
+    "kq_step_variant_name": (ctypes.c_char_p, [_I]),
+    "kq_step_count": (ctypes.c_uint64, [_I]),
+    "kq_step_count_reset": (None, []),
     "kq_select_variant": (_I, [_I, _I64, _I64, _I64]),
     "kq_calib_launch": (_I, [_I, _I, _P, _I64, ctypes.POINTER(ctypes.c_double), _P]),
     "kq_rope_append": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _F, _P, _I64, _I64, _I, _P, _I, _P, _P]),
@@ -269,6 +273,23 @@ def kq_logprobs(type, logits, M, V, ldx, tokens, n_given, n_top, logprob, entrop
                                     _stream(stream)), "kq_logprobs")
 
 
+def kq_num_step_variants():
+    return lib().kq_num_step_variants()
+
+
+def kq_step_variant_name(v):
+    s = lib().kq_step_variant_name(v)
+    return s.decode() if s else None
+
+
+def kq_step_count(v):
+    return lib().kq_step_count(v)
+
+
+def kq_step_count_reset():
+    lib().kq_step_count_reset()
+
+
 def kq_strerror(status):
     return lib().kq_strerror(status).decode()
 
@@ -278,6 +299,10 @@ def kq_version():
 
 
 # ------------------------------------------------- torch conveniences (allocation)
+
+def step_counts() -> dict:
+    return {kq_step_variant_name(v): kq_step_count(v) for v in range(kq_num_step_variants())}
+
 
 def dispatch_counts() -> dict:
     return {kq_variant_name(v): kq_dispatch_count(v) for v in range(kq_num_variants())}

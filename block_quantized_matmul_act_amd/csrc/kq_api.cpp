@@ -12,11 +12,40 @@
 #include "kq_calib.hpp"
 #include "kq_hooks.hpp"
 #include "kq_launch.hpp"
-#include "kq_variants.hpp"
 
 namespace {
 
-using namespace kq;
+enum Variant {
+    V_QUANT_Q8K = 0,
+    V_QUANT_Q8_128,
+    V_GEMM_Q4K_128x128,
+    V_GEMM_Q4K_MATVEC,
+    V_GEMM_Q6K_128x128,
+    V_GEMM_Q6K_MATVEC,
+    V_GEMM_TQ_128x128,
+    V_GEMM_TQ_MATVEC,
+    V_SUBSUMS_Q4K,
+    V_SUBSUMS_Q6K,
+    V_SUBSUMS_TQ,
+    V_GEMM_TQ2_128x128,
+    V_SUBSUMS_TQ2,
+    V_GEMM_ID_128x128,
+    V_GEMM_Q4K_64x128,
+    V_GEMM_ID_Q4K_64x128,
+    V_GEMM_Q4K_64x128_K2,
+    V_GEMM_Q4K_M16,
+    V_GEMM_TQ_128x128_REG,
+    V_GEMM_Q4K_M64_RING,
+    V_GEMM_Q6K_RING,
+    V_GEMM_TQ2_RING,
+    V_GEMM_TQ_RING,
+    V_GEMM_Q4K_RING_KP,
+    V_GEMM_TQ2_MATVEC,
+    V_GEMM_Q6K_128x128_K2,
+    V_GEMM_TQ_128x128_K2,
+    V_GEMM_TQ2_128x128_K2,
+    V_COUNT
+};
 
 const char *const kVariantNames[V_COUNT] = {
     "quant_q8_k",        "quant_q8_128",    "gemm_q4_k_128x128", "gemm_q4_k_matvec",
@@ -25,7 +54,6 @@ const char *const kVariantNames[V_COUNT] = {
     "gemm_id_q4_k_64x128", "gemm_q4_k_64x128_k2", "gemm_q4_k_m16", "gemm_tq_128x128_reg", "gemm_q4_k_m64_ring",
     "gemm_q6_k_ring", "gemm_tq2_ring", "gemm_tq_ring", "gemm_q4_k_ring_kp", "gemm_tq2_matvec",
     "gemm_q6_k_128x128_k2", "gemm_tq_128x128_k2", "gemm_tq2_128x128_k2",
-    "rope_append", "attn_few", "attn_rows", "cache_keep", "logprobs_row", "logprobs_parts",
 };
 
 std::atomic<uint64_t> g_count[V_COUNT];
@@ -122,10 +150,6 @@ int variant_for(int fmt, int64_t M, int64_t N, int64_t K) {
 }
 
 }  // namespace
-
-namespace kq {
-void count_dispatch(int variant) { g_count[variant].fetch_add(1); }
-}  // namespace kq
 
 extern "C" {
 

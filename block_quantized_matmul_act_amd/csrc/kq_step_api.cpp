@@ -4,6 +4,7 @@
 // a status without touching the runtime.
 #include "../../include/kq.h"
 
+#include <atomic>
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -11,7 +12,6 @@
 #include <cstdint>
 
 #include "kq_step.hpp"
-#include "kq_variants.hpp"
 
 namespace {
 
@@ -79,6 +79,12 @@ int check_attn(const kq_cache *c, const kq_batch *s, int64_t q_heads, int64_t ma
     return 1;
 }
 
+// Successful calls by variant, as kq.h numbers them.
+enum StepVariant { V_ROPE_APPEND, V_ATTN_FEW, V_ATTN_ROWS, V_CACHE_KEEP, V_LOGPROBS_ROW, V_LOGPROBS_PARTS, V_COUNT };
+const char *const kNames[V_COUNT] = {"rope_append", "attn_few", "attn_rows", "cache_keep", "logprobs_row", "logprobs_parts"};
+std::atomic<uint64_t> g_count[V_COUNT];
+void count_step(int variant) { g_count[variant].fetch_add(1); }
+
 }  // namespace
 
 namespace kq {
@@ -134,6 +140,15 @@ LogprobsPlan logprobs_plan(int64_t M, int64_t V, int64_t n_top) {
 
 extern "C" {
 
+int kq_num_step_variants(void) { return V_COUNT; }
+const char *kq_step_variant_name(int variant) {
+    return variant >= 0 && variant < V_COUNT ? kNames[variant] : nullptr;
+}
+uint64_t kq_step_count(int variant) { return variant >= 0 && variant < V_COUNT ? g_count[variant].load() : 0; }
+void kq_step_count_reset(void) {
+    for (auto &c : g_count) c.store(0);
+}
+
 int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x, int64_t ldx, int64_t q_heads,
                    const float *q_norm, const float *k_norm, float eps, const float *rope, int64_t n_pos,
                    int64_t rot_dim, int pairs, const int32_t *positions, int q_type, void *q, hipStream_t stream) {
@@ -174,7 +189,7 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
     a.positions = positions;
     a.q = static_cast<char *>(q);
     if (launch_rope_append(a, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
-    count_dispatch(V_ROPE_APPEND);
+    count_step(V_ROPE_APPEND);
     return KQ_OK;
 }
 
@@ -223,7 +238,7 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     a.grid = p.grid;
     a.unit_shift = p.unit_shift;
     if (launch_attn(a, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
-    count_dispatch(p.waves == 0 ? V_ATTN_FEW : V_ATTN_ROWS);
+    count_step(p.waves == 0 ? V_ATTN_FEW : V_ATTN_ROWS);
     return KQ_OK;
 }
 
@@ -259,7 +274,7 @@ int kq_cache_keep(const kq_cache *caches, int64_t n_caches, const kq_batch *batc
             a.v[j] = static_cast<char *>(caches[i + (j < n ? j : 0)].v);
         }
         if (launch_keep(a, n, caches->type == KQ_T_F8 ? 1 : 2, caches->dim, stream) != hipSuccess) return KQ_ERR_HIP;
-        count_dispatch(V_CACHE_KEEP);
+        count_step(V_CACHE_KEEP);
     }
     return KQ_OK;
 }
@@ -302,7 +317,7 @@ int kq_logprobs(int type, const void *logits, int64_t M, int64_t V, int64_t ldx,
     a.top_logprobs = top_logprobs;
     a.ws = static_cast<char *>(workspace);
     if (launch_logprobs(a, type, M, stream) != hipSuccess) return KQ_ERR_HIP;
-    count_dispatch(p.parts == 1 ? V_LOGPROBS_ROW : V_LOGPROBS_PARTS);
+    count_step(p.parts == 1 ? V_LOGPROBS_ROW : V_LOGPROBS_PARTS);
     return KQ_OK;
 }
 

@@ -385,6 +385,15 @@ int kq_logprobs(int type, const void *logits, int64_t M, int64_t V, int64_t ldx,
 /* Workspace bytes of that call (0: none needed); 0 for invalid arguments. */
 size_t kq_logprobs_workspace(int64_t M, int64_t V, int64_t n_top);
 
+/* Counters of the step operators' variants (launched successfully) and their
+ * names: rope_append, attn_few (up to 16 rows to a key head), attn_rows (more),
+ * cache_keep, logprobs_row (rows whole), logprobs_parts.  The counters further
+ * down are those of the products. */
+int kq_num_step_variants(void);
+const char *kq_step_variant_name(int variant);
+uint64_t kq_step_count(int variant);
+void kq_step_count_reset(void);
+
 /* Per-variant dispatch counters (incremented on each successful launch) and
  * their names, so tests can prove which kernel variant ran (vllm.cpp PR 3036
  * added such counters after finding tests that never reached a variant). */

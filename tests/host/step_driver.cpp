@@ -8,9 +8,9 @@
 
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 
 #include "../../block_quantized_matmul_act_amd/csrc/kq_step.hpp"
-#include "../../block_quantized_matmul_act_amd/csrc/kq_variants.hpp"
 
 namespace {
 int failures = 0;
@@ -22,7 +22,7 @@ int failures = 0;
         }                                                                \
     } while (0)
 
-int ropes = 0, attns = 0, keeps = 0, logs = 0, counted[kq::V_COUNT];
+int ropes = 0, attns = 0, keeps = 0, logs = 0;
 kq::AttnArgs attn;
 kq::AttnPlan plan;
 kq::KeepArgs keep;
@@ -31,7 +31,6 @@ kq::LogprobsArgs lp;
 }  // namespace
 
 namespace kq {
-void count_dispatch(int v) { ++counted[v]; }
 hipError_t launch_rope_append(const RopeArgs &, int, int, int, hipStream_t) {
     ++ropes;
     return hipSuccess;
@@ -54,6 +53,13 @@ hipError_t launch_logprobs(const LogprobsArgs &a, int, int64_t, hipStream_t) {
     return hipSuccess;
 }
 }  // namespace kq
+
+// calls counted under a variant's name
+int counted(const char *name) {
+    for (int v = 0; v < kq_num_step_variants(); ++v)
+        if (!std::strcmp(kq_step_variant_name(v), name)) return (int)kq_step_count(v);
+    return -1;
+}
 
 int main() {
     char *const A = reinterpret_cast<char *>((uintptr_t)1 << 20);
@@ -132,9 +138,12 @@ int main() {
             EXPECT(bytes == (lp.parts > 1 ? (size_t)((M * lp.parts * 12 + 7) / 8 * 8 + M * lp.parts * 8 * 7) : 0));
             if (bytes) EXPECT(kq_logprobs(KQ_T_BF16, A, M, V, V, I, 2, 7, F, nullptr, I, F, A, bytes - 1, nullptr) == KQ_ERR_SHAPE);
         }
-    EXPECT(ropes == counted[kq::V_ROPE_APPEND] && keeps == counted[kq::V_CACHE_KEEP]);
-    EXPECT(attns == counted[kq::V_ATTN_FEW] + counted[kq::V_ATTN_ROWS]);
-    EXPECT(logs == counted[kq::V_LOGPROBS_ROW] + counted[kq::V_LOGPROBS_PARTS]);
+    EXPECT(ropes == counted("rope_append"));
+    EXPECT(attns == counted("attn_few") + counted("attn_rows"));
+    EXPECT(logs == counted("logprobs_row") + counted("logprobs_parts") && keeps == counted("cache_keep"));
+    EXPECT(!kq_step_variant_name(-1) && !kq_step_variant_name(kq_num_step_variants()));
+    kq_step_count_reset();
+    EXPECT(counted("rope_append") == 0 && kq_step_count(-1) == 0);
     if (failures) return 1;
     std::puts("ok");
     return 0;

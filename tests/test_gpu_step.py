@@ -506,7 +506,7 @@ def test_logprobs_past_two_gigabytes(kq):
 # --------------------------------------------------------------- all of a step
 
 def test_variants_are_counted(kq):
-    kq.kq_dispatch_reset()
+    kq.kq_step_count_reset()
     step = Step(1, [40, 3], [1, 1], 16)
     cache = kq.PagedCache(*(t.to(DEV) for t in ref.empty_cache(step.n_pages, 1, 16, 64, F16, 0.0)))
     q = kq.rope_append(cache, step.batch(kq), torch.ones((2, 10 * 64), device=DEV), 8)
@@ -516,5 +516,5 @@ def test_variants_are_counted(kq):
     kq.logprobs(torch.zeros((2, 100), device=DEV))
     kq.logprobs(torch.zeros((2, 10000), device=DEV))
     torch.cuda.synchronize()
-    n = kq.dispatch_counts()
+    n = kq.step_counts()
     assert [n[v] for v in ("rope_append", "attn_few", "attn_rows", "cache_keep", "logprobs_row", "logprobs_parts")] == [1] * 6

@@ -225,3 +225,13 @@ def test_argument_handling_under_sanitizers(tmp_path):
                     os.path.join(ROOT, "block_quantized_matmul_act_amd", "csrc", "kq_step_api.cpp"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=dict(os.environ, ASAN_OPTIONS="detect_leaks=1"))
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-4000:]
+
+
+def test_step_variants_named_and_counted(kq):
+    names = [kq.kq_step_variant_name(v) for v in range(kq.kq_num_step_variants())]
+    assert names == ["rope_append", "attn_few", "attn_rows", "cache_keep", "logprobs_row", "logprobs_parts"]
+    assert kq.kq_step_variant_name(len(names)) is None and kq.kq_step_variant_name(-1) is None
+    assert kq.kq_step_count(-1) == kq.kq_step_count(len(names)) == 0
+    kq.kq_step_count_reset()
+    assert set(kq.step_counts().values()) == {0}
+    assert not set(names) & set(kq.dispatch_counts())  # the products' counters are apart
