@@ -883,7 +883,10 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
         tl.load_k(next);
         tl.load_v(next);
         next = tl.find(pc.from + KEYS);
-        at.begin(sq, pc.h, pc.rb * a.rows_wg + wave * RW);
+        const int row0 = pc.rb * a.rows_wg + wave * RW;
+        // (a wave without rows only stages: trees of 5 tokens by 4 heads over 16k slots 77 -> 65 us)
+        const bool rows = row0 < sq.T * a.group;
+        at.begin(sq, pc.h, row0);
         __syncthreads();  // the piece before has been read
         tl.store_k(lds, 0);
         if (tl.store_v(lds, TL::K_BYTES, pc.from)) odd = 1;
@@ -893,7 +896,7 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
         int buf = 0;
         for (int key0 = pc.from; key0 < to; key0 += KEYS) {
             __syncthreads();
-            at.tile(lds, buf, key0, sq.len);
+            if (rows) at.tile(lds, buf, key0, sq.len);
             buf = TL::BYTES - buf;
             if (key0 + KEYS < to) {
                 tl.store_k(lds, buf);
