@@ -379,13 +379,14 @@ def gemm_id(fmt, W, n_experts, a_q8, M, N, K, expert_offsets, rows, out=None, st
 # one test each of device, type, shape and layout, and the message is worked out
 # only for one that is not.
 
-_types = _current_stream = _step = None
+_types = _current_stream = _step = _torch = None
 
 
 def _step_lib():
-    """The library's entry points of the step, and torch's types, once."""
-    global _types, _current_stream, _step
+    """The library's entry points of the step, torch and its types, once."""
+    global _types, _current_stream, _step, _torch
     import torch
+    _torch = torch
     _types = {torch.float32: KQ_T_F32, torch.bfloat16: KQ_T_BF16, torch.float16: KQ_T_F16,
               torch.float8_e4m3fn: KQ_T_F8}
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -475,18 +476,23 @@ class Batch:
     __slots__ = ("offsets", "lens", "pages", "device", "c", "at")
 
     def __init__(self, offsets, lens, pages):
-        import torch
-        i32 = torch.int32
+        if _torch is None:
+            _step_lib()
+        i32 = _torch.int32
         n = lens.shape[0]
         wide = pages.shape[-1]
         self.offsets, self.lens, self.pages = offsets, lens, pages
         self.device = device = lens.get_device()
-        self.c = c = kq_batch(_tensor(offsets, i32, (n + 1,), device, "Batch offsets"),
-                              _tensor(lens, i32, (n,), device, "Batch lens"),
-                              _tensor(pages, i32, (n, wide), device, "Batch pages"), n, 0, wide)
-        self.at = ctypes.addressof(c)
-        if device < 0:
+        if not (device >= 0 and offsets.dtype is i32 and lens.dtype is i32 and pages.dtype is i32 and lens.dim() == 1
+                and offsets.shape == (n + 1,) and pages.shape == (n, wide) and offsets.get_device() == device
+                and pages.get_device() == device and offsets.is_contiguous() and lens.is_contiguous()
+                and pages.is_contiguous()):
+            _tensor(offsets, i32, (n + 1,), device, "Batch offsets")
+            _tensor(lens, i32, (n,), device, "Batch lens")
+            _tensor(pages, i32, (n, wide), device, "Batch pages")
             raise ValueError("Batch: expected device tensors")
+        self.c = c = kq_batch(offsets.data_ptr(), lens.data_ptr(), pages.data_ptr(), n, 0, wide)
+        self.at = ctypes.addressof(c)
 
 
 def _together(device, cache, batch, where):
@@ -500,7 +506,7 @@ def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None
     returned as [n_tokens][q_heads][dim] (q_dtype: the cache's, bfloat16 for an
     8-bit cache); k normed and rotated, and v, stored in the cache's slots of the
     rows.  rope: float32 [n_pos][rot_dim], the cosines and then the sines."""
-    import torch
+    torch = _torch
     if stream is not None:
         with _on(stream, x.device):
             return rope_append(cache, batch, x, q_heads, rope, positions, q_norm, k_norm, eps, pairs, q_dtype, out)
@@ -540,7 +546,7 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
     name (int64 [n_tokens], bit j: the j-th new row; None: the rows up to its
     own).  max_tokens / max_len: upper bounds of a sequence's new rows and of its
     whole length (default: what the pages hold).  out_dtype: q's or float32."""
-    import torch
+    torch = _torch
     if stream is not None:
         with _on(stream, q.device):
             return attn_tree(cache, batch, q, mask, scale, max_tokens, max_len, out_dtype, out)
@@ -577,8 +583,7 @@ def cache_keep(caches, batch, path, counts, stream=None):
     """Keep an accepted branch in every cache of a list (one per layer): slot
     lens[b] + j takes what slot lens[b] + path[offsets[b] + j] held, j < counts[b]
     (int32 [n_tokens] and [n_seqs])."""
-    import torch
-    i32, device, n = torch.int32, path.get_device(), len(caches)
+    i32, device, n = _torch.int32, path.get_device(), len(caches)
     if device < 0 or path.dim() != 1:
         _refuse(path, i32, (None,), device, "cache_keep path")
     pp = _tensor(path, i32, path.shape, device, "cache_keep path")
@@ -609,7 +614,9 @@ def logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     """Log probabilities of tokens [M][n_given] (int32) under logits [M][V]
     (float32, bfloat16 or float16; rows may lie apart), the entropy of each row,
     and the n_top largest logits' indices and log probabilities."""
-    import torch
+    if _torch is None:
+        _step_lib()
+    torch = _torch
     if stream is not None:
         with _on(stream, logits.device):
             return logprobs(logits, tokens, n_top, entropy)
