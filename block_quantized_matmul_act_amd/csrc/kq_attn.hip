@@ -34,8 +34,11 @@ namespace kq {
 
 namespace {
 
-constexpr float M_START = -1e30f;  // below every score, and finite: exp2(-inf - m) is 0, not NaN
+constexpr float M_START = -3.402823466e38f;  // no finite score is below it; finite: exp2(-inf - m) is 0, not NaN
 constexpr float M_SLACK = 8.f;
+// From here on the rounding of score * scale (half of 2^-23 of it) is felt in exp2 of
+// its distance from m, and further out passes every type: see far.
+constexpr float M_FAR = 1048576.f;
 
 typedef float v2f __attribute__((ext_vector_type(2)));
 
@@ -596,6 +599,10 @@ struct Attend {
     op_t qf[NK];
     acc_t o[ND];
     float m, l;
+    // Some row's m is beyond M_FAR: the scores are then scaled first and m is taken
+    // from them after (in one fma m is rounded and the product it came from is not).
+    // The same for the whole wave; set where m is.
+    bool far;
 
     __device__ __forceinline__ Attend(const AttnArgs &a_) : a(a_) {
         lane = threadIdx.x & 63;
@@ -632,6 +639,7 @@ struct Attend {
         for (int d = 0; d < ND; ++d) o[d] = acc_t{};
         m = M_START;
         l = 0.f;
+        far = false;
     }
     // Matrix products of one stream: with VALUES the probabilities pf times the values
     // at byte v of the LDS are added to the sums, with SCORES p gets the scores of
@@ -700,15 +708,21 @@ struct Attend {
             l *= f;
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] *= f;
+            far = __any(fabsf(m) >= M_FAR && m > M_START);  // (M_START: a row that has seen nothing)
+        }
+        if (far) {
+#pragma unroll
+            for (int r = 0; r < NT * NR; ++r) p[r] *= a.score_scale;
         }
     }
     // The probabilities of step s of the second product.
     __device__ __forceinline__ op_t probabilities(const float (&p)[NT * NR], int s) {
         v4u w;
+        const float by = far ? 1.f : a.score_scale;  // (far: scaled already)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], a.score_scale, -m));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], a.score_scale, -m));
+            const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], by, -m));
+            const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], by, -m));
             l += p0 + p1;
             w[j] = pack2<E>(p0, p1);
         }

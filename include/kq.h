@@ -334,8 +334,8 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  *         same type or KQ_T_F8 (converted to q's type, exactly)
  *   out   [n_tokens][q_heads][dim], q's type or KQ_T_F32 (the same sums before
  *         the last rounding)
- * Scores, maxima and sums are fp32; the probabilities enter the second product
- * in q's type.  max_tokens is an upper bound of the rows of a sequence (rows
+ * Scores, maxima and sums are fp32, of any size that fp32 holds; the
+ * probabilities enter the second product in q's type.  max_tokens is an upper bound of the rows of a sequence (rows
  * past it are not computed) and max_len of lens[b] + its rows (slots past it
  * are not read): they size the launch.  The workspace holds the partial sums of
  * the parts a long sequence is cut into; the same call gives the same bits.

@@ -1,0 +1,108 @@
+"""GPU tests of the step operators at the edges of their ranges: scores far
+from zero, probabilities below the type's smallest, more rows than the call
+allows, arrays that break the contract, many sequences over shared pages."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+import step_ref as ref
+from step_ref import BF16, F16, F32, F8, Step
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def kq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import block_quantized_matmul_act_amd as kq
+    kq.lib()
+    return kq
+
+
+def up(a):
+    return (a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))).to(DEV)
+
+
+def i32(a):
+    return torch.tensor(a, dtype=torch.int32, device=DEV)
+
+
+# rows to a key head: one wave (whole sequences and parts), 4 waves, 8 waves
+ROWS = [(1, 2), (5, 3), (6, 8), (40, 4)]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tokens,group", ROWS)
+@pytest.mark.parametrize("qt,q0,k0", [(BF16, 1.0, 2.0 ** 34), (BF16, 1.0, -2.0 ** 34), (BF16, 2.0 ** 50, -2.0 ** 56),
+                                      (BF16, 2.0 ** 50, 2.0 ** 56), (F16, 2.0 ** 15, -2.0 ** 14), (F16, 2.0 ** 15, 2.0 ** 14)],
+                         ids=str)
+@pytest.mark.parametrize("peak", [False, True])
+def test_attn_scores_far_from_zero(kq, dim, tokens, group, qt, q0, k0, peak):
+    """Every other token scores all its keys alike at 2^30 to 2^106 either side of
+    zero (a value whose product with the scale is rounded): it gets the mean of the
+    values it sees, or where one key scores more that key's value.  The rows
+    between have ordinary scores over the same keys.
+
+    Equal scores weigh the same, so the weights are exact and what remains is
+    fp32's sum of n <= 1400 values: each is off by half of 2^-23 of the sum of
+    magnitudes at most, and the sums of a lane or a product are added in fewer than
+    128 turns: 2^-17 of it."""
+    lens, new = [1300, 0, 70, 129], [tokens, tokens, max(1, tokens // 2), tokens]
+    step = Step(tokens + dim, lens, new, 32)
+    k, v = (t.float() for t in ref.fill_cache(step, 2, dim, qt))
+    k[..., 0] = k0 * (1 + 2.0 ** -6)
+    at_peak = [1203, None, 5, 128]
+    if peak:
+        for b, s in enumerate(at_peak):
+            if s is not None:
+                p, at = step.where(b, [s])
+                k[p, :, at, 0] *= 2.0 if k0 > 0 else 0.5
+    k, v = k.to(qt), v.to(qt)
+    q = ref.draw(step.rng, (step.M, 2 * group, dim), 0.3)
+    far = np.concatenate([np.arange(n) % 2 == 0 for n in new])
+    q[far] = 0.0
+    q[:, :, 0] = 0.0
+    q[far, :, 0] = q0 * (1 + 2.0 ** -7)
+    q = q.to(qt)
+    bits = np.concatenate([ref.chain_mask(n) for n in new])
+    scale = 1.0 / 3.0
+    k_near = k.clone()
+    k_near[..., 0] = 0.0
+    want, bound = ref.attn(step, k_near, v, q, bits, scale)   # (for far rows: the mean over equal scores)
+    for b in range(4):
+        for i in range(new[b]):
+            if i % 2 == 0:
+                row = int(step.offsets[b]) + i
+                p, at = step.where(b, np.arange(lens[b] + i + 1))
+                for h in range(2):
+                    vv = v[p, h, :, at].double()
+                    if peak and at_peak[b] is not None:
+                        vv = vv[at_peak[b]][None]
+                    want[row, h * group:(h + 1) * group] = vv.mean(0)
+                    bound[row, h * group:(h + 1) * group] = 2.0 ** -17 * vv.abs().mean(0)
+    for max_len in (step.max_len, 1 << 14):
+        got = kq.attn_tree(kq.PagedCache(up(k), up(v)), step.batch(kq), up(q), scale=scale, max_tokens=tokens,
+                           max_len=max_len, out_dtype=F32).cpu().double()
+        assert torch.isfinite(got).all()
+        assert ((got - want).abs() <= bound).all(), ((got - want).abs() / bound)[far].max()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attn_short_sequence_scores_far_from_zero(kq, dim):
+    """The same where a workgroup takes a short sequence whole."""
+    step = Step(1, [700], [1], 64)
+    k, v = ref.fill_cache(step, 1, dim, BF16)
+    k[..., 0] = -2.0 ** 100
+    q = torch.zeros((1, 2, dim))
+    q[:, :, 0] = 1.25 * 2.0 ** 5
+    got = kq.attn_tree(kq.PagedCache(up(k), up(v)), step.batch(kq), up(q.to(BF16)), scale=0.7, max_tokens=1, max_len=701,
+                       out_dtype=F32).cpu().double()
+    p, at = step.where(0, np.arange(701))
+    vv = v[p, 0, :, at].double()
+    assert ((got - vv.mean(0)).abs() <= 2.0 ** -17 * vv.abs().mean(0)).all()
