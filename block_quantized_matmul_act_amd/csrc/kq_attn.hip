@@ -19,6 +19,15 @@
 // units): until then exp2(S - m) stays within 2^8, far inside every type, and
 // neither a cross-lane maximum nor a rescaling of O is needed.
 //
+// P enters the second product in q's type, since the matrix cores take two 16-bit
+// operands (fp32 ones run at a sixteenth of the rate, P in two halves would double
+// the products): each probability is off by up to 2^-8 (bfloat16) or 2^-11
+// (float16) of it, where the output's own rounding is as much of the whole.  float16 has no
+// normal numbers below 2^-14, and many small probabilities beside a dominant one can
+// weigh more than a rounding, so there m is kept 7 below the maximum it is raised
+// to: P begins at 2^7, stays within 2^15, and loses bits from 2^-21 of the dominant
+// one down (131071 keys 25 below one: 1.9e-3 off without, 7e-5 with).
+//
 // A wave holds the sums of RW query rows (16 or 32).
 //
 // How the work is shared: a unit is 128 (short sequences: 1024) slots of one (sequence, key head, block
@@ -35,7 +44,11 @@ namespace kq {
 namespace {
 
 constexpr float M_START = -3.402823466e38f;  // no finite score is below it; finite: exp2(-inf - m) is 0, not NaN
-constexpr float M_SLACK = 8.f;
+// m: how far below a row's maximum, and how far a score may pass it
+template <class E>
+constexpr float M_BELOW = std::is_same_v<E, _Float16> ? 7.f : 0.f;
+template <class E>
+constexpr float M_SLACK = M_BELOW<E> + 8.f;
 // From here on the rounding of score * scale (half of 2^-23 of it) is felt in exp2 of
 // its distance from m, and further out passes every type: see far.
 constexpr float M_FAR = 1048576.f;
@@ -700,9 +713,9 @@ struct Attend {
 #pragma unroll
         for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
         top *= a.score_scale;
-        if (__any(top > m + M_SLACK)) {
+        if (__any(top - m > M_SLACK<E>)) {  // (exact where it is near; P past the slack could be infinite)
             top = groups_max<RW>(top);
-            const float up = fmaxf(m, top);
+            const float up = fmaxf(m, top - M_BELOW<E>);
             const float f = __builtin_amdgcn_exp2f(m - up);
             m = up;
             l *= f;
@@ -715,15 +728,16 @@ struct Attend {
             for (int r = 0; r < NT * NR; ++r) p[r] *= a.score_scale;
         }
     }
-    // The probabilities of step s of the second product.
-    __device__ __forceinline__ op_t probabilities(const float (&p)[NT * NR], int s) {
+    // The probabilities of step s of the second product, their sum to `sum` (a tile's,
+    // which then goes to l at once: one by one, small ones would be lost beside it).
+    __device__ __forceinline__ op_t probabilities(const float (&p)[NT * NR], int s, float &sum) {
         v4u w;
         const float by = far ? 1.f : a.score_scale;  // (far: scaled already)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], by, -m));
             const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], by, -m));
-            l += p0 + p1;
+            sum += p0 + p1;
             w[j] = pack2<E>(p0, p1);
         }
         return __builtin_bit_cast(op_t, w);
@@ -733,8 +747,10 @@ struct Attend {
         op_t pf[NS];
         products<false, true, 4>(lds, 0, pf, buf, p);
         raise(key0, len, p);
+        float sum = 0.f;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) pf[s] = probabilities(p, s);
+        for (int s = 0; s < NS; ++s) pf[s] = probabilities(p, s, sum);
+        l += sum;
         products<true, false, 4>(lds, buf + TL::K_BYTES, pf, 0, p);
     }
     // What infinite and NaN values of drafted tokens among keys [from, to) add; at a
@@ -986,12 +1002,14 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs a) {
         if (late) __syncthreads();
         auto vector_half = [&](int i, int before, int after) {
             at.raise(key0, sq.len, p);
+            float sum = 0.f;
 #pragma unroll
             for (int s = 0; s < AT::NS; ++s) {
-                v4u w = __builtin_bit_cast(v4u, at.probabilities(p, s));
+                v4u w = __builtin_bit_cast(v4u, at.probabilities(p, s, sum));
                 asm volatile("" : "+v"(w));  // (now, while the loads for the staging below arrive)
                 pf[s] = __builtin_bit_cast(typename AT::op_t, w);
             }
+            at.l += sum;
             if (i + 1 < tiles) {
                 tl.store_k(lds, before);  // keys i + 2
                 if (tl.store_v(lds, after + TL::K_BYTES, key0 + KEYS)) odd = 1;

@@ -106,3 +106,34 @@ def test_attn_short_sequence_scores_far_from_zero(kq, dim):
     p, at = step.where(0, np.arange(701))
     vv = v[p, 0, :, at].double()
     assert ((got - vv.mean(0)).abs() <= 2.0 ** -17 * vv.abs().mean(0)).all()
+
+
+@pytest.mark.parametrize("tokens,group,heads,seqs", [(1, 1, 8, 64), (8, 4, 8, 64), (64, 4, 8, 32)], ids=["one", "rows", "wide"])
+def test_attn_f16_small_probabilities_count(kq, tokens, group, heads, seqs):
+    """One key 25.05 log2 units above 131071 alike, all values 1: the result is 1,
+    although every other probability is below float16's smallest number and
+    together they weigh 0.4%.  (All sequences share two pages.)
+
+    A wave holds up to N keys: all of them, or where 4 waves take turns a quarter
+    with a dominant key for each.  The dominant one has weight 2^7, exactly; of the
+    others each is off by 2^-25 (half the spacing of subnormals), so N 2^-32 of the
+    dominant; the sums in fp32 are off by 2^-23 of it at most for every product that
+    is added (16 keys with waves of 32 rows, 32 with waves of 16) and for every
+    tile of 64 keys that is added to the weights' sum."""
+    n, dim, page = 131072, 64, 256
+    k = torch.zeros((2, heads, page, dim), dtype=F16)
+    few = tokens * group <= 16
+    k[1, :, [0, 64, 128, 192] if few else [0], 0] = 1.0
+    v = torch.ones((2, heads, dim, page), dtype=F16)
+    pages = torch.zeros((seqs, n // page), dtype=torch.int32)
+    pages[:, 0] = 1
+    q = torch.zeros((seqs * tokens, heads * group, dim), dtype=F16)
+    q[..., 0] = 1.0
+    batch = kq.Batch(i32(np.arange(seqs + 1) * tokens), i32([n - tokens] * seqs), up(pages))
+    got = kq.attn_tree(kq.PagedCache(up(k), up(v)), batch, up(q), scale=25.05 * math.log(2.0), max_tokens=tokens,
+                       max_len=n, out_dtype=F32)
+    N = n // 4 if few else n
+    tol = N * 2.0 ** -32 + N / (32 if few else 16) * 2.0 ** -23 + N / 64 * 2.0 ** -23
+    err = (got - 1.0).abs().max().item()
+    print(f"{n} keys, {tokens * group} rows: off by {err:.3g} of {tol:.3g}", flush=True)
+    assert err <= tol, (err, tol)
