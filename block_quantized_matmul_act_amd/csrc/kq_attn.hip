@@ -16,8 +16,8 @@
 //
 // One pass over the keys with the running maximum m and sum l of a softmax in
 // fp32.  m is raised only when a score passes it by more than 8 (in log2
-// units): until then exp2(S - m) stays within 2^8, far inside every type, and
-// neither a cross-lane maximum nor a rescaling of O is needed.
+// units): until then exp2(S - m) stays within 2^8 of what it began at, and neither
+// a cross-lane maximum nor a rescaling of O is needed.
 //
 // P enters the second product in q's type, since the matrix cores take two 16-bit
 // operands (fp32 ones run at a sixteenth of the rate, P in two halves would double
@@ -26,7 +26,9 @@
 // normal numbers below 2^-14, and many small probabilities beside a dominant one can
 // weigh more than a rounding, so there m is kept 7 below the maximum it is raised
 // to: P begins at 2^7, stays within 2^15, and loses bits from 2^-21 of the dominant
-// one down (131071 keys 25 below one: 1.9e-3 off without, 7e-5 with).
+// one down (131071 keys 25 below one: 1.9e-3 off without, 7e-5 with).  bfloat16 has
+// fp32's range: there m is 20 above the maximum, so that sums of P times values stay
+// in fp32 where their mean does (P from 2^-20 to 2^-12).
 //
 // A wave holds the sums of RW query rows (16 or 32).
 //
@@ -44,9 +46,9 @@ namespace kq {
 namespace {
 
 constexpr float M_START = -3.402823466e38f;  // no finite score is below it; finite: exp2(-inf - m) is 0, not NaN
-// m: how far below a row's maximum, and how far a score may pass it
+// m: how far below a row's maximum it is set, and how far a score may pass it
 template <class E>
-constexpr float M_BELOW = std::is_same_v<E, _Float16> ? 7.f : 0.f;
+constexpr float M_BELOW = std::is_same_v<E, _Float16> ? 7.f : -20.f;
 template <class E>
 constexpr float M_SLACK = M_BELOW<E> + 8.f;
 // From here on the rounding of score * scale (half of 2^-23 of it) is felt in exp2 of

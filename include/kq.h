@@ -335,13 +335,11 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  *   out   [n_tokens][q_heads][dim], q's type or KQ_T_F32 (the same sums before
  *         the last rounding)
  * Scores, maxima and sums are fp32, of any size that fp32 holds; the
- * probabilities enter the second product in q's type, a row's largest as 1 to
- * 2^8 (bfloat16) or 2^7 to 2^15 (float16), and the values are summed with these
- * weights before they are divided by the weights' sum (so bfloat16 values near
- * the end of the type's range may overflow).  max_tokens is an upper bound of the rows of a sequence (rows past it are
- * not computed) and max_len of lens[b] + its rows (slots past it are not read):
- * they size the launch.  The workspace holds the partial sums of
- * the parts a long sequence is cut into; the same call gives the same bits.
+ * probabilities enter the second product in q's type.  max_tokens is an upper
+ * bound of the rows of a sequence (rows past it are not computed) and max_len of
+ * lens[b] + its rows (slots past it are not read): they size the launch.  The
+ * workspace holds the partial sums of the parts a long sequence is cut into; the
+ * same call gives the same bits.
  * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31.
  */
 #define KQ_ATTN_MAX_TOKENS 64

@@ -137,3 +137,24 @@ def test_attn_f16_small_probabilities_count(kq, tokens, group, heads, seqs):
     err = (got - 1.0).abs().max().item()
     print(f"{n} keys, {tokens * group} rows: off by {err:.3g} of {tol:.3g}", flush=True)
     assert err <= tol, (err, tol)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tokens,group", ROWS)
+def test_attn_values_near_the_ends_of_the_range(kq, dim, tokens, group):
+    """bfloat16 values of 1e38 either sign, whose weighted mean is as far from
+    overflow as each of them, and of 1e-30."""
+    lens, new = [1300, 0, 129, 2], [tokens, tokens, max(1, tokens // 2), tokens]
+    step = Step(tokens + dim, lens, new, 32)
+    k, v = ref.fill_cache(step, 2, dim, BF16)
+    q = ref.draw(step.rng, (step.M, 2 * group, dim), 1.5).to(BF16)
+    bits = np.concatenate([ref.chain_mask(n) for n in new])
+    for size in (1e38, 1e-30):
+        ends = torch.where(v.isnan(), v, torch.where(v > -1.0, size, -size).to(BF16))
+        want, bound = ref.attn(step, k, ends, q, bits, dim ** -0.5)
+        for out in (F32, BF16):
+            got = kq.attn_tree(kq.PagedCache(up(k), up(ends)), step.batch(kq), up(q), max_tokens=tokens, max_len=step.max_len,
+                               out_dtype=out).cpu().double()
+            tol = bound if out == F32 else ref.rounded_bound(want, bound, out)
+            assert torch.isfinite(got).all()
+            assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
