@@ -495,9 +495,11 @@ class Batch:
         self.at = ctypes.addressof(c)
 
 
-def _together(device, cache, batch, where):
+def _together(device, cache, batch, rows, where):
     if cache.device != device or batch.device != device:
         raise ValueError(f"{where}: tensors on devices {device}, {cache.device} and {batch.device}")
+    if rows and not batch.c.n_seqs:
+        raise ValueError(f"{where}: {rows} rows of no sequence")
 
 
 def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None, k_norm=None, eps=1e-6, pairs=False,
@@ -515,8 +517,8 @@ def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None
     px, ldx = _rows(x, (q_heads + 2 * heads) * dim, device, "rope_append x")
     if x.dtype is not f32:
         _refuse(x, f32, x.shape, device, "rope_append x")
-    _together(device, cache, batch, "rope_append")
     M = x.shape[0]
+    _together(device, cache, batch, M, "rope_append")
     if out is None:
         if q_dtype is None:
             q_dtype = torch.bfloat16 if c.type == KQ_T_F8 else cache.dtype
@@ -544,8 +546,9 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
     """Attention of q [n_tokens][q_heads][dim] over the cache, each row over its
     sequence's cached tokens and those of its new rows that its bits in mask
     name (int64 [n_tokens], bit j: the j-th new row; None: the rows up to its
-    own).  max_tokens / max_len: upper bounds of a sequence's new rows and of its
-    whole length (default: what the pages hold).  out_dtype: q's or float32."""
+    own).  max_tokens / max_len: upper bounds of a sequence's new rows (past it:
+    refused where the host can tell, else NaN) and of its whole length (default: what
+    the pages hold).  out_dtype: q's or float32."""
     torch = _torch
     if stream is not None:
         with _on(stream, q.device):
@@ -555,7 +558,7 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
     if device < 0 or q.dim() != 3 or q.shape[2] != dim or not q.is_contiguous():
         _refuse(q, q_dtype, (None, None, dim), device, "attn_tree q")
     M, heads, _ = shape = q.shape
-    _together(device, cache, batch, "attn_tree")
+    _together(device, cache, batch, M, "attn_tree")
     if out is None:
         out = torch.empty_like(q) if out_dtype is None else torch.empty(shape, dtype=out_dtype, device=q.device)
         po = out.data_ptr()
@@ -590,7 +593,7 @@ def cache_keep(caches, batch, path, counts, stream=None):
     pc = _tensor(counts, i32, (batch.c.n_seqs,), device, "cache_keep counts")
     for c in caches:
         if c.device != device:
-            _together(device, c, batch, "cache_keep")
+            _together(device, c, batch, 0, "cache_keep")
     if batch.device != device:
         raise ValueError(f"cache_keep: tensors on devices {device} and {batch.device}")
     batch.c.n_tokens = path.shape[0]

@@ -251,12 +251,12 @@ struct Frag<E, true> {
 // A sequence as the kernels see it: rows and slots held inside the step and the
 // bounds of the call.
 struct Seq {
-    int first, T, len, total;
+    int first, rows, T, len, total;  // T of the rows are computed
 };
 __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b) {
     Seq q;
-    batch_rows(a.batch, b, q.first, q.T);
-    q.T = min(q.T, a.max_tokens);
+    batch_rows(a.batch, b, q.first, q.rows);
+    q.T = min(q.rows, a.max_tokens);
     q.len = min(max(a.batch.lens[b], 0), a.max_len);
     q.total = min(q.len + q.T, a.max_len);
     return q;
@@ -266,12 +266,15 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b) {
 // for one key head and how many come before.
 struct Share {
     int chunk, before, incl, all, tiles, blocks;
+    bool more;  // the sequence has more rows than the call allows
 };
 __device__ __forceinline__ void share_chunk(const AttnArgs &a, Share &s, int chunk) {
     const int lane = threadIdx.x & 63, b = chunk * 64 + lane;
     int tiles = 0, blocks = 0;
+    s.more = false;
     if (b < a.batch.n_seqs) {
         const Seq q = seq_of(a, b);
+        s.more = q.rows > q.T;
         tiles = q.T ? (q.total + (1 << a.unit_shift) - 1) >> a.unit_shift : 0;
         blocks = (q.T * a.group + a.rows_wg - 1) / a.rows_wg;
     }
@@ -288,17 +291,33 @@ __device__ __forceinline__ void share_chunk(const AttnArgs &a, Share &s, int chu
     s.blocks = blocks;
 }
 __device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+// The output of rows past the bound of the call: NaN, by the whole grid together.
+__device__ __forceinline__ void put_past(const AttnArgs &a, const Share &s, int dim) {
+    uint64_t more = __ballot(s.more);
+    if (!more) return;
+    const int pieces = a.cache.heads * a.group * dim / (a.out_f32 ? 4 : 8);  // of 16 bytes, to a row
+    const v4u nan = {0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};    // of every type
+    for (; more; more &= more - 1) {
+        const Seq q = seq_of(a, s.chunk * 64 + __ffsll((unsigned long long)more) - 1);
+        v4u *out = reinterpret_cast<v4u *>(a.out) + (int64_t)(q.first + q.T) * pieces;
+        const int64_t n = (int64_t)(q.rows - q.T) * pieces;
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+            out[i] = nan;
+    }
+}
 // all the units of one key head, and the first chunk; one wave of the grid notes
 // them for the kernel that joins the parts
-__device__ __forceinline__ Share share_of(const AttnArgs &a) {
+__device__ __forceinline__ Share share_of(const AttnArgs &a, int dim) {
     Share s;
     share_chunk(a, s, 0);
+    put_past(a, s, dim);
     s.before = 0;
     s.all = last_lane(s.incl);
     if (a.batch.n_seqs > 64) {
         Share t;
         for (int c = 1; c * 64 < a.batch.n_seqs; ++c) {
             share_chunk(a, t, c);
+            put_past(a, t, dim);
             s.all += last_lane(t.incl);
         }
     }
@@ -801,7 +820,7 @@ __global__ __launch_bounds__(WAVES * 64, D == 256 || WAVES == 8 ? 1 : 2) void at
     __shared__ __align__(1024) char lds[WAVES * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
     __shared__ float lm[WAVES * RW], ll[WAVES * RW];
 
-    Share share = share_of(a);
+    Share share = share_of(a, D);
     const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
     if ((int)blockIdx.x >= groups) return;
     const Runs runs(units, groups);
@@ -895,7 +914,7 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
     __shared__ __align__(1024) char lds[2 * TL::BYTES];
     __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
 
-    Share share = share_of(a);
+    Share share = share_of(a, D);
     const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
     if ((int)blockIdx.x >= groups) return;
     const Runs runs(units, groups);
@@ -966,7 +985,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs a) {
     __shared__ __align__(1024) char lds[3 * TL::BYTES];  // keys and values by turns
     __shared__ int odd;  // whether drafted tokens staged so far have infinite or NaN values
 
-    Share share = share_of(a);
+    Share share = share_of(a, D);
     const int heads = a.cache.heads, units = share.all * heads, groups = min((int)gridDim.x, units);
     if ((int)blockIdx.x >= groups) return;
     const Runs runs(units, groups);

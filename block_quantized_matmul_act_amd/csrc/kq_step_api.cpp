@@ -73,6 +73,7 @@ int check_attn(const kq_cache *c, const kq_batch *s, int64_t q_heads, int64_t ma
     if (rc == KQ_OK) return KQ_OK;
     if (s->n_tokens * q_heads >= ((int64_t)1 << 31) / c->dim) return KQ_ERR_UNSUPPORTED;
     if (max_tokens == 0 || max_len == 0) return KQ_ERR_SHAPE;  // rows to compute, none allowed
+    if (s->n_tokens > s->n_seqs * max_tokens) return KQ_ERR_SHAPE;  // some sequence has more
     // the kernels count units in int32: at most a row block to every 16 rows
     const int64_t blocks = (max_tokens * (q_heads / c->heads) + 15) / 16;
     if (s->n_seqs > kMaxInt / (c->heads * ((max_len + ATTN_UNIT - 1) / ATTN_UNIT) * blocks)) return KQ_ERR_UNSUPPORTED;

@@ -336,10 +336,11 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  *         the last rounding)
  * Scores, maxima and sums are fp32, of any size that fp32 holds; the
  * probabilities enter the second product in q's type.  max_tokens is an upper
- * bound of the rows of a sequence (rows past it are not computed) and max_len of
- * lens[b] + its rows (slots past it are not read): they size the launch.  The
- * workspace holds the partial sums of the parts a long sequence is cut into; the
- * same call gives the same bits.
+ * bound of the rows of a sequence (more rows than n_seqs sequences can have by it
+ * are refused; a sequence's rows past it come out as NaN) and max_len of lens[b] +
+ * its rows (slots past it are not read): they size the launch.  The workspace
+ * holds the partial sums of the parts a long sequence is cut into; the same call
+ * gives the same bits.
  * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31.
  */
 #define KQ_ATTN_MAX_TOKENS 64

@@ -158,3 +158,27 @@ def test_attn_values_near_the_ends_of_the_range(kq, dim, tokens, group):
             tol = bound if out == F32 else ref.rounded_bound(want, bound, out)
             assert torch.isfinite(got).all()
             assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
+@pytest.mark.parametrize("dim,group,T", [(64, 2, 4), (128, 6, 6), (256, 4, 9), (128, 8, 20)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_attn_rows_past_the_bound_are_nan(kq, dim, group, T, out):
+    """Rows of a sequence past max_tokens come out as NaN, the others as without
+    them, in more sequences than a wave has lanes."""
+    rng = np.random.default_rng(T)
+    new = rng.integers(0, T + 1, 70)
+    new[[0, 31, 66]] = T + 3, T + 1, 2 * T
+    step = Step(T, rng.integers(0, 200, 70), new, 16)
+    k, v = ref.fill_cache(step, 1, dim, BF16)
+    q = ref.draw(step.rng, (step.M, group, dim)).to(BF16)
+    bits = np.concatenate([ref.chain_mask(min(int(n), 64)) for n in new])
+    past = np.concatenate([np.arange(n) >= T for n in new])
+    want, bound = ref.attn(step, k, v, q, bits, dim ** -0.5)
+    whole = torch.full((step.M + 2, group, dim), 7.0, dtype=out, device=DEV)
+    kq.attn_tree(kq.PagedCache(up(k), up(v)), step.batch(kq), up(q), max_tokens=T, max_len=step.max_len, out=whole[1:-1])
+    got = whole.cpu().double()
+    assert (got[[0, -1]] == 7).all()
+    got = got[1:-1]
+    assert torch.isnan(got[past]).all()
+    tol = bound if out == F32 else ref.rounded_bound(want, bound, out)
+    assert ((got - want).abs() <= tol)[~past].all()
