@@ -379,18 +379,19 @@ def gemm_id(fmt, W, n_experts, a_q8, M, N, K, expert_offsets, rows, out=None, st
 # one test each of device, type, shape and layout, and the message is worked out
 # only for one that is not.
 
-_types = _current_stream = _step = _torch = None
+_types = _current_stream = _current_device = _step = _torch = None
 
 
 def _step_lib():
     """The library's entry points of the step, torch and its types, once."""
-    global _types, _current_stream, _step, _torch
+    global _types, _current_stream, _current_device, _step, _torch
     import torch
     _torch = torch
     _types = {torch.float32: KQ_T_F32, torch.bfloat16: KQ_T_BF16, torch.float16: KQ_T_F16,
               torch.float8_e4m3fn: KQ_T_F8}
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _step = lib()
     return _step
 
@@ -440,12 +441,20 @@ def _type(dtype, where):
 
 
 def _on(stream, device):
-    """A context in which a stream (a torch stream or a raw handle) is torch's
-    current one: what is allocated in it belongs to that stream, so neither the
-    results nor the workspace can be handed to other work that it overtakes."""
-    import torch
+    """A context in which the tensors' device is the current one (kernels go to the
+    current device, and a handle of 0 is its default stream), and a stream, if one
+    is given (a torch stream or a raw handle), torch's current one there: what is
+    allocated in it belongs to that stream, so neither the results nor the workspace
+    can be handed to other work that it overtakes."""
+    torch = _torch
+    if device < 0:
+        raise ValueError("expected device tensors")
+    if stream is None:
+        return torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    if stream.device_index != device:
+        raise ValueError(f"a stream of device {stream.device_index} for tensors on device {device}")
     return torch.cuda.stream(stream)
 
 
@@ -508,11 +517,11 @@ def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None
     returned as [n_tokens][q_heads][dim] (q_dtype: the cache's, bfloat16 for an
     8-bit cache); k normed and rotated, and v, stored in the cache's slots of the
     rows.  rope: float32 [n_pos][rot_dim], the cosines and then the sines."""
-    torch = _torch
-    if stream is not None:
-        with _on(stream, x.device):
+    torch, device = _torch, x.get_device()
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
             return rope_append(cache, batch, x, q_heads, rope, positions, q_norm, k_norm, eps, pairs, q_dtype, out)
-    f32, c, device = torch.float32, cache.c, x.get_device()
+    f32, c = torch.float32, cache.c
     heads, dim = c.heads, c.dim
     px, ldx = _rows(x, (q_heads + 2 * heads) * dim, device, "rope_append x")
     if x.dtype is not f32:
@@ -549,11 +558,11 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
     own).  max_tokens / max_len: upper bounds of a sequence's new rows (past it:
     refused where the host can tell, else NaN) and of its whole length (default: what
     the pages hold).  out_dtype: q's or float32."""
-    torch = _torch
-    if stream is not None:
-        with _on(stream, q.device):
+    torch, device = _torch, q.get_device()
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
             return attn_tree(cache, batch, q, mask, scale, max_tokens, max_len, out_dtype, out)
-    c, device, q_dtype = cache.c, q.get_device(), q.dtype
+    c, q_dtype = cache.c, q.dtype
     dim = c.dim
     if device < 0 or q.dim() != 3 or q.shape[2] != dim or not q.is_contiguous():
         _refuse(q, q_dtype, (None, None, dim), device, "attn_tree q")
@@ -587,6 +596,9 @@ def cache_keep(caches, batch, path, counts, stream=None):
     lens[b] + j takes what slot lens[b] + path[offsets[b] + j] held, j < counts[b]
     (int32 [n_tokens] and [n_seqs])."""
     i32, device, n = _torch.int32, path.get_device(), len(caches)
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
+            return cache_keep(caches, batch, path, counts)
     if device < 0 or path.dim() != 1:
         _refuse(path, i32, (None,), device, "cache_keep path")
     pp = _tensor(path, i32, path.shape, device, "cache_keep path")
@@ -603,8 +615,7 @@ def cache_keep(caches, batch, path, counts, stream=None):
         every = (kq_cache * n)(*[c.c for c in caches])
         at = ctypes.addressof(every)
     step = _step or _step_lib()
-    _check(step.kq_cache_keep(at, n, batch.at, pp, pc, _current_stream(device) if stream is None else _stream(stream)),
-           "kq_cache_keep")
+    _check(step.kq_cache_keep(at, n, batch.at, pp, pc, _current_stream(device)), "kq_cache_keep")
 
 
 class LogProbs:
@@ -619,11 +630,10 @@ def logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     and the n_top largest logits' indices and log probabilities."""
     if _torch is None:
         _step_lib()
-    torch = _torch
-    if stream is not None:
-        with _on(stream, logits.device):
+    torch, device = _torch, logits.get_device()
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
             return logprobs(logits, tokens, n_top, entropy)
-    device = logits.get_device()
     px, ldx = _rows(logits, None, device, "logprobs logits")
     M, V = logits.shape
     kind, dev = _type(logits.dtype, "logprobs logits"), logits.device

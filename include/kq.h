@@ -21,6 +21,8 @@
  *     kq_logprobs take a workspace whose size a query gives.
  *   - Work is enqueued asynchronously on `stream` (NULL = the default
  *     stream).  Device faults surface at the caller's next synchronization.
+ *     The device of the pointers and of the stream is the calling thread's
+ *     current device.
  *   - Arguments are validated on the host before any HIP call.  On any error
  *     nothing is launched and a negative KQ_ERR_* code is returned; a shape
  *     with no verified kernel variant is declined with KQ_ERR_UNSUPPORTED

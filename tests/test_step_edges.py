@@ -2,6 +2,9 @@
 can tell of a call is refused, whatever the arrays on the device hold."""
 from __future__ import annotations
 
+import contextlib
+import types
+
 import pytest
 
 from test_step_abi import A, attn, batch, cache, kq  # noqa: F401
@@ -51,10 +54,66 @@ def test_attn_more_rows_than_the_bound_allows(kq, seqs, tokens, bound):  # noqa:
     assert kq.kq_attn_tree_workspace(cache(kq), s, 4, bound, 100000) > 0
 
 
-def test_rows_of_no_sequence(kq):  # noqa: F811
+def test_rows_of_no_sequence(kq, devices):  # noqa: F811
     """Nothing would compute them, and what comes back would be what lay in memory."""
     c, b, x, q = step_args(kq, 3, 0)
     with pytest.raises(ValueError, match="no sequence"):
         kq.rope_append(c, b, x, 4, out=q)
     with pytest.raises(ValueError, match="no sequence"):
         kq.attn_tree(c, b, q, out=q)
+
+
+@pytest.fixture
+def devices(kq, monkeypatch):  # noqa: F811
+    """Two devices of which 0 is current; the library notes which one is current
+    when it is called, and whose stream it is given."""
+    now, calls = [0], []
+    kq._step_lib()
+
+    @contextlib.contextmanager
+    def switch(device):
+        before, now[0] = now[0], device
+        yield
+        now[0] = before
+
+    def call(*args):
+        calls.append((now[0], args[-1]))
+        return 0
+
+    names = ("kq_rope_append", "kq_attn_tree", "kq_cache_keep", "kq_logprobs")
+    spaces = ("kq_attn_tree_workspace", "kq_logprobs_workspace")
+    fake = types.SimpleNamespace(**{n: call for n in names}, **{n: lambda *a: 0 for n in spaces})
+    monkeypatch.setattr(kq, "_step", fake)
+    monkeypatch.setattr(kq, "_current_device", lambda: now[0])
+    monkeypatch.setattr(kq, "_current_stream", lambda device: 100 + device)
+    monkeypatch.setattr(torch.cuda, "device", switch)
+    return now, calls
+
+
+def calls_on(kq, device):  # noqa: F811
+    c, b, x, q = step_args(kq, 3, 3, device)
+    i32 = lambda *n: Tensor(torch.int32, *n, device=device)  # noqa: E731
+    logits = Tensor(torch.float32, 3, 50, device=device)
+    return [lambda **kw: kq.rope_append(c, b, x, 4, out=q, **kw), lambda **kw: kq.attn_tree(c, b, q, out=q, **kw),
+            lambda **kw: kq.cache_keep([c], b, i32(3), i32(3), **kw),
+            lambda **kw: kq.logprobs(logits, i32(3, 2), n_top=1, **kw)]
+
+
+@pytest.mark.parametrize("device", [0, 1])
+def test_calls_run_on_their_tensors_device(kq, devices, device):  # noqa: F811
+    now, seen = devices
+    for call in calls_on(kq, device):
+        call()
+    assert seen == [(device, 100 + device)] * 4 and now == [0]
+
+
+def test_stream_of_another_device(kq, devices):  # noqa: F811
+    for call in calls_on(kq, 1):
+        with pytest.raises(ValueError, match="stream of device 0"):
+            call(stream=types.SimpleNamespace(device_index=0, cuda_stream=7))
+    assert not devices[1]
+
+
+def test_stream_with_host_tensors(kq):  # noqa: F811
+    with pytest.raises(ValueError, match="device tensors"):
+        kq.logprobs(torch.zeros(2, 10), stream=5)
