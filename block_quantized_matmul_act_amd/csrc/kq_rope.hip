@@ -271,25 +271,15 @@ __global__ __launch_bounds__(256) void rope_append_kernel(const RopeArgs a, int 
     if (row < a.batch.n_tokens) RO::template heads<GROUPS>(a, row, (item - row * waves) * HEADS);
 }
 
-template <class E, bool F8, int D, int TT, int GROUPS>
-hipError_t launch_sized(const RopeArgs &a, hipStream_t stream) {
-    const int kv = a.cache.heads;
-    constexpr int HEADS = Rope<E, F8, D>::HPW * GROUPS;
-    const int64_t value_blocks = (int64_t)((a.batch.n_tokens + TT - 1) / TT) * kv;
-    const int64_t waves = (a.q_heads + kv + HEADS - 1) / HEADS;
-    const int64_t blocks = value_blocks + (waves * a.batch.n_tokens + 3) / 4;
-    hipLaunchKernelGGL((rope_append_kernel<E, F8, D, TT, GROUPS>), dim3((unsigned)blocks), dim3(256), 0, stream, a,
-                       (int)value_blocks);
-    return hipGetLastError();
-}
-
 template <class E, bool F8, int D>
 hipError_t launch(const RopeArgs &a, hipStream_t stream) {
-    // Fewer values: as many waves and tiles as there can be.  More: tiles of 64 rows,
-    // of which all but the ends are whole runs, and two groups of heads to a wave
-    // (1k rows of 48 heads of 128: 11 us and 14; 2k of 40: 18 and 16; 12k of 40: 105 and 93).
-    const int64_t values = (int64_t)a.batch.n_tokens * (a.q_heads + a.cache.heads) * D;
-    return values < (1 << 23) ? launch_sized<E, F8, D, 16, 1>(a, stream) : launch_sized<E, F8, D, 64, 2>(a, stream);
+    const RopePlan p = rope_plan(a.batch.n_tokens, a.q_heads, a.cache.heads, D);
+    const dim3 grid((unsigned)p.blocks);
+    if (p.tile == 16)
+        hipLaunchKernelGGL((rope_append_kernel<E, F8, D, 16, 1>), grid, dim3(256), 0, stream, a, (int)p.value_blocks);
+    else
+        hipLaunchKernelGGL((rope_append_kernel<E, F8, D, 64, 2>), grid, dim3(256), 0, stream, a, (int)p.value_blocks);
+    return hipGetLastError();
 }
 
 template <class E, bool F8>

@@ -21,6 +21,10 @@ struct BatchArgs {
     int n_seqs, n_tokens, max_pages;
 };
 
+// A launch counts its threads along a dimension in 32 bits, and workgroups here
+// have at least this many.
+constexpr int64_t MAX_GROUPS = UINT32_MAX / 256;
+
 struct RopeArgs {
     CacheArgs cache;
     BatchArgs batch;
@@ -34,6 +38,24 @@ struct RopeArgs {
     const int32_t *positions;
     char *q;
 };
+// How many rows of values a workgroup takes and how many groups of 512 / dim heads a
+// wave.  Fewer values: as many waves and tiles as there can be.  More: tiles of 64
+// rows, of which all but the ends are whole runs, and two groups of heads to a wave
+// (1k rows of 48 heads of 128: 11 us and 14; 2k of 40: 18 and 16; 12k of 40: 105 and 93).
+struct RopePlan {
+    int tile, groups;
+    int64_t value_blocks, blocks;  // workgroups of values, and all
+};
+inline RopePlan rope_plan(int64_t n_tokens, int64_t q_heads, int64_t heads, int dim) {
+    RopePlan p;
+    const bool few = n_tokens * (q_heads + heads) * dim < (1 << 23);
+    p.tile = few ? 16 : 64;
+    p.groups = few ? 1 : 2;
+    const int64_t wave_heads = 512 / dim * p.groups, waves = (q_heads + heads + wave_heads - 1) / wave_heads;
+    p.value_blocks = (n_tokens + p.tile - 1) / p.tile * heads;
+    p.blocks = p.value_blocks + (waves * n_tokens + 3) / 4;
+    return p;
+}
 // type / q_type: KQ_T_*; dim: 64, 128 or 256 (checked by the caller)
 hipError_t launch_rope_append(const RopeArgs &a, int type, int dim, int q_type, hipStream_t stream);
 

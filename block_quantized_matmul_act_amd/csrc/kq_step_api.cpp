@@ -170,8 +170,10 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(rope, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
         !aligned(positions, 4))
         return KQ_ERR_ALIGN;
-    // workgroups: at most a wave to a head and row, and 16 rows to a value head
-    if (batch->n_tokens > kMaxInt / (q_heads + 2 * cache->heads)) return KQ_ERR_UNSUPPORTED;
+    // waves are counted in int32: at most one to a head and row
+    if (batch->n_tokens > kMaxInt / (q_heads + 2 * cache->heads) ||
+        rope_plan(batch->n_tokens, q_heads, cache->heads, cache->dim).blocks > MAX_GROUPS)
+        return KQ_ERR_UNSUPPORTED;
     RopeArgs a;
     a.cache = cache_args(cache);
     a.batch = batch_args(batch);
@@ -213,6 +215,7 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     rc = check_step(cache, batch);
     if (rc != KQ_OK) return rc;
     const AttnPlan p = attn_plan(*cache, batch->n_seqs, q_heads, max_tokens, max_len);
+    if (p.bytes && batch->n_tokens > MAX_GROUPS) return KQ_ERR_UNSUPPORTED;  // a workgroup to a row joins the parts
     if (!q || !out || (p.bytes && !workspace)) return KQ_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 8) || !aligned(workspace, 16)) return KQ_ERR_ALIGN;
     if (workspace_bytes < (size_t)p.bytes) return KQ_ERR_SHAPE;
@@ -257,6 +260,7 @@ int kq_cache_keep(const kq_cache *caches, int64_t n_caches, const kq_batch *batc
     int rc = check_batch(batch);
     if (rc <= 0) return rc;
     if (n_caches == 0) return KQ_OK;
+    if (batch->n_seqs > MAX_GROUPS) return KQ_ERR_UNSUPPORTED;  // a workgroup to a sequence (and head and cache)
     for (int64_t i = 0; i < n_caches; ++i) {
         rc = check_step(caches + i, batch);
         if (rc != KQ_OK) return rc;
@@ -295,7 +299,7 @@ int kq_logprobs(int type, const void *logits, int64_t M, int64_t V, int64_t ldx,
     if (V == 0 || n_top > V) return KQ_ERR_SHAPE;
     if (n_top > KQ_LOGPROBS_MAX_TOP) return KQ_ERR_UNSUPPORTED;
     const LogprobsPlan p = logprobs_plan(M, V, n_top);
-    if (M > kMaxInt / p.parts) return KQ_ERR_UNSUPPORTED;
+    if (M > MAX_GROUPS / p.parts) return KQ_ERR_UNSUPPORTED;  // a workgroup to a part
     if (!logits || (n_given && (!tokens || !logprob)) || (n_top && (!top_ids || !top_logprobs)) ||
         (p.bytes && !workspace))
         return KQ_ERR_NULL;

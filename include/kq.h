@@ -315,7 +315,9 @@ typedef struct kq_batch {
  * in its text: in a tree of drafts several rows share one.  Positions outside
  * [0, n_pos) are taken at the nearest end.  The arithmetic is fp32, each
  * result rounded once (to nearest even).  Slots that no row belongs to keep what they
- * held.  Two rows must not share a slot.
+ * held.  Two rows must not share a slot.  Steps that would take 2^24 workgroups
+ * of 256 threads or more (a wave takes up to 1024 / dim heads of a row) are declined
+ * with KQ_ERR_UNSUPPORTED.
  */
 int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x, int64_t ldx,
                    int64_t q_heads, const float *q_norm, const float *k_norm, float eps,
@@ -343,7 +345,8 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  * its rows (slots past it are not read): they size the launch.  The workspace
  * holds the partial sums of the parts a long sequence is cut into; the same call
  * gives the same bits.
- * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31.
+ * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31, and
+ * n_tokens below 2^24 where there is a workspace.
  */
 #define KQ_ATTN_MAX_TOKENS 64
 int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q,
@@ -360,7 +363,7 @@ size_t kq_attn_tree_workspace(const kq_cache *cache, const kq_batch *batch, int6
  * lens[b] + path[offsets[b] + j] held before the call (path: int32 [n_tokens],
  * values in [0, rows of the sequence)), in the keys and values of every one of
  * the n_caches caches (host array; one per layer, alike in all but k and v).
- * The caller then counts counts[b] more tokens in the cache.
+ * The caller then counts counts[b] more tokens in the cache.  n_seqs below 2^24.
  */
 #define KQ_KEEP_MAX_TOKENS 64
 int kq_cache_keep(const kq_cache *caches, int64_t n_caches, const kq_batch *batch,
@@ -375,7 +378,8 @@ int kq_cache_keep(const kq_cache *caches, int64_t n_caches, const kq_batch *batc
  *   top_ids [M][n_top], top_logprobs [M][n_top]: the largest logits, the
  *                          lowest index first among equal ones
  * all fp32 (ids int32), from one pass over the logits.  n_given and n_top may
- * be 0; entropy may be NULL.  n_top is at most KQ_LOGPROBS_MAX_TOP and V.
+ * be 0; entropy may be NULL.  n_top is at most KQ_LOGPROBS_MAX_TOP and V; M times
+ * the parts of a row (one where M is 1024 or more) is below 2^24.
  * A logit of -infinity has no probability (and counts 0 in the entropy); a row
  * of nothing else, or with +infinity or a NaN in it, has no distribution: its
  * floats are NaN (-infinity for a t outside [0, V)), and a NaN leaves its ids

@@ -3,12 +3,16 @@ can tell of a call is refused, whatever the arrays on the device hold."""
 from __future__ import annotations
 
 import contextlib
+import os
+import shutil
+import subprocess
 import types
 
 import pytest
 
-from test_step_abi import A, attn, batch, cache, kq  # noqa: F401
+from test_step_abi import A, attn, batch, cache, keep, kq, logprobs, rope  # noqa: F401
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 torch = pytest.importorskip("torch")
 
 
@@ -117,3 +121,27 @@ def test_stream_of_another_device(kq, devices):  # noqa: F811
 def test_stream_with_host_tensors(kq):  # noqa: F811
     with pytest.raises(ValueError, match="device tensors"):
         kq.logprobs(torch.zeros(2, 10), stream=5)
+
+
+def test_launches_past_the_grid(kq):  # noqa: F811
+    """More workgroups of 256 threads than a launch can count threads for."""
+    n = 1 << 24
+    one = dict(heads=1, dim=64)
+    assert logprobs(kq, M=n, V=64, ldx=64) == kq.KQ_ERR_UNSUPPORTED
+    assert logprobs(kq, M=(1 << 31) - 1, V=1, ldx=1, n_top=0) == kq.KQ_ERR_UNSUPPORTED
+    assert rope(kq, cache(kq, **one), batch(kq, n_tokens=4 * n, n_seqs=n), q_heads=1, rot=0) == kq.KQ_ERR_UNSUPPORTED
+    assert keep(kq, cache(kq, **one), batch(kq, n_seqs=n)) == kq.KQ_ERR_UNSUPPORTED
+    assert attn(kq, cache(kq, **one), batch(kq, n_seqs=n, n_tokens=n), q_heads=1, max_tokens=1, max_len=129) == kq.KQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
+                    reason="g++ or the ROCm headers not available")
+def test_every_launch_that_is_let_through_fits_the_grid(tmp_path):
+    """kq_step_api.cpp with stubs for the launchers (tests/host/step_grids.cpp):
+    the workgroups of each launch at sizes around the limit."""
+    exe = str(tmp_path / "step_grids")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                    "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", os.path.join(ROOT, "tests", "host", "step_grids.cpp"),
+                    os.path.join(ROOT, "block_quantized_matmul_act_amd", "csrc", "kq_step_api.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-4000:]
