@@ -257,7 +257,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b) {
     Seq q;
     batch_rows(a.batch, b, q.first, q.rows);
     q.T = min(q.rows, a.max_tokens);
-    q.len = min(max(a.batch.lens[b], 0), a.max_len);
+    q.len = min(batch_len(a.batch, b), a.max_len);
     q.total = min(q.len + q.T, a.max_len);
     return q;
 }

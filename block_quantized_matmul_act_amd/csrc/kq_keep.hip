@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void keep_kernel(const KeepArgs a) {
     batch_rows(a.batch, b, first, rows);
     const int n = min(min(max(a.counts[b], 0), rows), MAX);
     if (n == 0) return;
-    const int len = max(a.batch.lens[b], 0);
+    const int len = batch_len(a.batch, b);
     const int shift = a.cache.page_shift;
     if (threadIdx.x < 2 * MAX) {
         const int which = threadIdx.x / MAX, j = threadIdx.x % MAX;

@@ -84,7 +84,7 @@ struct Rope {
             const int b = batch_seq(a.batch, row);
             int first, count;
             batch_rows(a.batch, b, first, count);
-            slot = max(a.batch.lens[b], 0) + (row - first);
+            slot = batch_len(a.batch, b) + (row - first);
             page = slot_page(a.cache, a.batch, b, slot);
         }
         const float *cs = a.rope;
@@ -177,7 +177,7 @@ struct Rope {
             if (row) {
                 int first, count;
                 batch_rows(a.batch, b, first, count);
-                const int slot = max(a.batch.lens[b], 0) + (row0 + lane - first);
+                const int slot = batch_len(a.batch, b) + (row0 + lane - first);
                 in = slot & ((1 << shift) - 1);
                 at = ((((int64_t)slot_page(a.cache, a.batch, b, slot) * kv + h) * D << shift) + in) * ES;
                 where[lane] = at;

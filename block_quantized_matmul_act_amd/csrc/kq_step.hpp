@@ -21,6 +21,9 @@ struct BatchArgs {
     int n_seqs, n_tokens, max_pages;
 };
 
+// Slots of a sequence: with as many rows of a step still an int.
+constexpr int MAX_LEN = 1 << 30;
+
 // A launch counts its threads along a dimension in 32 bits, and workgroups here
 // have at least this many.
 constexpr int64_t MAX_GROUPS = UINT32_MAX / 256;

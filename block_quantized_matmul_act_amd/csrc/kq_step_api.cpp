@@ -18,7 +18,7 @@ namespace {
 using namespace kq;
 
 constexpr int64_t kMaxInt = INT32_MAX;
-constexpr int64_t kMaxLen = (int64_t)1 << 30;  // slots of a sequence: int arithmetic with room to spare
+constexpr int64_t kMaxLen = MAX_LEN;
 constexpr int64_t kMaxPages = (int64_t)1 << 31;
 constexpr int64_t kMaxHeads = 65535;           // a grid's second dimension
 

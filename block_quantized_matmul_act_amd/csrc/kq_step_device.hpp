@@ -42,6 +42,9 @@ __device__ __forceinline__ void batch_rows(const BatchArgs &s, int b, int &first
     count = min(max(s.offsets[b + 1], first), s.n_tokens) - first;
 }
 
+// The tokens of sequence b in the cache, held where a row's slot does not overflow.
+__device__ __forceinline__ int batch_len(const BatchArgs &s, int b) { return min(max(s.lens[b], 0), MAX_LEN); }
+
 // The page of slot `slot` of sequence b: its entry in the table, held inside the
 // cache; a page outside the cache or a slot past the table gives a wrong page,
 // never one outside the cache.

@@ -292,7 +292,7 @@ typedef struct kq_cache {
  */
 typedef struct kq_batch {
     const int32_t *offsets; /* [n_seqs + 1], offsets[0] = 0, offsets[n_seqs] = n_tokens */
-    const int32_t *lens;    /* [n_seqs] */
+    const int32_t *lens;    /* [n_seqs], each up to 2^30 */
     const int32_t *pages;   /* [n_seqs][max_pages] */
     int64_t n_seqs, n_tokens, max_pages;
 } kq_batch;

@@ -182,3 +182,47 @@ def test_attn_rows_past_the_bound_are_nan(kq, dim, group, T, out):
     assert torch.isnan(got[past]).all()
     tol = bound if out == F32 else ref.rounded_bound(want, bound, out)
     assert ((got - want).abs() <= tol)[~past].all()
+
+
+@pytest.mark.parametrize("dim,kvt", [(64, F16), (128, F8), (256, BF16)])
+@pytest.mark.parametrize("M", [40, 12000])
+def test_append_and_keep_stay_inside(kq, dim, kvt, M):
+    """Offsets, lengths, pages, positions, paths and counts of nonsense, in a small
+    step and in one of whole tiles: what lies before and behind the cache and the
+    queries keeps its canaries."""
+    heads, q_heads, page, n = 2, 4, 16, 3
+    qt = BF16 if kvt == F8 else kvt
+
+    def guarded(shape, dtype):
+        pad = 64 * page   # rows of the shape's last dimension's neighbours on each side, a multiple of 16 bytes
+        size = math.prod(shape)
+        whole = torch.full((size + 2 * pad,), 7.0, dtype=F32, device=DEV).to(dtype)
+        return whole, whole[pad:pad + size].view(shape)
+
+    def untouched(whole, inner):
+        pad = (whole.numel() - inner.numel()) // 2
+        return bool((whole[:pad].float() == 7).all()) and bool((whole[-pad:].float() == 7).all())
+
+    low, high = -2 ** 31, 2 ** 31 - 1
+    arrays = [([0, 50, 3], [-9, 1 << 30], [[77, -3]] * 2),
+              ([5, -5, 1 << 30], [high, low], [[0, high]] * 2),
+              ([0, M // 2, M], [high, high], [[low, high]] * 2),
+              ([0, M // 2, M], [(1 << 30) + 1, high - M // 4], [[2, 1]] * 2),
+              ([high, low, high], [31, 17], [[high, 1]] * 2),
+              ([-3, -2, -1], [0, 31], [[-1, 3]] * 2)]
+    x = torch.ones((M, (q_heads + 2 * heads) * dim), device=DEV)
+    rope = torch.ones((5, dim), device=DEV)
+    for off, lens, pages in arrays:
+        print(off, lens, pages, flush=True)
+        guards = [guarded((n, heads, page, dim), kvt), guarded((n, heads, dim, page), kvt), guarded((M, q_heads, dim), qt)]
+        (_, k), (_, v), (_, q) = guards
+        cache, batch = kq.PagedCache(k, v), kq.Batch(i32(off), i32(lens), i32(pages))
+        for positions in (None, i32(([high, low, -1, 5] * M)[:M])):
+            kq.rope_append(cache, batch, x, q_heads, rope, positions, out=q)
+        torch.cuda.synchronize()
+        assert all(untouched(*g) for g in guards)
+        path = i32(([high, low, -1, 5, M] * M)[:M])
+        for counts in ([90, 3], [high, low], [64, 64]):
+            kq.cache_keep([cache], batch, path, i32(counts))
+        torch.cuda.synchronize()
+        assert all(untouched(*g) for g in guards)
