@@ -379,6 +379,7 @@ def gemm_id(fmt, W, n_experts, a_q8, M, N, K, expert_offsets, rows, out=None, st
 # one test each of device, type, shape and layout, and the message is worked out
 # only for one that is not.
 
+_addressof = ctypes.addressof
 _types = _current_stream = _current_device = _step = _torch = None
 
 
@@ -482,7 +483,7 @@ class PagedCache:
 class Batch:
     """The sequences of one step (int32 device tensors): offsets [n_seqs + 1] of
     their token rows, lens [n_seqs] tokens already cached, pages [n_seqs][max_pages]."""
-    __slots__ = ("offsets", "lens", "pages", "device", "c", "at")
+    __slots__ = ("offsets", "lens", "pages", "device", "c", "_last", "_spare")
 
     def __init__(self, offsets, lens, pages):
         if _torch is None:
@@ -501,7 +502,22 @@ class Batch:
             _tensor(pages, i32, (n, wide), device, "Batch pages")
             raise ValueError("Batch: expected device tensors")
         self.c = c = kq_batch(offsets.data_ptr(), lens.data_ptr(), pages.data_ptr(), n, 0, wide)
-        self.at = ctypes.addressof(c)
+        self._last, self._spare = None, [c]
+
+    def of(self, n_tokens):
+        """The descriptor of a step of n_tokens rows.  Calls with any number of rows (in
+        other threads, too) share this object, so a descriptor that a call may hold is
+        not changed: the first call takes the one that is there, others make one."""
+        c = self._last
+        if c is None or c.n_tokens != n_tokens:
+            try:
+                c = self._spare.pop()
+                c.n_tokens = n_tokens
+            except IndexError:
+                b = self.c
+                c = kq_batch(b.offsets, b.lens, b.pages, b.n_seqs, n_tokens, b.max_pages)
+            self._last = c
+        return c
 
 
 def _together(device, cache, batch, rows, where):
@@ -543,8 +559,8 @@ def rope_append(cache, batch, x, q_heads, rope=None, positions=None, q_norm=None
     pqn = None if q_norm is None else _tensor(q_norm, f32, (dim,), device, "rope_append q_norm")
     pkn = None if k_norm is None else _tensor(k_norm, f32, (dim,), device, "rope_append k_norm")
     pp = None if positions is None else _tensor(positions, torch.int32, (M,), device, "rope_append positions")
-    batch.c.n_tokens = M
-    _check((_step or _step_lib()).kq_rope_append(cache.at, batch.at, px, ldx, q_heads, pqn, pkn, eps, pr, n_pos, rot,
+    rows = batch.of(M)
+    _check((_step or _step_lib()).kq_rope_append(cache.at, _addressof(rows), px, ldx, q_heads, pqn, pkn, eps, pr, n_pos, rot,
                                                  1 if pairs else 0, pp, _type(q_dtype, "rope_append out"), pq,
                                                  _current_stream(device)), "kq_rope_append")
     return out
@@ -578,14 +594,15 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
         max_len = batch.c.max_pages * c.page
     if scale is None:
         scale = dim ** -0.5
-    batch.c.n_tokens = M
+    rows = batch.of(M)
+    at = _addressof(rows)
     step = _step or _step_lib()
-    need = step.kq_attn_tree_workspace(cache.at, batch.at, heads, max_tokens, max_len)
+    need = step.kq_attn_tree_workspace(cache.at, at, heads, max_tokens, max_len)
     work = pw = None
     if need:
         work = torch.empty(need, dtype=torch.uint8, device=q.device)
         pw = work.data_ptr()
-    _check(step.kq_attn_tree(cache.at, batch.at, _type(q_dtype, "attn_tree q"), q.data_ptr(), heads, pm, scale, max_tokens,
+    _check(step.kq_attn_tree(cache.at, at, _type(q_dtype, "attn_tree q"), q.data_ptr(), heads, pm, scale, max_tokens,
                              max_len, _type(out.dtype, "attn_tree out"), po, pw, need, _current_stream(device)),
            "kq_attn_tree")
     return out
@@ -608,14 +625,14 @@ def cache_keep(caches, batch, path, counts, stream=None):
             _together(device, c, batch, 0, "cache_keep")
     if batch.device != device:
         raise ValueError(f"cache_keep: tensors on devices {device} and {batch.device}")
-    batch.c.n_tokens = path.shape[0]
+    rows = batch.of(path.shape[0])
     if n == 1:
         at = caches[0].at
     else:
         every = (kq_cache * n)(*[c.c for c in caches])
         at = ctypes.addressof(every)
     step = _step or _step_lib()
-    _check(step.kq_cache_keep(at, n, batch.at, pp, pc, _current_stream(device)), "kq_cache_keep")
+    _check(step.kq_cache_keep(at, n, _addressof(rows), pp, pc, _current_stream(device)), "kq_cache_keep")
 
 
 class LogProbs:

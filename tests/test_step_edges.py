@@ -145,3 +145,34 @@ def test_every_launch_that_is_let_through_fits_the_grid(tmp_path):
                     os.path.join(ROOT, "block_quantized_matmul_act_amd", "csrc", "kq_step_api.cpp"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-4000:]
+
+
+def test_one_batch_with_other_row_counts(kq, devices, monkeypatch):  # noqa: F811
+    """While a call is under way (in another thread, say) the same batch serves
+    calls of other row counts: each has its own, to its end."""
+    c, b, x, q = step_args(kq, 3, 3)
+    _, _, more, q_more = step_args(kq, 5, 3)
+    rows = []
+
+    def n_tokens(at):
+        return kq.kq_batch.from_address(at).n_tokens
+
+    def append(cache, at, *a):
+        outer = len(rows) == 0
+        rows.append(n_tokens(at))
+        if outer:
+            kq.rope_append(c, b, more, 4, out=q_more)
+            kq.attn_tree(c, b, q_more, out=q_more)
+            kq.cache_keep([c], b, Tensor(torch.int32, 4), Tensor(torch.int32, 3))
+            rows.append(n_tokens(at))
+        return 0
+
+    def attend(cache, at, *a):
+        rows.append(n_tokens(at))
+        return 0
+
+    monkeypatch.setattr(kq._step, "kq_rope_append", append)
+    monkeypatch.setattr(kq._step, "kq_attn_tree", attend)
+    monkeypatch.setattr(kq._step, "kq_cache_keep", lambda caches, n, at, *a: rows.append(n_tokens(at)) or 0)
+    kq.rope_append(c, b, x, 4, out=q)
+    assert rows == [3, 5, 5, 4, 3]
