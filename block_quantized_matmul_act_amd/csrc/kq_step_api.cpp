@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -162,6 +163,8 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
     if (rot_dim < 0 || rot_dim > cache->dim || rot_dim % 8 || n_pos < 0 || n_pos > kMaxInt) return KQ_ERR_SHAPE;
     if (rot_dim && n_pos == 0 && work == 1) return KQ_ERR_SHAPE;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return KQ_ERR_SHAPE;
+    const float k_inv = 1.0f / cache->k_scale, v_inv = 1.0f / cache->v_scale;
+    if (!std::isfinite(k_inv) || !std::isfinite(v_inv)) return KQ_ERR_SHAPE;  // (0 times infinity were NaN)
     if (ldx % 4 || ldx < (q_heads + 2 * (int64_t)cache->heads) * cache->dim || ldx > kMaxLen) return KQ_ERR_SHAPE;
     if (work == KQ_OK) return KQ_OK;
     rc = check_step(cache, batch);
@@ -183,8 +186,8 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
     a.q_norm = q_norm;
     a.k_norm = k_norm;
     a.eps = eps;
-    a.k_inv = 1.0f / cache->k_scale;
-    a.v_inv = 1.0f / cache->v_scale;
+    a.k_inv = k_inv;
+    a.v_inv = v_inv;
     a.rope = rope;
     a.n_pos = (int)n_pos;
     a.rot = (int)rot_dim;
@@ -209,7 +212,9 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     if (rc != KQ_OK) return rc;
     if (!type16(q_type) || (cache->type != KQ_T_F8 && cache->type != q_type)) return KQ_ERR_FMT;
     if (out_type != q_type && out_type != KQ_T_F32) return KQ_ERR_FMT;
-    if (!std::isfinite(scale)) return KQ_ERR_SHAPE;
+    const double to_log2 = (double)scale * cache->k_scale * 1.44269504088896340736;
+    if (!(std::fabs(to_log2) <= FLT_MAX)) return KQ_ERR_SHAPE;
+    const float c = (float)to_log2;
     rc = check_attn(cache, batch, q_heads, max_tokens, max_len);
     if (rc <= 0) return rc;
     rc = check_step(cache, batch);
@@ -225,7 +230,6 @@ int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const
     a.q = static_cast<const char *>(q);
     a.group = (int)(q_heads / cache->heads);
     a.mask = mask;
-    const float c = (float)((double)scale * cache->k_scale * 1.44269504088896340736);
     a.q_keep = c == 0.f ? 0u : ~0u;
     a.q_flip = c < 0.f ? 0x80008000u : 0u;
     a.score_scale = c == 0.f ? 1.f : std::fabs(c);

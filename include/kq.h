@@ -276,7 +276,7 @@ typedef struct kq_cache {
     void *k, *v;
     int64_t n_pages;
     int32_t type, heads, dim, page;
-    float k_scale, v_scale; /* finite, > 0 */
+    float k_scale, v_scale; /* finite, > 0, for kq_rope_append with a finite inverse */
 } kq_cache;
 
 /*
@@ -346,7 +346,8 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  * holds the partial sums of the parts a long sequence is cut into; the same call
  * gives the same bits.
  * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31, and
- * n_tokens below 2^24 where there is a workspace.
+ * n_tokens below 2^24 where there is a workspace; scale * k_scale * log2(e) finite
+ * in fp32.
  */
 #define KQ_ATTN_MAX_TOKENS 64
 int kq_attn_tree(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q,

@@ -123,6 +123,15 @@ def test_stream_with_host_tensors(kq):  # noqa: F811
         kq.logprobs(torch.zeros(2, 10), stream=5)
 
 
+def test_scales_that_leave_fp32(kq):  # noqa: F811
+    """A cache scale without a finite inverse, a score scale that is infinite in
+    the kernel's units: zeros would come out as NaN."""
+    for bad in (dict(k_scale=1e-39), dict(v_scale=1e-39)):
+        assert rope(kq, cache(kq, **bad), batch(kq)) == kq.KQ_ERR_SHAPE
+    assert attn(kq, cache(kq), batch(kq), scale=3e38) == kq.KQ_ERR_SHAPE
+    assert attn(kq, cache(kq, k_scale=1e20), batch(kq), scale=-1e19) == kq.KQ_ERR_SHAPE
+
+
 def test_launches_past_the_grid(kq):  # noqa: F811
     """More workgroups of 256 threads than a launch can count threads for."""
     n = 1 << 24
