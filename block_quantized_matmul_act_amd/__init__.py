@@ -573,7 +573,9 @@ def attn_tree(cache, batch, q, mask=None, scale=None, max_tokens=KQ_ATTN_MAX_TOK
     name (int64 [n_tokens], bit j: the j-th new row; None: the rows up to its
     own).  max_tokens / max_len: upper bounds of a sequence's new rows (past it:
     refused where the host can tell, else NaN) and of its whole length (default: what
-    the pages hold).  out_dtype: q's or float32."""
+    the pages hold).  A longer prompt, appended whole, attends as several sequences
+    over its page row, the i-th with 64 i more cached tokens and the next 64 rows.
+    out_dtype: q's or float32."""
     torch, device = _torch, q.get_device()
     if stream is not None or (device >= 0 and device != _current_device()):
         with _on(stream, device):

@@ -345,6 +345,9 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  * its rows (slots past it are not read): they size the launch.  The workspace
  * holds the partial sums of the parts a long sequence is cut into; the same call
  * gives the same bits.
+ * A prompt of more rows, all of them appended, is several sequences here that share
+ * its page row: the i-th has lens + 64 i cached tokens and the next 64 rows (mask
+ * NULL).
  * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31, and
  * n_tokens below 2^24 where there is a workspace; scale * k_scale * log2(e) finite
  * in fp32.

@@ -226,3 +226,38 @@ def test_append_and_keep_stay_inside(kq, dim, kvt, M):
             kq.cache_keep([cache], batch, path, i32(counts))
         torch.cuda.synchronize()
         assert all(untouched(*g) for g in guards)
+
+
+@pytest.mark.parametrize("group,dim,qt,kvt", [(6, 128, BF16, BF16), (3, 64, F16, F8), (1, 256, BF16, BF16)])
+def test_attn_prompts_as_sequences_over_their_pages(kq, group, dim, qt, kvt):
+    """Prompts whose rows are all in the cache attend 64 at a time: sequence i of
+    a prompt has its pages, 64 i more cached tokens and the next 64 rows.  85 such
+    sequences are more than a wave has lanes, and 64 rows of 6 heads more than a
+    workgroup takes at once."""
+    lens, new, rows = [37, 0, 300], [4400, 200, 731], 64
+    step = Step(group, lens, new, 64)
+    k, v = ref.fill_cache(step, 1, dim, kvt)
+    q = ref.draw(step.rng, (step.M, group, dim), 1.5).to(qt)
+    offsets, cached, pages = [0], [], []
+    for b, n in enumerate(new):
+        for i in range(0, n, rows):
+            cached.append(lens[b] + i)
+            pages.append(step.pages[b])
+            offsets.append(offsets[-1] + min(rows, n - i))
+    assert len(cached) > 64 and offsets[-1] == step.M
+    batch = kq.Batch(i32(offsets), i32(cached), up(np.stack(pages)))
+    got = kq.attn_tree(kq.PagedCache(up(k), up(v), 0.5, 0.25), batch, up(q), max_len=step.max_len, out_dtype=F32).cpu().double()
+    for b, n in enumerate(new):
+        L = lens[b] + n
+        p, at = step.where(b, np.arange(L))
+        kk, vv = 0.5 * k[p, 0, at].double(), 0.25 * v[p, 0, :, at].double()
+        unseen = torch.arange(L)[None] > lens[b] + torch.arange(n)[:, None]
+        for h in range(group):
+            qq = q[step.rows(b), h].double()
+            score = qq @ kk.t()
+            most = (qq.abs() @ kk.abs().t()).amax() * dim ** -0.5
+            w = (score * dim ** -0.5).masked_fill_(unseen, -math.inf).softmax(-1)
+            # (the terms of step_ref.attn's bound)
+            rel = ref.ROUND[qt] + 2.0 ** -24 * (dim + 16) * (1.0 + float(most)) + 2.0 ** -18
+            bound = rel * (w @ vv.abs()) + ref.TINY[qt] * L * vv.abs().amax()
+            assert ((got[step.rows(b), h] - w @ vv).abs() <= bound).all(), (b, h)
