@@ -804,8 +804,8 @@ struct Attend {
 };
 
 // Bound: HBM bandwidth.  64 sequences of up to 8191 slots, 4 rows to a key head of 128,
-// bfloat16: 220 us for 1.39 GB, 6.3 TB/s; two of 131k slots in 8 bits, 8 rows: 80 us
-// for 473 MB, 5.9 TB/s.
+// bfloat16: 218 us for 1.39 GB, 6.4 TB/s; two of 131k slots in 8 bits, 8 rows: 79 us
+// for 473 MB, 6.0 TB/s.
 // Up to 16 rows: one wave's worth, so the waves of a workgroup take tiles in
 // turn, each its own in LDS without a barrier, and their sums are joined in LDS.
 template <class E, bool F8, int D, int WAVES>
@@ -974,8 +974,9 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs a) {
 // early or late they are in LDS by 2 i + 3, before anyone's products at 2 i + 4; what
 // they overwrite, keys i - 1 and values i - 2 (three of each in LDS), was last read at
 // 2 i - 1.
-// Bound: matrix products and softmax on one SIMD.  512 rows to a key head of 128: 870
-// TFLOP/s at even load, 171 - 200 us for 1.2e11 operations on 8 ragged trees.
+// Bound: matrix products and softmax on one SIMD.  512 rows to a key head of 128: 860
+// TFLOP/s at even load (8 trees of 64 over 16384 slots each, 320 us with the join),
+// 168 - 216 us for 1.2e11 operations on 8 ragged trees.
 template <class E, bool F8, int D>
 __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs a) {
     constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;

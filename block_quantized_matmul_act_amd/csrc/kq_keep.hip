@@ -9,7 +9,7 @@
 // each feature, so a move reads and writes 64 times what it moves).  So all
 // layers go in one launch, nothing but the places of the slots is in LDS, and
 // eight workgroups to a compute unit have their chains under way together: 16
-// layers x 32 sequences x 8 heads of 128 in 21 us (27 with the slots in LDS, where
+// layers x 32 sequences x 8 heads of 128 in 22 us (27 with the slots in LDS, where
 // four workgroups fit).
 #include "kq_step_device.hpp"
 

@@ -22,7 +22,10 @@
 // part leaves (m, s, t) and its n largest, and a second kernel joins them.
 // Bound: HBM bandwidth (each logit is read once): 1537 rows of 100277 fp32 logits with 8
 // alternatives in 109 us, 5.6 TB/s (a batch loaded a turn ahead: 118 us without).  One
-// row of 128256 with 20 alternatives: 8 us and 7 for the join, bound by latency.
+// row of 128256 with 20 alternatives: 8 - 9 us and 7 for the join, bound by latency.  In
+// between the selection's fixed cost counts (a sort, candidates and joins in turn for
+// every part of a row): 300 x 128256 47 us, 2.2 times the read; and 16-bit logits take
+// hardly less time than fp32 ones (1537 x 100277: 107 us), bound by the work on each value.
 #include "kq_step_device.hpp"
 
 namespace kq {

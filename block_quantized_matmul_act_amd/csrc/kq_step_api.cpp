@@ -107,12 +107,23 @@ AttnPlan attn_plan(const kq_cache &cache, int64_t n_seqs, int64_t q_heads, int64
     // or the units there can be.
     p.unit_shift = ATTN_UNIT_SHIFT;
     // Few rows of short sequences, no more of them than compute units: a workgroup
-    // of 8 waves takes a head's keys whole, and no second kernel is launched.  The
-    // call, in parts / whole, one sequence of 8 heads of 128, bfloat16: 500 slots
-    // 15.9 / 11.2 us, 1000 slots 15.8 / 12.7, 2000 slots 15.6 / 20.1 (the rate of one
-    // compute unit); 32 sequences of 500 slots 20.0 / 14.9, of 1000 25.5 / 21.5;
-    // more than 256 heads: 200 sequences of 500 62 / 76.  (At dim 256 8 waves' sums do
-    // not fit the registers.)
+    // of 8 waves takes a head's keys whole, and no second kernel is launched.  In
+    // parts / whole, 8 heads, us of a call from Python and (of the kernels alone):
+    //                       250 slots               500                     1000
+    //   bf16, 64:   1 seq  13.7/10.0 (10.0/ 6.4)   13.8/ 9.8 (10.0/ 7.2)   13.5/ 9.8 ( 9.9/ 8.8)
+    //               8      13.5/ 9.7 (10.2/ 6.4)   13.6/ 9.7 (10.1/ 7.3)   13.3/10.0 (11.7/ 9.9)
+    //              32      13.2/ 9.6 (12.1/ 6.6)   13.4/ 9.5 (13.2/ 8.5)   19.4/14.7 (19.6/15.0)
+    //   bf16, 128:  1      13.3/ 9.6 ( 9.7/ 8.0)   13.6/ 9.7 ( 9.8/ 9.5)   13.5/12.2 ( 9.8/12.1)
+    //               8      13.6/ 9.7 (10.0/ 8.0)   13.3/11.0 (10.1/11.0)   13.3/16.1 (12.5/16.1)
+    //              32      13.5/ 9.5 (13.3/ 9.2)   19.6/15.8 (19.7/16.0)   28.7/24.9 (28.7/25.1)
+    //   f8, 64:     1      13.2/ 9.6 ( 9.2/ 5.4)   13.6/ 9.8 ( 9.2/ 6.1)   13.7/ 9.7 ( 9.1/ 7.4)
+    //              32      13.3/ 9.8 (11.1/ 5.5)   13.3/ 9.5 (11.3/ 6.6)   13.5/ 9.5 (13.3/ 8.5)
+    //   f8, 128:    1      13.5/ 9.7 ( 9.9/ 7.2)   13.6/ 9.7 (10.0/ 8.1)   13.5/10.5 (10.1/10.3)
+    //              32      13.2/ 9.5 (12.9/ 7.5)   13.9/ 9.5 (13.9/ 9.4)   20.1/15.9 (20.2/16.1)
+    // It loses towards 1000 slots of 16-bit heads of 128 in few sequences (the rate of
+    // one compute unit), in a captured step from 500 on; 2000 slots of one sequence
+    // 15.6 / 20.1; more than 256 heads: 200 sequences of 500 62 / 76.  (At dim 256 8
+    // waves' sums do not fit the registers.)
     if (p.waves == 0 && max_len > ATTN_UNIT && max_len <= ATTN_WHOLE && n_seqs * heads <= 256 && dim < 256)
         p.unit_shift = ATTN_WHOLE_SHIFT;
     const int unit = 1 << p.unit_shift;
