@@ -661,7 +661,9 @@ def logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     if tokens is not None:
         given = tokens.shape[-1]
         pt = _tensor(tokens, torch.int32, (M, given), device, "logprobs tokens")
-    n_top = max(int(n_top), 0)
+    n_top = int(n_top)
+    if n_top < 0:
+        raise ValueError(f"logprobs n_top: {n_top}")
     # one allocation: the floats [M][n_given], [M], [M][n_top], the ids, the workspace
     lens = (M * given, M if entropy else 0, M * n_top)
     need = step.kq_logprobs_workspace(M, V, n_top)

@@ -185,3 +185,9 @@ def test_one_batch_with_other_row_counts(kq, devices, monkeypatch):  # noqa: F81
     monkeypatch.setattr(kq._step, "kq_cache_keep", lambda caches, n, at, *a: rows.append(n_tokens(at)) or 0)
     kq.rope_append(c, b, x, 4, out=q)
     assert rows == [3, 5, 5, 4, 3]
+
+
+def test_logprobs_of_fewer_than_no_alternatives(kq, devices):  # noqa: F811
+    with pytest.raises(ValueError, match="n_top"):
+        kq.logprobs(Tensor(torch.float32, 3, 50), n_top=-1)
+    assert not devices[1]
