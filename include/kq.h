@@ -338,13 +338,13 @@ int kq_rope_append(const kq_cache *cache, const kq_batch *batch, const float *x,
  *         same type or KQ_T_F8 (converted to q's type, exactly)
  *   out   [n_tokens][q_heads][dim], q's type or KQ_T_F32 (the same sums before
  *         the last rounding)
- * Scores, maxima and sums are fp32, of any size that fp32 holds; the
- * probabilities enter the second product in q's type.  max_tokens is an upper
- * bound of the rows of a sequence (more rows than n_seqs sequences can have by it
- * are refused; a sequence's rows past it come out as NaN) and max_len of lens[b] +
- * its rows (slots past it are not read): they size the launch.  The workspace
- * holds the partial sums of the parts a long sequence is cut into; the same call
- * gives the same bits.
+ * Scores, maxima and sums are fp32, of any size that fp32 holds (in units of
+ * log 2); the probabilities enter the second product in q's type.  max_tokens is
+ * an upper bound of the rows of a sequence (more rows than n_seqs sequences can
+ * have by it are refused; a sequence's rows past it come out as NaN) and max_len of
+ * lens[b] + its rows (slots past it are not read): they size the launch.  The
+ * workspace holds the partial sums of the parts a long sequence is cut into; the
+ * same call gives the same bits.
  * A prompt of more rows, all of them appended, is several sequences here that share
  * its page row: the i-th has lens + 64 i cached tokens and the next 64 rows (mask
  * NULL).
