@@ -309,8 +309,8 @@ typedef struct kq_batch {
  *     rope[position][j], rope[position][rot_dim / 2 + j] (fp32 [n_pos][rot_dim];
  *     rot_dim a multiple of 8 up to dim, 0: no rotation, rope may be NULL);
  *   - write q [n_tokens][q_heads][dim] (q_type KQ_T_BF16 or KQ_T_F16), and k
- *     and v to the rows' slots of the cache, divided by k_scale / v_scale
- *     (KQ_T_F8: clamped to +-448).
+ *     and v to the rows' slots of the cache, times 1 / k_scale, 1 / v_scale
+ *     (themselves rounded to fp32; KQ_T_F8: clamped to +-448).
  * positions (int32 [n_tokens]; NULL: the row's slot) is the place of each row
  * in its text: in a tree of drafts several rows share one.  Positions outside
  * [0, n_pos) are taken at the nearest end.  The arithmetic is fp32, each
