@@ -9,11 +9,14 @@
 #include <atomic>
 #include <cstdint>
 
+#include "kq_act_layout.hpp"
 #include "kq_calib.hpp"
 #include "kq_hooks.hpp"
 #include "kq_launch.hpp"
 
 namespace {
+
+using namespace kq;
 
 enum Variant {
     V_QUANT_Q8K = 0,
@@ -58,42 +61,11 @@ const char *const kVariantNames[V_COUNT] = {
 
 std::atomic<uint64_t> g_count[V_COUNT];
 
-constexpr int64_t kMaxDim = INT32_MAX;  // kernels index rows and columns with int
-constexpr int64_t kMaxBytes = (int64_t)1 << 46;
-
 int qk_of(int fmt) {
     return fmt == KQ_Q4_K || fmt == KQ_Q6_K ? 256 : fmt == KQ_TQ || fmt == KQ_TQ2 ? 128 : 0;
 }
 int bb_of(int fmt) {
     return fmt == KQ_Q4_K ? 144 : fmt == KQ_Q6_K ? 210 : fmt == KQ_TQ ? 28 : fmt == KQ_TQ2 ? 34 : 0;
-}
-int bs_of(int act_fmt) {
-    return act_fmt == KQ_ACT_Q8_K ? 256 : act_fmt == KQ_ACT_Q8_128 ? 128 : 0;
-}
-int64_t align256(int64_t v) { return (v + 255) & ~(int64_t)255; }
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Section offsets of an activation buffer; false when invalid.
-struct ActLayout {
-    int64_t d, bsums, alpha, total;  // byte offsets; -1 for absent sections
-};
-bool act_layout(int act_fmt, int64_t M, int64_t K, ActLayout *L) {
-    const int bs = bs_of(act_fmt);
-    if (!bs || M < 0 || K < 0 || K % bs || M > kMaxDim || K > kMaxDim) return false;
-    if (M != 0 && K > kMaxBytes / M) return false;
-    const int64_t qs_bytes = align256(M * K);
-    const int64_t d_bytes = align256(M * (K / bs) * 4);
-    L->d = qs_bytes;
-    if (act_fmt == KQ_ACT_Q8_K) {
-        L->bsums = qs_bytes + d_bytes;
-        L->alpha = L->bsums + align256(M * (K / 16) * 2);
-        L->total = L->alpha + align256((K / 256) * 2 * M * 8 * 2);
-    } else {
-        L->bsums = -1;
-        L->alpha = -1;
-        L->total = qs_bytes + d_bytes;
-    }
-    return true;
 }
 
 // Shared validation of kq_gemm / kq_gemm_subsums arguments.

@@ -22,22 +22,9 @@
 // exactly; written once per activation instead of once per GEMM tile.  The
 // kernel is bound by HBM bandwidth: it reads 4 bytes and writes ~1.2 bytes per
 // value.
-#include "kq_device.hpp"
+#include "kq_quant_device.hpp"
 
 namespace kq {
-
-namespace {
-// DPP controls: quad permutes (lane ^ 1, lane ^ 2 within a quad) and the
-// half-row (lane i <- 7 - i in each 8) and row (lane i <- 15 - i in each 16)
-// mirrors
-constexpr int DPP_QUAD_XOR1 = 0xB1, DPP_QUAD_XOR2 = 0x4E;
-constexpr int DPP_ROW_HALF_MIRROR = 0x141, DPP_ROW_MIRROR = 0x140;
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-}  // namespace
 
 constexpr int QROWS_PER_WG = 4;                       // one row per wave
 constexpr int QROWS_PER_LAUNCH = 65535 * QROWS_PER_WG;  // grid.y limit
@@ -67,54 +54,8 @@ __global__ __launch_bounds__(256) void quant_act_kernel(const float *__restrict_
         for (int i = 0; i < 4; ++i) v[i] = p[i];
     }
 
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, __builtin_bit_cast(uint32_t, fabsf(v[i][e])));
-    m = max(m, dpp<DPP_QUAD_XOR1>(m));
-    m = max(m, dpp<DPP_QUAD_XOR2>(m));
-    m = max(m, dpp<DPP_ROW_HALF_MIRROR>(m));
-    if constexpr (G == 16) m = max(m, dpp<DPP_ROW_MIRROR>(m));
-    const float amax = __builtin_bit_cast(float, m);
-
-    const float s = 127.0f / amax;
-    const bool zero = !(amax > 0.0f) || !isfinite(s);
-    v4i packed = {0, 0, 0, 0};
-    int sum = 0;
-    if (!zero) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int q = (int)fminf(fmaxf(rintf(v[i][e] * s), -127.f), 127.f);
-                sum += q;
-                w |= (uint32_t)(q & 0xFF) << (8 * e);
-            }
-            packed[i] = (int)w;
-        }
-    }
-    const float dv = zero ? 0.0f : amax / 127.0f;
-    if (valid) {
-        *reinterpret_cast<v4i *>(qs + row * K + col) = packed;
-        if (gl == 0) d[sblk * M + row] = dv;
-    }
-    if constexpr (BSUMS) {
-        // this lane's 16 values are one bsums group
-        if (valid) bsums[row * (K / 16) + col / 16] = (int16_t)sum;
-        // 32 values = lanes 2j, 2j+1: B_j = sum32 (|B_j| <= 4064), parts
-        // 64 * floor(B_j / 64) (a 7-bit integer times 64) and B_j mod 64, both
-        // exact in bf16
-        const int sum32 = sum + (int)dpp<DPP_QUAD_XOR1>((uint32_t)sum);
-        const __bf16 p0 = (__bf16)(float)(sum32 & ~63);
-        const __bf16 p1 = (__bf16)(float)(sum32 & 63);
-        if (valid && (gl & 1) == 0) {
-            const int j = gl >> 1;
-            alpha[((sblk * 2 + 0) * M + row) * 8 + j] = __builtin_bit_cast(uint16_t, p0);
-            alpha[((sblk * 2 + 1) * M + row) * 8 + j] = __builtin_bit_cast(uint16_t, p1);
-        }
-    }
+    const Quantized q = quantize16(v, block_amax<BS>(v));
+    put16<BS, BSUMS>(ActSections{qs, d, bsums, alpha}, q, valid, row, M, K, col, sblk, gl);
 }
 
 // Host-side launcher (called from kq_api.cpp after validation): rows in
