@@ -27,6 +27,7 @@ KQ_ERR_FMT, KQ_ERR_SHAPE, KQ_ERR_NULL, KQ_ERR_ALIGN, KQ_ERR_UNSUPPORTED, KQ_ERR_
 
 KQ_T_F32, KQ_T_BF16, KQ_T_F16, KQ_T_F8 = 1, 2, 3, 4
 KQ_ATTN_MAX_TOKENS = KQ_KEEP_MAX_TOKENS = KQ_LOGPROBS_MAX_TOP = 64
+KQ_NORM_MAX_K = 65536
 
 # Every symbol include/kq.h declares, with its ctypes signature.
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -68,6 +69,15 @@ SIGNATURES = {
     "kq_cache_keep": (_I, [_P, _I64, _P, _P, _P, _P]),
     "kq_logprobs": (_I, [_I, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "kq_logprobs_workspace": (_SZ, [_I64, _I64, _I64]),
+    "kq_norm_quantize": (_I, [_I, _I, _P, _I64, _I, _P, _I64, _P, _I64, _P, _F, _I64, _I64, _P, _P]),
+    "kq_attn_chunk": (_I, [_P, _P, _I, _P, _I64, _I64, _I64, _F, _I64, _I64, _I, _P, _P, _SZ, _P]),
+    "kq_attn_chunk_workspace": (_SZ, [_P, _P, _I64, _I64, _I64, _I64, _I64]),
+    "kq_lora": (_I, [_I, _I64, _P, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "kq_lora_workspace": (_SZ, [_I64, _I64]),
+    "kq_num_layer_variants": (_I, []),
+    "kq_layer_variant_name": (ctypes.c_char_p, [_I]),
+    "kq_layer_count": (ctypes.c_uint64, [_I]),
+    "kq_layer_count_reset": (None, []),
     "kq_strerror": (ctypes.c_char_p, [_I]),
     "kq_version": (_I, []),
 }
@@ -290,6 +300,50 @@ def kq_step_count_reset():
     lib().kq_step_count_reset()
 
 
+def kq_norm_quantize(act_fmt, x_type, x, ldx, r_type, residual, ldr, sum, lds, weight, eps, M, K, a_q8, stream=None):
+    return _check(lib().kq_norm_quantize(act_fmt, x_type, _ptr(x), ldx, r_type, _ptr(residual), ldr, _ptr(sum), lds,
+                                         _ptr(weight), eps, M, K, _ptr(a_q8), _stream(stream)), "kq_norm_quantize")
+
+
+def kq_attn_chunk_workspace(cache, batch, q_heads, window, sinks, max_tokens, max_len):
+    return lib().kq_attn_chunk_workspace(_ref(cache), _ref(batch), q_heads, window, sinks, max_tokens, max_len)
+
+
+def kq_attn_chunk(cache, batch, q_type, q, q_heads, window, sinks, scale, max_tokens, max_len, out_type, out, workspace,
+                  workspace_bytes, stream=None):
+    return _check(lib().kq_attn_chunk(_ref(cache), _ref(batch), q_type, _ptr(q), q_heads, window, sinks, scale, max_tokens,
+                                      max_len, out_type, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)),
+                  "kq_attn_chunk")
+
+
+def kq_lora_workspace(rank, M):
+    return lib().kq_lora_workspace(rank, M)
+
+
+def kq_lora(type, rank, A, B, scale, n_adapters, act_fmt, a_q8, M, N, K, ids, base, ldb, out, ldo, workspace,
+            workspace_bytes, stream=None):
+    return _check(lib().kq_lora(type, rank, _ptr(A), _ptr(B), _ptr(scale), n_adapters, act_fmt, _ptr(a_q8), M, N, K,
+                                _ptr(ids), _ptr(base), ldb, _ptr(out), ldo, _ptr(workspace), workspace_bytes,
+                                _stream(stream)), "kq_lora")
+
+
+def kq_num_layer_variants():
+    return lib().kq_num_layer_variants()
+
+
+def kq_layer_variant_name(v):
+    s = lib().kq_layer_variant_name(v)
+    return s.decode() if s else None
+
+
+def kq_layer_count(v):
+    return lib().kq_layer_count(v)
+
+
+def kq_layer_count_reset():
+    lib().kq_layer_count_reset()
+
+
 def kq_strerror(status):
     return lib().kq_strerror(status).decode()
 
@@ -302,6 +356,10 @@ def kq_version():
 
 def step_counts() -> dict:
     return {kq_step_variant_name(v): kq_step_count(v) for v in range(kq_num_step_variants())}
+
+
+def layer_counts() -> dict:
+    return {kq_layer_variant_name(v): kq_layer_count(v) for v in range(kq_num_layer_variants())}
 
 
 def dispatch_counts() -> dict:
@@ -684,3 +742,130 @@ def logprobs(logits, tokens=None, n_top=0, entropy=True, stream=None):
     _check(step.kq_logprobs(kind, px, M, V, ldx, pt, given, n_top, p_given, p_entropy, p_ids, p_tops,
                             p + 4 * at if need else None, need, _current_stream(device)), "kq_logprobs")
     return r
+
+
+# --------------------------- around the products of a layer that serves many requests
+
+def norm_quantize(x, residual=None, weight=None, eps=1e-6, act_fmt=KQ_ACT_Q8_K, sum_out=None, out=None, stream=None):
+    """The activation buffer (a uint8 tensor, as quantize_act returns it) of the normed
+    rows of x + residual: x [M][K] and residual float32, bfloat16 or float16, rows may lie
+    apart; weight float32 [K].  The sum is written to sum_out (the residual's type; x's
+    where there is none), or over the residual if sum_out is None."""
+    if _torch is None:
+        _step_lib()
+    torch, device = _torch, x.get_device()
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
+            return norm_quantize(x, residual, weight, eps, act_fmt, sum_out, out)
+    px, ldx = _rows(x, None, device, "norm_quantize x")
+    M, K = shape = x.shape
+    x_type = r_type = _type(x.dtype, "norm_quantize x")
+    pr = ps = None
+    ldr = lds = 0
+    if residual is not None:
+        if residual.shape != shape or residual.get_device() != device:
+            _refuse(residual, residual.dtype, shape, device, "norm_quantize residual")
+        pr, ldr = _rows(residual, K, device, "norm_quantize residual")
+        r_type = _type(residual.dtype, "norm_quantize residual")
+        ps, lds = pr, ldr
+    if sum_out is not None:
+        kind = (x if residual is None else residual).dtype
+        if sum_out.dtype is not kind or sum_out.shape != shape or sum_out.get_device() != device:
+            _refuse(sum_out, kind, shape, device, "norm_quantize sum_out")
+        ps, lds = _rows(sum_out, K, device, "norm_quantize sum_out")
+    pw = None if weight is None else _tensor(weight, torch.float32, (K,), device, "norm_quantize weight")
+    step = _step or _step_lib()
+    need = step.kq_act_bytes(act_fmt, M, K)
+    if out is None:
+        out = torch.empty(need, dtype=torch.uint8, device=x.device)
+        po = out.data_ptr()
+    else:
+        po = _tensor(out, torch.uint8, (need,), device, "norm_quantize out")
+    _check(step.kq_norm_quantize(act_fmt, x_type, px, ldx, r_type, pr, ldr, ps, lds, pw, eps, M, K, po,
+                                 _current_stream(device)), "kq_norm_quantize")
+    return out
+
+
+def attn_chunk(cache, batch, q, window=0, sinks=0, scale=None, max_tokens=None, max_len=None, out_dtype=None, out=None,
+               stream=None):
+    """Attention of q [n_tokens][q_heads][dim], any number of rows to a sequence, over the
+    cache: each row over the slots up to its own, under a window > 0 over the last
+    `window` of them and the sequence's first `sinks`.  max_tokens / max_len: what to
+    expect of a sequence's new rows and of its whole length (default: all rows, what the
+    pages hold); they change the speed alone.  out_dtype: q's or float32."""
+    torch, device = _torch, q.get_device()
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
+            return attn_chunk(cache, batch, q, window, sinks, scale, max_tokens, max_len, out_dtype, out)
+    c, q_dtype = cache.c, q.dtype
+    dim = c.dim
+    if device < 0 or q.dim() != 3 or q.shape[2] != dim or not q.is_contiguous():
+        _refuse(q, q_dtype, (None, None, dim), device, "attn_chunk q")
+    M, heads, _ = shape = q.shape
+    _together(device, cache, batch, M, "attn_chunk")
+    if out is None:
+        out = torch.empty_like(q) if out_dtype is None else torch.empty(shape, dtype=out_dtype, device=q.device)
+        po = out.data_ptr()
+    else:
+        po = _tensor(out, out_dtype or out.dtype, shape, device, "attn_chunk out")
+    if max_len is None:
+        max_len = min(batch.c.max_pages * c.page, 1 << 30)
+    if max_tokens is None:
+        max_tokens = M
+    if scale is None:
+        scale = dim ** -0.5
+    rows = batch.of(M)
+    at = _addressof(rows)
+    step = _step or _step_lib()
+    need = step.kq_attn_chunk_workspace(cache.at, at, heads, window, sinks, max_tokens, max_len)
+    work = pw = None
+    if need:
+        work = torch.empty(need, dtype=torch.uint8, device=q.device)
+        pw = work.data_ptr()
+    _check(step.kq_attn_chunk(cache.at, at, _type(q_dtype, "attn_chunk q"), q.data_ptr(), heads, window, sinks, scale,
+                              max_tokens, max_len, _type(out.dtype, "attn_chunk out"), po, pw, need,
+                              _current_stream(device)), "kq_attn_chunk")
+    return out
+
+
+def lora(a_q8, A, B, ids, scale=None, base=None, act_fmt=KQ_ACT_Q8_K, out=None, stream=None):
+    """base + the adapters' part of a product with the activations a_q8: row m adds
+    scale[i] B[i] (A[i] a^[m]), i = ids[m] (int32 [M]; outside the adapters: nothing).  A
+    [n][rank][K] and B [n][N][rank] bfloat16 or float16, scale float32 [n]; base and out
+    float32 [M][N], whose rows may lie apart (out may be base; base None: zeros)."""
+    if _torch is None:
+        _step_lib()
+    torch, device = _torch, a_q8.get_device()
+    if stream is not None or (device >= 0 and device != _current_device()):
+        with _on(stream, device):
+            return lora(a_q8, A, B, ids, scale, base, act_fmt, out)
+    f32, dtype = torch.float32, A.dtype
+    n, rank, K = A.shape if A.dim() == 3 else (None, None, None)
+    pa = _tensor(A, dtype, (n, rank, K), device, "lora A")
+    N = B.shape[1] if B.dim() == 3 else None
+    pb = _tensor(B, dtype, (n, N, rank), device, "lora B")
+    M = ids.shape[0] if ids.dim() == 1 else None
+    pi = _tensor(ids, torch.int32, (M,), device, "lora ids")
+    psc = None if scale is None else _tensor(scale, f32, (n,), device, "lora scale")
+    step = _step or _step_lib()
+    pq = _tensor(a_q8, torch.uint8, (step.kq_act_bytes(act_fmt, M, K),), device, "lora a_q8")
+    pbase, ldb = None, 0
+    if base is not None:
+        if base.dtype is not f32 or base.shape != (M, N) or base.get_device() != device:
+            _refuse(base, f32, (M, N), device, "lora base")
+        pbase, ldb = _rows(base, N, device, "lora base")
+    # one allocation: the values between the two products, the result
+    need = step.kq_lora_workspace(rank, M)
+    if out is None:
+        block = torch.empty(need // 4 + M * N, dtype=f32, device=A.device)
+        out, pw = block.as_strided((M, N), (N, 1), need // 4), block.data_ptr()
+        po, ldo = pw + need, N
+    else:
+        if out.dtype is not f32 or out.shape != (M, N) or out.get_device() != device:
+            _refuse(out, f32, (M, N), device, "lora out")
+        po, ldo = _rows(out, N, device, "lora out")
+        block = torch.empty(need, dtype=torch.uint8, device=A.device)
+        pw = block.data_ptr()
+    _check(step.kq_lora(_type(dtype, "lora A"), rank, pa, pb, psc, n, act_fmt, pq, M, N, K, pi, pbase, ldb, po, ldo, pw,
+                        need, _current_stream(device)), "kq_lora")
+    return out

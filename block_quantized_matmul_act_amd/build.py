@@ -11,7 +11,8 @@ LIB = os.path.join(HERE, "libkq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["kq_api.cpp", "kq_quant.hip", "kq_gemm.hip", "kq_gemm_q4k.hip", "kq_gemm_ring.hip", "kq_gemm_tq.hip", "kq_gemv.hip", "kq_calib.hip",
-           "kq_step_api.cpp", "kq_rope.hip", "kq_attn.hip", "kq_keep.hip", "kq_logprobs.hip"]
+           "kq_step_api.cpp", "kq_rope.hip", "kq_attn.hip", "kq_keep.hip", "kq_logprobs.hip",
+           "kq_layer_api.cpp", "kq_norm.hip", "kq_chunk.hip", "kq_lora.hip"]
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",

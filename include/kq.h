@@ -17,8 +17,9 @@
  * Conventions (all entry points):
  *   - Every pointer argument is a DEVICE pointer except where noted.  The
  *     caller allocates and frees all memory; the library allocates nothing and
- *     keeps no handles.  The products need no scratch; kq_attn_tree and
- *     kq_logprobs take a workspace whose size a query gives.
+ *     keeps no handles.  The products need no scratch; kq_attn_tree,
+ *     kq_logprobs, kq_attn_chunk and kq_lora take a workspace whose size a query
+ *     gives.
  *   - Work is enqueued asynchronously on `stream` (NULL = the default
  *     stream).  Device faults surface at the caller's next synchronization.
  *     The device of the pointers and of the stream is the calling thread's
@@ -405,6 +406,92 @@ int kq_num_step_variants(void);
 const char *kq_step_variant_name(int variant);
 uint64_t kq_step_count(int variant);
 void kq_step_count_reset(void);
+
+/* ------------------------------------------------------------------------
+ * Around the products of a layer that serves many requests, prompts and single
+ * tokens in one step:
+ *
+ *   kq_norm_quantize -> kq_gemm (+ kq_lora) -> kq_rope_append -> kq_attn_chunk ->
+ *   kq_quantize_act -> kq_gemm (+ kq_lora) -> kq_norm_quantize ...
+ */
+
+/*
+ * The input of a product: with s = x + residual (residual NULL: s = x),
+ *   sum  = s                                        rounded once to r_type (NULL: not kept)
+ *   a_q8 = quantize(s * weight / sqrt(mean s^2 + eps))   the mean over a row's K values
+ * as kq_quantize_act lays it out and rounds (act_fmt; kq_act_bytes(act_fmt, M, K) bytes).
+ * x [M][K] is KQ_T_F32, KQ_T_BF16 or KQ_T_F16, residual and sum are of one such type
+ * r_type (not looked at where both are NULL), weight is fp32 [K] (NULL: ones).  Rows may
+ * lie apart: ldx, ldr and lds elements, multiples of 4 (fp32) or 8.  sum may be the
+ * residual itself (lds == ldr) and overlaps nothing else.  The arithmetic is fp32, and
+ * the norm is of s before its rounding; sums of squares that leave fp32's range are
+ * formed in 64 bits.  A row of zeros gives zeros with any eps.  A row with an infinity
+ * or a NaN, or a block whose normed values pass fp32, has NaN for its scales and 0 for its
+ * values and sums: every product with it is NaN.  All pointers are 16-byte aligned; K at
+ * most KQ_NORM_MAX_K (KQ_ERR_UNSUPPORTED beyond).  The same call gives the same bits.
+ */
+#define KQ_NORM_MAX_K 65536
+int kq_norm_quantize(int act_fmt, int x_type, const void *x, int64_t ldx, int r_type, const void *residual,
+                     int64_t ldr, void *sum, int64_t lds, const float *weight, float eps, int64_t M, int64_t K,
+                     void *a_q8, hipStream_t stream);
+
+/*
+ * Attention of each sequence's new rows, any number of them, over its cache, their own
+ * keys and values already in it: row i of sequence b, at slot p = lens[b] + i, sees the
+ * slots s <= p; with a window > 0 only those of them with s > p - window or s < sinks.
+ *   out[i][h] = sum_s p_s v_s,   p = softmax_s(scale * q[i][h] . k_s)
+ * Head h reads key head h / (q_heads / heads).  What an unseen slot holds (infinities and
+ * NaN too) does not count.  Types, scores, sums, roundings and q and out as in
+ * kq_attn_tree.  Rows that belong to no sequence (n_tokens above offsets[n_seqs]) are left
+ * as they were.
+ * max_tokens and max_len are what to expect of the rows of a sequence and of lens[b] + its
+ * rows: they choose the kernel and its cuts, and where a sequence has more the result is
+ * the same within rounding, only slower.  Slots past max_pages pages are not read.  The
+ * workspace holds the partial sums of blocks whose keys are cut into parts; the same
+ * call gives the same bits.  Calls that may run at the same time need one each.
+ * Sizes: q_heads a multiple of heads; n_tokens * q_heads * dim below 2^31; scale * k_scale *
+ * log2(e) finite in fp32; launches of 2^32 threads or more are declined with
+ * KQ_ERR_UNSUPPORTED.
+ */
+int kq_attn_chunk(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q,
+                  int64_t q_heads, int64_t window, int64_t sinks, float scale, int64_t max_tokens,
+                  int64_t max_len, int out_type, void *out, void *workspace, size_t workspace_bytes,
+                  hipStream_t stream);
+/* Workspace bytes of that call (0: none needed); 0 for invalid arguments. */
+size_t kq_attn_chunk_workspace(const kq_cache *cache, const kq_batch *batch, int64_t q_heads,
+                               int64_t window, int64_t sinks, int64_t max_tokens, int64_t max_len);
+
+/*
+ * Low-rank adapters of many requests beside a shared product with the same activations:
+ *   out[m] = base[m] + scale[i] * B_i (A_i a^[m]),   i = ids[m]
+ * a^[m][k] = d[m][block] * qs[m][k] as in kq_gemm.  A is [n_adapters][rank][K] and B
+ * [n_adapters][N][rank], both KQ_T_BF16 or KQ_T_F16, scale fp32 [n_adapters] (NULL: ones),
+ * ids int32 [M] on the device: any order, any number of rows to an adapter, and a row
+ * whose id lies outside [0, n_adapters) has none (out = base).  rank is 8, 16, 32, 64 or
+ * 128 (KQ_ERR_UNSUPPORTED otherwise; adapters of a smaller rank are padded with zeros).
+ * base is fp32 with rows ldb elements apart (NULL: zeros), out fp32 with rows ldo apart; out
+ * may be base itself (ldb == ldo) and overlaps nothing else, so the adapters of a
+ * part of a wider product are a call on its columns.  Sums are fp32, the adapters are used
+ * as they are and the values between the two products stay in fp32.  An adapter's
+ * infinities and NaN reach the rows that use it and no other.  The workspace
+ * (kq_lora_workspace bytes, 16-byte aligned) holds those values; calls that may run at the
+ * same time need one each.  M up to 65535 * 64, N below 2^31 - 256; A, B and a_q8
+ * 16-byte aligned.  The same call gives the same bits.
+ */
+int kq_lora(int type, int64_t rank, const void *A, const void *B, const float *scale, int64_t n_adapters,
+            int act_fmt, const void *a_q8, int64_t M, int64_t N, int64_t K, const int32_t *ids,
+            const float *base, int64_t ldb, float *out, int64_t ldo, void *workspace,
+            size_t workspace_bytes, hipStream_t stream);
+/* Workspace bytes of that call; 0 for invalid arguments. */
+size_t kq_lora_workspace(int64_t rank, int64_t M);
+
+/* Counters of these three operators' variants (launched successfully) and their names:
+ * norm_quantize, chunk_few (up to 16 rows to a key head), chunk_rows (more), lora_few,
+ * lora_tile (more rows). */
+int kq_num_layer_variants(void);
+const char *kq_layer_variant_name(int variant);
+uint64_t kq_layer_count(int variant);
+void kq_layer_count_reset(void);
 
 /* Per-variant dispatch counters (incremented on each successful launch) and
  * their names, so tests can prove which kernel variant ran (vllm.cpp PR 3036
