@@ -120,21 +120,6 @@ __device__ __forceinline__ Share share_of(const AttnArgs &a, int dim) {
     }
     return s;
 }
-// Equal runs of `units` for `groups` workgroups (at least as many units as groups):
-// the first `more` have one unit more than the others.
-struct Runs {
-    int size, more;
-    __device__ __forceinline__ Runs(int units, int groups) {
-        size = units / groups;
-        more = units - size * groups;
-    }
-    __device__ __forceinline__ int begin(int w) const { return w * size + min(w, more); }
-    __device__ __forceinline__ int holder(int u) const {  // the workgroup that has unit u
-        const int longer = more * (size + 1);
-        return u < longer ? u / (size + 1) : more + (u - longer) / size;
-    }
-};
-
 // One block's share of a run: keys [from, to) of a row block of a head; `whole`
 // if that is all of its keys, else the workspace slot of its sums.
 struct Piece {

@@ -225,6 +225,21 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b) {
     return q;
 }
 
+// Equal runs of `units` for `groups` workgroups (at least as many units as groups):
+// the first `more` have one unit more than the others.
+struct Runs {
+    int size, more;
+    __device__ __forceinline__ Runs(int units, int groups) {
+        size = units / groups;
+        more = units - size * groups;
+    }
+    __device__ __forceinline__ int begin(int w) const { return w * size + min(w, more); }
+    __device__ __forceinline__ int holder(int u) const {  // the workgroup that has unit u
+        const int longer = more * (size + 1);
+        return u < longer ? u / (size + 1) : more + (u - longer) / size;
+    }
+};
+
 // Where a sequence's values lie, for what add_odd reads again.
 struct ValueRows {
     const CacheArgs &cache;
@@ -484,8 +499,9 @@ struct Attend {
     // The same for the whole wave; set where m is.
     bool far;
 
-    __device__ __forceinline__ Attend(const AttnArgs &a_) : a(a_) {
-        lane = threadIdx.x & 63;
+    __device__ __forceinline__ Attend(const AttnArgs &a_) : Attend(a_, threadIdx.x) {}
+    __device__ __forceinline__ Attend(const AttnArgs &a_, unsigned thread) : a(a_) {
+        lane = thread & 63;
         n = lane & (RW - 1);
         g = lane / RW;
         // this lane's row of the first product's results: see the head of the file

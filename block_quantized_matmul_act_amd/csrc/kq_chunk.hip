@@ -16,33 +16,37 @@
 // workgroup finds its block by one search of the offsets.  A few numbers have no
 // block, and their workgroups end at once.
 //
-// Where the blocks do not fill the chip their keys are cut into equal parts, which
-// leave their sums in the workspace for a second kernel to join, in a fixed order.
-// Blocks late in a text have the most keys, and go first.
+// Many blocks: a workgroup to a block, those late in a text, which have the most keys,
+// first.  Few (or long ones among them): a grid that just fills the chip adds up the
+// units of all blocks and every workgroup takes an equal run of them.  A run covers
+// parts of at most two blocks and any number of whole ones; a part leaves its sums in
+// the workspace and a second kernel joins the parts, in a fixed order.
 #include "kq_attn_device.hpp"
+#include "kq_copy.hpp"
 #include "kq_layer.hpp"
 
 namespace kq {
 
 namespace {
 
-// A block's share of the work: tiles [from, to) of KEYS slots.  Slots are counted in
-// units of 64: first the units of the sinks, then those of the window.
+// A block's share of the work: units [from, to) of CHUNK_UNIT slots, first those of the
+// sinks, then those of the window.
 struct Block {
     int b, h, rb;
     Seq sq;
     int pos0, pos1;  // slots of its first and last token
-    int sink_units, window_unit;
-    int from, to;    // units
-    int part, parts;
+    int sink_units, window_unit, units;
+    int from, to;
+    bool whole;
 };
 
-// The sequence that has block number j of a key head: the last one whose first
-// number is not above it.
+// The first block number of sequence b.
 __device__ __forceinline__ int64_t first_block(const ChunkArgs &c, int b) {
     const int64_t row = (int64_t)min(max(c.a.batch.offsets[b], 0), c.a.batch.n_tokens) * c.a.group;
     return (row >> c.rows_shift) + b;
 }
+// The sequence that has block number j of a key head: the last one whose first
+// number is not above it; found by a whole wave together.
 __device__ __forceinline__ int block_seq(const ChunkArgs &c, int j) {
     const int lane = __lane_id();
     int lo = 0, n = c.a.batch.n_seqs;  // the answer is in [lo, lo + n)
@@ -55,14 +59,24 @@ __device__ __forceinline__ int block_seq(const ChunkArgs &c, int j) {
         n = min(step, lo + n - from);
         lo = from;
     }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+// The same for one lane by itself.
+__device__ __forceinline__ int lane_seq(const ChunkArgs &c, int j) {
+    int lo = 0, hi = c.a.batch.n_seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_block(c, mid) <= j)
+            lo = mid;
+        else
+            hi = mid;
+    }
     return lo;
 }
 
-// Block j of head h; false if there is none, or no such part of it.
-__device__ __forceinline__ bool block_at(const ChunkArgs &c, int j, int h, int part, Block &k) {
-    const int b = __builtin_amdgcn_readfirstlane(block_seq(c, j));
+// Block j as one of sequence b; false if there is none.
+__device__ __forceinline__ bool block_of(const ChunkArgs &c, int b, int j, Block &k) {
     k.b = b;
-    k.h = h;
     k.rb = j - (int)first_block(c, b);
     Seq &q = k.sq;
     batch_rows(c.a.batch, b, q.first, q.rows);
@@ -72,59 +86,156 @@ __device__ __forceinline__ bool block_at(const ChunkArgs &c, int j, int h, int p
     const int64_t table = (int64_t)c.a.batch.max_pages << c.a.cache.page_shift;
     q.total = (int)min((int64_t)q.len + q.T, table);
     const int64_t row0 = (int64_t)k.rb << c.rows_shift, rows = (int64_t)q.T * c.a.group;
+    k.units = 0;
     if (k.rb < 0 || row0 >= rows) return false;
     const int64_t row1 = min(row0 + (1 << c.rows_shift), rows);
-    k.pos0 = q.len + (int)(row0 / c.a.group);
-    k.pos1 = q.len + (int)((row1 - 1) / c.a.group);
+    k.pos0 = q.len + (int)((uint32_t)row0 / (uint32_t)c.a.group);
+    k.pos1 = q.len + (int)((uint32_t)(row1 - 1) / (uint32_t)c.a.group);
     const int end = min(k.pos1 + 1, q.total);
     const int begin = min(max(k.pos0 - (c.window - 1), 0), end);
     k.window_unit = begin >> CHUNK_UNIT_SHIFT;
     const int end_unit = (int)(((int64_t)end + CHUNK_UNIT - 1) >> CHUNK_UNIT_SHIFT);
     const int sinks = (min(c.sinks, end) + CHUNK_UNIT - 1) >> CHUNK_UNIT_SHIFT;
     k.sink_units = min(sinks, k.window_unit);
-    const int units = k.sink_units + end_unit - k.window_unit;
-    const int size = max(c.part_units, (units + c.parts - 1) / c.parts);
-    k.parts = max(1, (units + size - 1) / size);
-    k.part = part;
-    k.from = min(part * size, units);
-    k.to = min(k.from + size, units);
-    return part < k.parts;
+    k.units = k.sink_units + max(end_unit - k.window_unit, 1);
+    return true;
 }
 
-// What a workgroup does of the grid.
-__device__ __forceinline__ bool my_block(const ChunkArgs &c, Block &k, int64_t &slot_row) {
-    const int heads = c.a.cache.heads;
-    const unsigned w = blockIdx.x, rest = w / heads;
-    const int h = (int)(w - rest * heads), part = (int)(rest % c.parts), j = c.blocks - 1 - (int)(rest / c.parts);
-    slot_row = (((int64_t)j * heads + h) * c.parts + part) << c.rows_shift;
-    return block_at(c, j, h, part, k);
+// The units of all blocks of a key head, added up by the whole workgroup: before[j] (in
+// LDS) is what comes before block j, before[blocks] all.
+template <int THREADS>
+__device__ __forceinline__ void add_up(const ChunkArgs &c, int *before, int *waves) {
+    int base = 0;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int j0 = 0; j0 < c.blocks; j0 += THREADS) {
+        const int j = j0 + threadIdx.x;
+        Block k;
+        k.units = 0;
+        if (j < c.blocks) block_of(c, lane_seq(c, j), j, k);
+        int incl = k.units;
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);  // in rows of 16: from 1, 2, 4, 8 to the left
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, false);
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, false);
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);  // lane 15 of rows 0 and 2 to rows 1 and 3
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);  // lane 31 to the upper half
+        if (lane == 63) waves[wave] = incl;
+        __syncthreads();
+        int all = 0, mine = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) {
+            mine = w < wave ? mine + waves[w] : mine;
+            all += waves[w];
+        }
+        if (j < c.blocks) before[j] = base + mine + incl - k.units;
+        base += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) before[c.blocks] = base;
+    __syncthreads();
 }
 
-// The tiles of a part, and who sees what of them.
+// What a workgroup does, piece by piece.
+template <int THREADS>
+struct Work {
+    const ChunkArgs &c;
+    int *before;
+    int u, end, begin, group, all;
+    bool first;
+    // lds: CHUNK_RUN_BLOCKS + 1 and a wave's number of ints
+    __device__ __forceinline__ Work(const ChunkArgs &c_, int *lds, int *waves) : c(c_), before(lds), first(true) {
+        u = begin = 0;
+        end = 1;
+        group = blockIdx.x;
+        if (!c.runs) return;
+        add_up<THREADS>(c, before, waves);
+        all = before[c.blocks];
+        const int units = all * c.a.cache.heads, groups = min((int)gridDim.x, units);
+        // workgroups go round the chip's 8 dies: neighbouring runs, which mostly share a
+        // head's keys, to the same one
+        const int per = (int)gridDim.x >> 3;
+        if (((int)gridDim.x & 7) == 0) group = (group & 7) * per + (group >> 3);
+        if (blockIdx.x == 0)
+            for (int j = threadIdx.x; j <= c.blocks; j += THREADS) c.a.ws_seq[j] = before[j];
+        if (group >= groups) {
+            end = 0;
+            return;
+        }
+        const Runs runs(units, groups);
+        u = begin = runs.begin(group);
+        end = runs.begin(group + 1);
+    }
+    // The next piece and, where it is a part, its slot; false at the end.
+    __device__ __forceinline__ bool next(Block &k, int64_t &slot) {
+        if (u >= end) return false;
+        const int heads = c.a.cache.heads;
+        int j;
+        slot = 0;
+        if (!c.runs) {
+            const unsigned w = blockIdx.x, back = w / heads;
+            u = end;
+            j = c.blocks - 1 - (int)back;
+            k.h = (int)(w - back * heads);
+            if (!block_of(c, block_seq(c, j), j, k)) return false;
+            k.from = 0;
+            k.to = k.units;
+        } else {
+            k.h = u / all;
+            const int x = u - k.h * all;
+            // the last block with before[j] <= x
+            const int lane = __lane_id();
+            int lo = 0, n = c.blocks;
+            while (n > 1) {
+                const int step = (n + 63) >> 6, at = lo + lane * step;
+                const int few = __popcll(__ballot(at < lo + n && before[at] <= x));
+                const int from = lo + max(few - 1, 0) * step;
+                n = min(step, lo + n - from);
+                lo = from;
+            }
+            j = __builtin_amdgcn_readfirstlane(lo);
+            block_of(c, block_seq(c, j), j, k);
+            k.from = x - __builtin_amdgcn_readfirstlane(before[j]);
+            k.to = min(k.units, k.from + end - u);
+            slot = 2 * (int64_t)group + (u != begin);
+            u += k.to - k.from;
+        }
+        k.whole = k.to - k.from == k.units;
+        return true;
+    }
+};
+
+// The tiles of a part, counted from the block's first, and who sees what of them.
 template <int KEYS>
 struct Tiles {
     static constexpr int F = CHUNK_UNIT / KEYS;
     const ChunkArgs &c;
-    int sink_units, window_unit, from, to;  // tiles
-    int pos0, pos1;
+    int sink_tiles, start;  // tiles of the sinks; the slot of the first tile after them
+    int from, to;
+    // Tiles that some row between two slots does not see whole: [low0, low1), where sinks
+    // or the window end, and from `high` on, where the rows' own slots are.
+    struct Edges {
+        int low0, low1, high;
+        __device__ __forceinline__ bool low(int t) const { return t >= low0 && t < low1; }
+        __device__ __forceinline__ bool at(int t) const { return low(t) || t >= high; }
+    };
+    Edges block;
+    __device__ __forceinline__ Edges edges(int pos0, int pos1) const {
+        Edges e;
+        e.low0 = min(sink_tiles, c.sinks / KEYS);
+        // (the slots not below start: their differences fit 32 bits)
+        e.low1 = sink_tiles + max(pos1 - (c.window - 1) - start + KEYS - 1, 0) / KEYS;
+        e.high = sink_tiles + max(pos0 + 1 - start, 0) / KEYS;
+        return e;
+    }
     __device__ __forceinline__ Tiles(const ChunkArgs &c_, const Block &k) : c(c_) {
-        sink_units = k.sink_units;
-        window_unit = k.window_unit;
+        sink_tiles = k.sink_units * F;
+        start = k.window_unit << CHUNK_UNIT_SHIFT;
         from = k.from * F;
         to = k.to * F;
-        pos0 = k.pos0;
-        pos1 = k.pos1;
-        if (F > 1 && to > from && key(to - 1) > pos1) --to;  // half a unit past the end
+        if (F > 1 && to > from && key(to - 1) > k.pos1) --to;  // half a unit past the end
+        block = edges(k.pos0, k.pos1);
     }
-    __device__ __forceinline__ int key(int t) const {
-        const int u = t / F;
-        return ((u < sink_units ? u : u - sink_units + window_unit) << CHUNK_UNIT_SHIFT) + t % F * KEYS;
-    }
-    // whether rows from slot p0 to slot p1 all see the whole tile at key0
-    __device__ __forceinline__ bool whole(int key0, int p0, int p1) const {
-        return key0 + KEYS - 1 <= p0 && (key0 > p1 - c.window || key0 + KEYS <= c.sinks);
-    }
-    __device__ __forceinline__ bool edge(int key0) const { return !whole(key0, pos0, pos1); }
+    __device__ __forceinline__ int key(int t) const { return t < sink_tiles ? t * KEYS : start + (t - sink_tiles) * KEYS; }
     // which of the 8 keys from k the row of slot pos sees
     __device__ __forceinline__ uint32_t on(int k, int pos) const {
         const int back = max(pos - k, -1);  // (below 0 for all the same: the sums stay in 32 bits)
@@ -134,42 +245,112 @@ struct Tiles {
     }
 };
 
+// The thread's number, worked out anew for each piece: what follows from it is not kept
+// in registers across the pieces (the ways of few and of many rows together have too many).
+__device__ __forceinline__ unsigned this_thread() {
+    unsigned t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// Two 16-bit values, whose sum is added to an fp32 one (exactly, but for one rounding; float16's
+// smallest values count).
+__device__ __forceinline__ float add2(uint32_t w, float sum, __bf16) {
+    constexpr uint32_t one = 0x3F803F80u;
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, w), __builtin_bit_cast(v2bf, one), sum, false);
+}
+__device__ __forceinline__ float add2(uint32_t w, float sum, _Float16) {
+    constexpr uint32_t one = 0x3C003C00u;
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, w), __builtin_bit_cast(v2h, one), sum, false);
+}
+
 // One wave's rows over the tiles.
 template <class E, bool F8, int D, int KEYS, int RW>
 struct Rows {
     typedef Attend<E, F8, D, KEYS, RW> AT;
     AT at;
     const Tiles<KEYS> &tiles;
-    int pos, pos0, pos1;  // slot of this lane's row, of the wave's first and last
-    __device__ __forceinline__ Rows(const AttnArgs &a, const Tiles<KEYS> &t) : at(a), tiles(t) {}
+    int pos;  // slot of this lane's row
+    typename Tiles<KEYS>::Edges edge;
+    __device__ __forceinline__ Rows(const AttnArgs &a, const Tiles<KEYS> &t, unsigned thread) : at(a, thread), tiles(t) {}
     __device__ __forceinline__ void begin(const Block &k, int row0) {
         const int G = at.a.group;
         pos = k.sq.len + at.begin_rows(k.sq, k.h, row0);
-        pos0 = __builtin_amdgcn_readfirstlane(min(k.sq.len + row0 / G, k.pos1));
-        pos1 = __builtin_amdgcn_readfirstlane(min(k.sq.len + (row0 + RW - 1) / G, k.pos1));
+        const int pos0 = __builtin_amdgcn_readfirstlane(min(k.sq.len + row0 / G, k.pos1));
+        const int pos1 = __builtin_amdgcn_readfirstlane(min(k.sq.len + (row0 + RW - 1) / G, k.pos1));
         if (!at.used) pos = pos1;
+        edge = tiles.edges(pos0, pos1);
     }
-    __device__ __forceinline__ void mask(int key0, float (&p)[AT::NT * AT::NR]) {
-        if (!tiles.whole(key0, pos0, pos1)) {
+    // Masks the scores of tile t, the one at key0, and raises m where it must.  p[r] is key
+    // key0 + 8 NG (r / 8) + 8 g + r % 8.
+    __device__ __forceinline__ void mask(int t, int key0, float (&p)[AT::NT * AT::NR]) {
+        if (edge.at(t)) {
             int k0 = key0;
             asm volatile("" : "+s"(k0));  // (the masks are not worked out ahead of this branch)
-            at.hide(p, [&](int s) { return tiles.on(k0 + 8 * AT::NG * s + 8 * at.g, pos); });
+            const int back = pos - (k0 + 8 * at.g);  // the last key that is not after the row
+            if (t >= edge.high) {
+#pragma unroll
+                for (int r = 0; r < AT::NT * AT::NR; ++r) p[r] = 8 * AT::NG * (r / 8) + r % 8 <= back ? p[r] : -__builtin_inff();
+            }
+            if (edge.low(t)) {
+                const int out = max(back, -1) - tiles.c.window, sink = tiles.c.sinks - (k0 + 8 * at.g);
+#pragma unroll
+                for (int r = 0; r < AT::NT * AT::NR; ++r) {
+                    const float s = 8 * AT::NG * (r / 8) + r % 8 < sink ? p[r] : -__builtin_inff();
+                    p[r] = 8 * AT::NG * (r / 8) + r % 8 > out ? p[r] : s;
+                }
+            }
         }
         at.lift(p);
     }
-    __device__ __forceinline__ void tile(const char *lds, int buf, int key0) {
+    // The probabilities of step s, as operands of the second product.  Their sum is taken
+    // after their rounding: the weights of a row then add up to 1, and what rounding does
+    // to a large one is taken back by the division.
+    __device__ __forceinline__ typename AT::op_t probabilities(const float (&p)[AT::NT * AT::NR], int s, float (&sum)[2]) {
+        v4u w;
+        const float by = at.far ? 1.f : at.a.score_scale;  // (far: scaled already)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], by, -at.m));
+            const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], by, -at.m));
+            w[j] = pack2<E>(p0, p1);
+            sum[j & 1] = add2(w[j], sum[j & 1], E{});
+        }
+        return __builtin_bit_cast(typename AT::op_t, w);
+    }
+    __device__ __forceinline__ void tile(const char *lds, int buf, int t, int key0) {
         float p[AT::NT * AT::NR];
         typename AT::op_t pf[AT::NS];
         at.template products<false, true, 4>(lds, 0, pf, buf, p);
-        mask(key0, p);
-        at.add_values(lds, buf, p, pf);
+        mask(t, key0, p);
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < AT::NS; ++s) pf[s] = probabilities(p, s, sum);
+        at.l += sum[0] + sum[1];
+        at.template products<true, false, 4>(lds, buf + AT::TL::K_BYTES, pf, 0, p);
+    }
+    // The wave's rows to the output or, a part, to the workspace as they lie in the lanes.
+    __device__ __forceinline__ void put(const Block &k, int64_t slot, int wave) {
+        if (k.whole) {
+            at.put(true, 0);
+            return;
+        }
+        at.end();
+        const int64_t wave_rows = (slot << tiles.c.rows_shift) + wave * RW;
+        v4f *o = reinterpret_cast<v4f *>(at.a.ws_o + wave_rows * D) + at.lane;
+#pragma unroll
+        for (int d = 0; d < AT::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < AT::NR; r += 4)
+                o[(d * AT::NR + r) * 16] = v4f{at.o[d][r], at.o[d][r + 1], at.o[d][r + 2], at.o[d][r + 3]};
+        if (at.g == 0) *reinterpret_cast<v2f *>(at.a.ws_ml + 2 * (wave_rows + at.n)) = v2f{at.m, at.l};
     }
     // What infinite and NaN values in tiles that some row does not see whole add.
     __device__ __forceinline__ void odd_values(const Block &k, int from, int step) {
 #pragma nounroll
         for (int t = from; t < tiles.to; t += step) {
+            if (!tiles.block.at(t)) continue;
             const int key0 = tiles.key(t);
-            if (!tiles.edge(key0)) continue;
 #pragma nounroll
             for (int key = key0; key < key0 + KEYS; key += 8 * AT::NG)
                 add_odd<E, F8, D, RW>(ValueRows{at.a.cache, at.a.batch, k.b, k.h, k.sq.total}, key, at.lane,
@@ -181,26 +362,31 @@ struct Rows {
 // Up to 16 rows: the waves take tiles in turn, each its own in LDS without a barrier,
 // and their sums are joined in LDS.
 template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const ChunkArgs c) {
-    constexpr int RW = 16, WAVES = 4;
-    constexpr int KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
+struct Few {
+    static constexpr int RW = 16, KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
     typedef Tile<E, F8, D, KEYS, RW, 64, true> TL;
     typedef Rows<E, F8, D, KEYS, RW> RS;
-    constexpr int O_FLOATS = RW * (D + 4);
-    constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : (O_FLOATS * 4 + 1023) / 1024 * 1024;
-
-    __shared__ __align__(1024) char lds[WAVES * WAVE_BYTES];  // a wave's tile, then its sums [row][dim]
-    __shared__ float lm[WAVES * RW], ll[WAVES * RW];
-
-    Block k;
-    int64_t slot_row;
-    if (!my_block(c, k, slot_row)) return;
+    static constexpr int O_FLOATS = RW * (D + 4);
+    static constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : (O_FLOATS * 4 + 1023) / 1024 * 1024;
+};
+// The waves that take few rows in the kernel of many: 8, or none (dim 256 in 16 bits) where
+// neither LDS nor registers hold them.
+template <class E, bool F8, int D>
+constexpr int FEW_IN_WIDE = 8 * Few<E, F8, D>::WAVE_BYTES <= 147456 ? 8 : 0;
+// lds: WAVES * WAVE_BYTES, a wave's tile and then its sums [row][dim]; lm, ll: WAVES * 16
+template <class E, bool F8, int D, int WAVES>
+__device__ __forceinline__ void few_rows(const ChunkArgs &c, const Block &k, int64_t slot, char *lds, float *lm, float *ll) {
+    typedef Few<E, F8, D> FW;
+    typedef typename FW::TL TL;
+    typedef typename FW::RS RS;
+    constexpr int RW = FW::RW, KEYS = FW::KEYS, WAVE_BYTES = FW::WAVE_BYTES;
     const AttnArgs &a = c.a;
     const Tiles<KEYS> tiles(c, k);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned thread = this_thread();
+    const int wave = __builtin_amdgcn_readfirstlane(thread >> 6);
     const int mine = wave * WAVE_BYTES;
-    TL tl(a, threadIdx.x & 63);
-    RS rs(a, tiles);
+    TL tl(a, thread & 63);
+    RS rs(a, tiles, thread);
     typename RS::AT &at = rs.at;
     tl.aim(k.b, k.h, k.sq);
     int t = tiles.from + wave;
@@ -208,20 +394,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const 
     tl.load_k(next);
     tl.load_v(next);
     next = tl.find(tiles.key(t + WAVES));
-    const int row0 = k.rb * RW;
+    const int row0 = k.rb << c.rows_shift;
     rs.begin(k, row0);
     bool odd = false;
     for (; t < tiles.to; t += WAVES) {
         const int key0 = tiles.key(t);
         tl.store_k(lds, mine);
-        odd |= tl.store_v(lds, mine + TL::K_BYTES, key0, tiles.edge(key0));
+        odd |= tl.store_v(lds, mine + TL::K_BYTES, key0, tiles.block.at(t));
         if (t + WAVES < tiles.to) {
             tl.load_k(next);
             tl.load_v(next);
             next = tl.find(tiles.key(t + 2 * WAVES));
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        rs.tile(lds, mine, key0);
+        rs.tile(lds, mine, t, key0);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     if (__any(odd)) rs.odd_values(k, tiles.from + wave, WAVES);
@@ -236,9 +422,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const 
         ll[wave * RW + at.n] = at.l;
     }
     __syncthreads();
-    const int row = threadIdx.x >> 4, jt = threadIdx.x & 15;  // 16 threads to a row
-    if (row0 + row >= k.sq.T * a.group) return;
-    const bool all = k.parts == 1;
+    const int row = thread >> 4, jt = thread & 15;  // 16 threads to a row
+    if (row >= RW || row0 + row >= k.sq.T * a.group) return;  // (no barrier follows here)
+    const bool all = k.whole;
+    const int64_t slot_row = slot << c.rows_shift;
     float mm = M_START;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) mm = fmaxf(mm, lm[row + w * RW]);
@@ -263,6 +450,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const 
     }
     if (!all && jt == 0) *reinterpret_cast<v2f *>(a.ws_ml + 2 * (slot_row + row)) = v2f{mm, sum};
 }
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const ChunkArgs c) {
+    constexpr int WAVES = 4;
+    __shared__ __align__(1024) char lds[WAVES * Few<E, F8, D>::WAVE_BYTES];
+    __shared__ float lm[WAVES * 16], ll[WAVES * 16];
+    __shared__ int before[CHUNK_RUN_BLOCKS + 1], waves[WAVES];
+    Work<256> work(c, before, waves);
+    Block k;
+    int64_t slot;
+    while (work.next(k, slot)) {
+        few_rows<E, F8, D, WAVES>(c, k, slot, lds, lm, ll);
+        __syncthreads();  // (the sums in LDS have been read)
+    }
+}
 
 // Up to 128 rows: 4 waves of 32 share the tiles, two in LDS.
 template <class E, bool F8, int D>
@@ -273,16 +474,18 @@ __global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
 
     __shared__ __align__(1024) char lds[2 * TL::BYTES];
     __shared__ int odd;  // whether masked tiles staged so far have infinite or NaN values
+    __shared__ int before[CHUNK_RUN_BLOCKS + 1], waves[4];
 
+    Work<256> work(c, before, waves);
     Block k;
-    int64_t slot_row;
-    if (!my_block(c, k, slot_row)) return;
+    int64_t slot;
     const AttnArgs &a = c.a;
-    const Tiles<KEYS> tiles(c, k);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     TL tl(a, threadIdx.x);
-    RS rs(a, tiles);
     if (threadIdx.x == 0) odd = 0;
+    while (work.next(k, slot)) {
+    const Tiles<KEYS> tiles(c, k);
+    RS rs(a, tiles, threadIdx.x);
     tl.aim(k.b, k.h, k.sq);
     const int first = tiles.from;
     typename TL::Place next = tl.find(tiles.key(first));
@@ -294,19 +497,19 @@ __global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
     rs.begin(k, row0);
     __syncthreads();
     tl.store_k(lds, 0);
-    if (tl.store_v(lds, TL::K_BYTES, tiles.key(first), tiles.edge(tiles.key(first)))) odd = 1;
+    if (tl.store_v(lds, TL::K_BYTES, tiles.key(first), tiles.block.at(first))) odd = 1;
     tl.load_k(next);
     tl.load_v(next);
     next = tl.find(tiles.key(first + 2));
     int buf = 0;
     for (int t = first; t < tiles.to; ++t) {
         __syncthreads();
-        if (rows) rs.tile(lds, buf, tiles.key(t));
+        if (rows) rs.tile(lds, buf, t, tiles.key(t));
         buf = TL::BYTES - buf;
         if (t + 1 < tiles.to) {
             const int key1 = tiles.key(t + 1);
             tl.store_k(lds, buf);
-            if (tl.store_v(lds, buf + TL::K_BYTES, key1, tiles.edge(key1))) odd = 1;
+            if (tl.store_v(lds, buf + TL::K_BYTES, key1, tiles.block.at(t + 1))) odd = 1;
             tl.load_k(next);
             tl.load_v(next);
             next = tl.find(tiles.key(t + 3));
@@ -314,164 +517,394 @@ __global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
     }
     __syncthreads();
     if (odd) rs.odd_values(k, tiles.from, 1);
-    rs.at.put(k.parts == 1, slot_row + wave * RW);
+    rs.put(k, slot, wave);
+    }
 }
 
-// More rows: 8 waves, two to a SIMD, the second four half a turn behind the first
-// (kq_attn.hip, attn_wide_kernel: the same turns).
-template <class E, bool F8, int D>
+// A wave's share of the copies of tiles into LDS (8 waves share them).  A copy fills 1 KB
+// of LDS in the order of the lanes, so the places of Tile::k_pos and v_pos are met by
+// what each lane reads: the piece that belongs where it writes.  A wave's keys lie in one
+// page, and so do the values of a tile where a page covers it: their addresses are
+// scalar, looked up a turn before they are needed, and a lane adds an offset that never
+// changes.
+// SMALL: pages smaller than a tile.
+template <class E, bool F8, int D, int KEYS, int RW, bool SMALL>
+struct Stage {
+    typedef Tile<E, F8, D, KEYS, RW, 64, true> PL;  // (for the places in LDS alone)
+    typedef Frag<E, F8> FR;
+    static constexpr int ES = FR::BYTES, KB = PL::KB, VB = PL::VB;
+    static constexpr int COPIES = KEYS * KB / 1024;             // of a tile's keys, and of its values
+    static constexpr int N = COPIES >= 8 ? COPIES / 8 : 1;      // a wave's of each
+    static constexpr bool HALF = COPIES < 8;                    // the first 4 waves: keys, the others: values
+    static constexpr int TURN = HALF ? 1 : 2 * N;               // a wave's of a tile
+    static constexpr int K_ROWS = N * 1024 / KB;                // keys of a wave, in one run of 16
+    static_assert(16 % K_ROWS == 0 && (HALF ? COPIES == 4 : COPIES % 8 == 0), "a wave's keys share a page");
+
+    const_ints pages;     // the sequence's row of the table
+    const char *k_head, *v_head;  // the head's place in page 0
+    uint64_t page_bytes;  // from page to page
+    int last_page, shift;
+    int wave, lane, total;
+    uint32_t k_off[N], v_off[N];  // of this lane's pieces from the first key's row / the tile's first value
+    int v_key[N];         // the first key of its piece of the values
+    uint32_t lds;
+
+    __device__ __forceinline__ Stage(const AttnArgs &a, const Block &k, char *lds_, int wave_, int lane_) : wave(wave_), lane(lane_) {
+        shift = a.cache.page_shift;
+        total = k.sq.total;
+        pages = (const_ints)a.batch.pages + (int64_t)k.b * a.batch.max_pages;
+        last_page = (int)(a.cache.n_pages - 1);
+        page_bytes = (uint64_t)a.cache.heads * (D * ES) << shift;
+        const int64_t head = (int64_t)k.h * (D * ES) << shift;
+        k_head = a.cache.k + head;
+        v_head = a.cache.v + head;
+        lds = lds_offset(lds_);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k_at = copy(i) * 1024 + lane * 16, v_at = copy(i) * 1024 + lane * 16;  // in the tile
+            const int row = k_at / KB, piece = (k_at % KB / 16) ^ PL::k_xor(row);
+            k_off[i] = (row - k_row()) * KB + piece * 16;
+            const int d = v_at / VB, v_piece = (v_at % VB / 16) ^ PL::v_xor(d);
+            v_key[i] = v_piece * (16 / ES);
+            v_off[i] = ((uint32_t)d << shift) * ES + (SMALL ? 0 : v_piece * 16);
+        }
+    }
+    __device__ __forceinline__ int copy(int i) const { return HALF ? wave & 3 : N * wave + i; }
+    __device__ __forceinline__ int k_row() const { return copy(0) * 1024 / KB; }
+    __device__ __forceinline__ bool has_k() const { return !HALF || wave < 4; }
+    __device__ __forceinline__ bool has_v() const { return !HALF || wave >= 4; }
+
+    // A slot past the sequence's end is taken to lie in its last run (masked later).
+    __device__ __forceinline__ int k_slot(int key0) const { return min(key0 + k_row(), (total - 1) & -K_ROWS); }
+    __device__ __forceinline__ int v_slot(int key0) const { return min(key0, (total - 1) & -KEYS); }
+    __device__ __forceinline__ int lane_slot(int key0, int i) const {
+        return min(key0 + v_key[i], ((total - 1) & ~15) + (v_key[i] & 15));
+    }
+    __device__ __forceinline__ uint64_t page_at(int e) const { return (uint64_t)(uint32_t)min(max(e, 0), last_page) * page_bytes; }
+    // The tile's page entries.
+    __device__ __forceinline__ int k_entry(int key0) const { return pages[k_slot(key0) >> shift]; }
+    struct Pages {
+        int e[SMALL ? KEYS / 16 : 1];  // of its runs of 16 slots, or one for all
+    };
+    __device__ __forceinline__ Pages v_entry(int key0) const {
+        Pages p;
+        if constexpr (SMALL) {
+#pragma unroll
+            for (int r = 0; r < KEYS / 16; ++r) p.e[r] = pages[min(key0 + 16 * r, (total - 1) & ~15) >> shift];
+        } else {
+            p.e[0] = pages[v_slot(key0) >> shift];
+        }
+        return p;
+    }
+    __device__ __forceinline__ void copy_k(int buf, int key0, int e) const {
+        if (!has_k()) return;
+        const char *p = k_head + page_at(e) + (uint32_t)((k_slot(key0) & ((1 << shift) - 1)) * KB);
+#pragma unroll
+        for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, k_off[i]);
+    }
+    __device__ __forceinline__ void copy_v(int buf, int key0, const Pages &e) const {
+        if (!has_v()) return;
+        const int mask = (1 << shift) - 1;
+        if constexpr (SMALL) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int run = v_key[i] >> 4;
+                int mine = e.e[0];
+#pragma unroll
+                for (int r = 1; r < KEYS / 16; ++r) mine = run == r ? e.e[r] : mine;
+                copy16(lds + buf + copy(i) * 1024, v_head + page_at(mine) + (v_off[i] + (uint32_t)((lane_slot(key0, i) & mask) * ES)));
+            }
+        } else {
+            const char *p = v_head + page_at(e.e[0]) + (uint32_t)((v_slot(key0) & mask) * ES);
+#pragma unroll
+            for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, v_off[i]);
+        }
+    }
+    // In a tile that some row does not see whole, after this wave's copies of it have arrived:
+    // zeros for values past the end, which may be anything, and for infinite and NaN ones;
+    // whether this lane met any of those.
+    __device__ __forceinline__ bool clean_v(char *at, int buf, int key0) const {
+        bool found = false;
+        if (!has_v()) return false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v4u *p = reinterpret_cast<v4u *>(at + buf + copy(i) * 1024 + lane * 16);
+            v4u w = *p;
+            const int left = total - (key0 + v_key[i]);
+            if constexpr (F8) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    typename FR::raw r = {w[2 * j], w[2 * j + 1]};
+                    FR::first(r, min(max(left - 8 * j, 0), 8));
+                    found |= FR::drop_odd(r);
+                    w[2 * j] = r[0];
+                    w[2 * j + 1] = r[1];
+                }
+            } else {
+                FR::first(w, min(max(left, 0), 8));
+                found |= FR::drop_odd(w);
+            }
+            *p = w;
+        }
+        return found;
+    }
+};
+
+// More rows: 8 waves, two to a SIMD, share the tiles, and the second four run half a turn
+// behind the first.  A turn has a half of matrix products (the values of the tile before,
+// the scores of this one) and a half of vector work (softmax, copies), so that one wave
+// of a SIMD keeps its matrix unit busy while the other has its vector unit; a barrier ends
+// every half.  Times in halves: the early waves multiply tile i at 2 i, the late ones at
+// 2 i + 1.  There are three buffers each for keys and values.  In its vector half i an
+// early wave (at 2 i + 1) starts its copies of keys i + 2 and values i + 1: keys i - 1 and
+// values i - 2 before them were last read at 2 i - 1, by the late waves.  A late wave (at 2 i
+// + 2) starts those of keys i + 3 and values i + 2: keys i and values i - 1 were last read
+// at 2 i + 1.  Both wait for them at the end of their next vector half, at 2 i + 4 at
+// the latest, and they are first read (keys i + 2 and values i + 1 by the early waves, at
+// 2 i + 4; keys i + 3 at 2 i + 6) after the barrier that follows.
+// A sequence that brings only a few rows among others that bring many takes the way of
+// the few.
+template <class E, bool F8, int D, bool SMALL>
 __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
     constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
-    typedef Tile<E, F8, D, KEYS, RW, 512, false> TL;
+    typedef Stage<E, F8, D, KEYS, RW, SMALL> ST;
     typedef Rows<E, F8, D, KEYS, RW> RS;
     typedef typename RS::AT AT;
+    constexpr int BYTES = AT::TL::BYTES, K_BYTES = AT::TL::K_BYTES, FEW_BYTES = Few<E, F8, D>::WAVE_BYTES;
+    constexpr int FEW_WAVES = FEW_IN_WIDE<E, F8, D>;
+    constexpr int LDS = 3 * BYTES > FEW_WAVES * FEW_BYTES ? 3 * BYTES : FEW_WAVES * FEW_BYTES;
 
-    __shared__ __align__(1024) char lds[3 * TL::BYTES];  // keys and values by turns
+    __shared__ __align__(1024) char lds[LDS];  // keys and values by turns
+    __shared__ float lm[FEW_WAVES * 16 + 1], ll[FEW_WAVES * 16 + 1];
     __shared__ int odd;
+    __shared__ int before_j[CHUNK_RUN_BLOCKS + 1], waves[8];
 
+    Work<512> work(c, before_j, waves);
     Block k;
-    int64_t slot_row;
-    if (!my_block(c, k, slot_row)) return;
+    int64_t slot;
     const AttnArgs &a = c.a;
-    const Tiles<KEYS> ts(c, k);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool late = wave >= 4;
-    TL tl(a, threadIdx.x);
-    RS rs(a, ts);
-    AT &at = rs.at;
     if (threadIdx.x == 0) odd = 0;
-    const int first = ts.from, tiles = ts.to - ts.from;
-    tl.aim(k.b, k.h, k.sq);
-    // keys 0, 1 and values 0 to LDS; keys 2 and values 1 on their way
-    typename TL::Place p0 = tl.find(ts.key(first)), p1 = tl.find(ts.key(first + 1)), p2 = tl.find(ts.key(first + 2));
-    tl.load_k(p0);
-    tl.load_v(p0);
-    rs.begin(k, (k.rb << c.rows_shift) + wave * RW);
-    __syncthreads();
-    tl.store_k(lds, 0);
-    if (tl.store_v(lds, TL::K_BYTES, ts.key(first), ts.edge(ts.key(first)))) odd = 1;
-    tl.load_k(p1);
-    tl.store_k(lds, TL::BYTES);
-    tl.load_v(p1);
-    tl.load_k(p2);
-    p1 = p2;
-    p2 = tl.find(ts.key(first + 3));
-    float p[AT::NT * AT::NR];
-    typename AT::op_t pf[AT::NS];
-    int key0 = ts.key(first), buf = 0;  // buf: where tile i is (i % 3)
-    __syncthreads();
-    if (late) __syncthreads();
-    auto vector_half = [&](int i, int before, int after) {
-        rs.mask(key0, p);
-        float sum = 0.f;
+    while (work.next(k, slot)) {
+        __syncthreads();  // the piece before has been read
+        if constexpr (FEW_WAVES > 0) {
+            if (k.sq.T * a.group <= 16) {
+                few_rows<E, F8, D, FEW_WAVES>(c, k, slot, lds, lm, ll);
+                continue;
+            }
+        }
+        const Tiles<KEYS> ts(c, k);
+        const unsigned thread = this_thread();
+        const ST st(a, k, lds, wave, thread & 63);
+        RS rs(a, ts, thread);
+        AT &at = rs.at;
+        // tiles first .. first + n - 1
+        const int first = ts.from, n = ts.to - ts.from;
+        const int ahead = late ? 1 : 0;  // the copies of a vector half: keys i + 2 + ahead, values i + 1 + ahead
+        for (int i = 0; i < 2 + ahead; ++i) {
+            const int key = ts.key(first + i);
+            st.copy_k(i * BYTES, key, st.k_entry(key));
+            if (i < 1 + ahead) st.copy_v(i * BYTES + K_BYTES, key, st.v_entry(key));
+        }
+        int kn = ts.key(first + 2 + ahead), vn = ts.key(first + 1 + ahead);  // the slots of the next
+        int ke = st.k_entry(kn);
+        typename ST::Pages ve = st.v_entry(vn);
+        int kb = late ? 0 : 2 * BYTES, vb = late ? 2 * BYTES : BYTES;  // and their buffers
+        rs.begin(k, (k.rb << c.rows_shift) + wave * RW);
+        float p[AT::NT * AT::NR];
+        typename AT::op_t pf[AT::NS];
+        int key0 = ts.key(first), buf = 0;  // where the turn's tile is
+        arrived<0>();
+        for (int i = 0; i < 1 + ahead; ++i)
+            if (ts.block.at(first + i) && st.clean_v(lds, i * BYTES + K_BYTES, ts.key(first + i))) odd = 1;
+        __syncthreads();
+        if (late) __syncthreads();
+        auto vector_half = [&](int i) {
+            const int t = first + i;
+            const int clean = t + ahead;  // the tile whose values' copies, started a turn ago, are waited for here
+            const bool more = i + 1 < n;
+            const int old = vb == 0 ? 2 * BYTES : vb - BYTES;
+            if (more) {
+                const int kn2 = ts.key(t + 3 + ahead), ke2 = st.k_entry(kn2);
+                const typename ST::Pages ve2 = st.v_entry(kn);
+                st.copy_v(vb + K_BYTES, vn, ve);
+                st.copy_k(kb, kn, ke);
+                vn = kn;
+                kn = kn2;
+                ke = ke2;
+                ve = ve2;
+                kb = kb == 2 * BYTES ? 0 : kb + BYTES;
+                vb = vb == 2 * BYTES ? 0 : vb + BYTES;
+            }
+            rs.mask(t, key0, p);
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < AT::NS; ++s) {
-            v4u w = __builtin_bit_cast(v4u, at.probabilities(p, s, sum));
-            asm volatile("" : "+v"(w));  // (now, while the loads for the staging below arrive)
-            pf[s] = __builtin_bit_cast(typename AT::op_t, w);
-        }
-        at.l += sum;
-        if (i + 1 < tiles) {
-            const int key1 = ts.key(first + i + 1);
-            tl.store_k(lds, before);  // keys i + 2
-            if (tl.store_v(lds, after + TL::K_BYTES, key1, ts.edge(key1))) odd = 1;
-            tl.load_v(p1);
-            tl.load_k(p2);
-            p1 = p2;
-            p2 = tl.find(ts.key(first + i + 4));
-        }
-    };
-    at.template products<false, true, 6>(lds, 0, pf, 0, p);
-    __syncthreads();
-    vector_half(0, 2 * TL::BYTES, TL::BYTES);
-    __syncthreads();
-    for (int i = 1; i < tiles; ++i) {
-        key0 = ts.key(first + i);
-        const int before = buf;
-        buf = buf == 2 * TL::BYTES ? 0 : buf + TL::BYTES;
-        at.template products<true, true, 6>(lds, before + TL::K_BYTES, pf, buf, p);
+            for (int s = 0; s < AT::NS; ++s) {
+                v4u w = __builtin_bit_cast(v4u, rs.probabilities(p, s, sum));
+                asm volatile("" : "+v"(w));  // (here, and not among the products)
+                pf[s] = __builtin_bit_cast(typename AT::op_t, w);
+            }
+            at.l += sum[0] + sum[1];
+            key0 = ts.key(t + 1);
+            if (more)
+                arrived<ST::TURN>();
+            else
+                arrived<0>();
+            if (i && clean < ts.to && ts.block.at(clean) && st.clean_v(lds, old + K_BYTES, ts.key(clean))) odd = 1;
+        };
+        at.template products<false, true, 6>(lds, 0, pf, 0, p);
         __syncthreads();
-        vector_half(i, before, buf == 2 * TL::BYTES ? 0 : buf + TL::BYTES);
+        vector_half(0);
         __syncthreads();
+        for (int i = 1; i < n; ++i) {
+            const int before = buf;
+            buf = buf == 2 * BYTES ? 0 : buf + BYTES;
+            at.template products<true, true, 6>(lds, before + K_BYTES, pf, buf, p);
+            __syncthreads();
+            vector_half(i);
+            __syncthreads();
+        }
+        at.template products<true, false, 6>(lds, buf + K_BYTES, pf, 0, p);
+        __syncthreads();
+        if (!late) __syncthreads();
+        if (odd) rs.odd_values(k, ts.from, 1);
+        rs.put(k, slot, wave);
     }
-    at.template products<true, false, 6>(lds, buf + TL::K_BYTES, pf, 0, p);
-    __syncthreads();
-    if (!late) __syncthreads();
-    if (odd) rs.odd_values(k, ts.from, 1);
-    at.put(k.parts == 1, slot_row + wave * RW);
 }
 
-// out = sum over the parts of a cut block, each weighted by exp2(its maximum - the
-// largest).  D / 4 threads read a part's sums of a row; a workgroup has 256 / (D / 4)
-// such sets, `sets` of them to a row, which share out its parts.
-template <class E, int D>
-__global__ __launch_bounds__(256) void chunk_join_kernel(const ChunkArgs c, int sets) {
-    constexpr int TPP = D / 4, SETS = 256 / TPP;
-    __shared__ v4f so[256];
-    __shared__ v2f sml[SETS];
-    const AttnArgs &a = c.a;
-    const int heads = a.cache.heads, rows_wg = SETS / sets;
-    const unsigned turns = (1u << c.rows_shift) / rows_wg;  // workgroups of a block
-    const unsigned jh = blockIdx.x / turns;
-    const int j = (int)(jh / heads), h = (int)(jh % heads);
-    Block k;
-    if (!block_at(c, j, h, 0, k) || k.parts == 1) return;
+// Where the parts of a cut block lie: workgroups w0 .. w1 have one each.
+struct Parts {
+    int from, w0, w1;
+    Runs runs;
+    __device__ __forceinline__ Parts(const ChunkArgs &c, int j, int h, int units)
+        : runs(c.a.ws_seq[c.blocks] * c.a.cache.heads, min(c.a.grid, c.a.ws_seq[c.blocks] * c.a.cache.heads)) {
+        from = h * c.a.ws_seq[c.blocks] + c.a.ws_seq[j];
+        w0 = runs.holder(from);
+        w1 = runs.holder(from + units - 1);
+    }
+    // a workgroup's first piece lies in its first slot
+    __device__ __forceinline__ int64_t slot(int w) const { return 2 * (int64_t)w + (runs.begin(w) < from); }
+};
+// Adds a part (maximum and weight ml, sums po) to the sums o, weight l under maximum m.
+template <int N>
+__device__ __forceinline__ void join(v4f (&o)[N], float &m, float &l, v2f ml, const v4f (&po)[N]) {
+    const float up = fmaxf(m, ml[0]);
+    const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
+    m = up;
+    l = l * f + ml[1] * pf;
+#pragma unroll
+    for (int q = 0; q < N; ++q) o[q] = o[q] * f + po[q] * pf;
+}
+__device__ __forceinline__ int64_t out_row(const ChunkArgs &c, const Block &k, int in_seq) {
+    const int G = c.a.group, tok = in_seq / G;
+    return (int64_t)(k.sq.first + tok) * ((int64_t)c.a.cache.heads * G) + k.h * G + (in_seq - tok * G);
+}
+// A row of up to 16 that few_rows left: D / 4 threads to a row, `sets` sets of them, which
+// share out its parts.
+template <class E, int D, int THREADS>
+__device__ __forceinline__ void join_few(const ChunkArgs &c, const Block &k, const Parts &parts, int row, int sets, v4f *so, v2f *sml) {
+    constexpr int TPP = D / 4;
     const int lane = threadIdx.x % TPP, set = threadIdx.x / TPP, sub = set % sets;
-    const int row = (int)(blockIdx.x % turns) * rows_wg + set / sets;
-    const int64_t in_seq = ((int64_t)k.rb << c.rows_shift) + row;
-    const bool used = in_seq < (int64_t)k.sq.T * a.group;
-    const int64_t slot0 = (((int64_t)j * heads + h) * c.parts << c.rows_shift) + row;
+    const int in_seq = (k.rb << c.rows_shift) + row;
+    const bool used = row < 16 && in_seq < k.sq.T * c.a.group;
     float m = M_START, l = 0.f;
-    v4f o = {0.f, 0.f, 0.f, 0.f};
+    v4f o[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
     if (used) {
-        for (int p = sub; p < k.parts; p += sets) {
-            const int64_t r = slot0 + ((int64_t)p << c.rows_shift);
-            const v2f ml = *reinterpret_cast<const v2f *>(a.ws_ml + 2 * r);
-            const v4f po = *reinterpret_cast<const v4f *>(a.ws_o + r * D + 4 * lane);
-            const float up = fmaxf(m, ml[0]);
-            const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
-            m = up;
-            l = l * f + ml[1] * pf;
-            o = o * f + po * pf;
+        for (int w = parts.w0 + sub; w <= parts.w1; w += sets) {
+            const int64_t r = (parts.slot(w) << c.rows_shift) + row;
+            const v4f po[1] = {*reinterpret_cast<const v4f *>(c.a.ws_o + r * D + 4 * lane)};
+            join<1>(o, m, l, *reinterpret_cast<const v2f *>(c.a.ws_ml + 2 * r), po);
         }
     }
     if (sets > 1) {
-        so[threadIdx.x] = o;
+        so[threadIdx.x] = o[0];
         if (lane == 0) sml[set] = v2f{m, l};
         __syncthreads();
         if (sub) return;
         for (int s = 1; s < sets; ++s) {
-            const v2f ml = sml[set + s];
-            const float up = fmaxf(m, ml[0]);
-            const float f = __builtin_amdgcn_exp2f(m - up), pf = __builtin_amdgcn_exp2f(ml[0] - up);
-            m = up;
-            l = l * f + ml[1] * pf;
-            o = o * f + so[threadIdx.x + s * TPP] * pf;
+            const v4f po[1] = {so[threadIdx.x + s * TPP]};
+            join<1>(o, m, l, sml[set + s], po);
         }
     }
     if (!used) return;
-    const float norm = l == 0.f ? 0.f : a.v_scale / l;
-    const int tok = (int)(in_seq / a.group);
-    const int64_t row_out = (int64_t)(k.sq.first + tok) * ((int64_t)heads * a.group) + h * a.group + (in_seq - (int64_t)tok * a.group);
-    put4<E>(a, true, o * norm, row_out * D + 4 * lane, 0);
+    put4<E>(c.a, true, o[0] * (l == 0.f ? 0.f : c.a.v_scale / l), out_row(c, k, in_seq) * D + 4 * lane, 0);
+}
+// out = sum over the parts of a cut block, each weighted by exp2(its maximum - the
+// largest).  Blocks of 16 rows: a workgroup to a row.
+template <class E, int D>
+__global__ __launch_bounds__(256) void chunk_join_few_kernel(const ChunkArgs c) {
+    __shared__ v4f so[256];
+    __shared__ v2f sml[1024 / D];
+    const unsigned jh = blockIdx.x >> 4;
+    const int j = (int)(jh / (unsigned)c.a.cache.heads);
+    Block k;
+    k.h = (int)(jh - (unsigned)j * c.a.cache.heads);
+    if (!block_of(c, block_seq(c, j), j, k)) return;
+    const Parts parts(c, j, k.h, k.units);
+    if (parts.w0 == parts.w1) return;  // finished there
+    join_few<E, D, 256>(c, k, parts, blockIdx.x & 15, 1024 / D, so, sml);
+}
+// More rows: a workgroup to a block, a wave to the rows that one wave left.
+template <class E, int D, int RW, int WAVES, bool FEW>
+__global__ __launch_bounds__(WAVES * 64) void chunk_join_kernel(const ChunkArgs c) {
+    constexpr int QUADS = RW * D / 256;
+    const int j = (int)(blockIdx.x / (unsigned)c.a.cache.heads);
+    Block k;
+    k.h = (int)(blockIdx.x - (unsigned)j * c.a.cache.heads);
+    if (!block_of(c, block_seq(c, j), j, k)) return;
+    const Parts parts(c, j, k.h, k.units);
+    if (parts.w0 == parts.w1) return;  // finished there
+    if (FEW && k.sq.T * c.a.group <= 16) {
+        constexpr int TPP = D / 4, SETS = WAVES * 64 / TPP;
+        for (int row = threadIdx.x / TPP; row < 16; row += SETS) join_few<E, D, WAVES * 64>(c, k, parts, row, 1, nullptr, nullptr);
+        return;
+    }
+    const int lane = threadIdx.x & 63, n = lane & (RW - 1), g = lane / RW, row = (threadIdx.x >> 6) * RW + n;
+    const int in_seq = (k.rb << c.rows_shift) + row;
+    float m = M_START, l = 0.f;
+    v4f o[QUADS];
+#pragma unroll
+    for (int q = 0; q < QUADS; ++q) o[q] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int w = parts.w0; w <= parts.w1; ++w) {
+        const int64_t r = (parts.slot(w) << c.rows_shift) + row;
+        const v4f *from = reinterpret_cast<const v4f *>(c.a.ws_o + (r - n) * D) + lane;
+        v4f po[QUADS];
+#pragma unroll
+        for (int q = 0; q < QUADS; ++q) po[q] = from[q * 64];
+        join<QUADS>(o, m, l, *reinterpret_cast<const v2f *>(c.a.ws_ml + 2 * r), po);
+    }
+    if (in_seq >= k.sq.T * c.a.group) return;
+    const float norm = l == 0.f ? 0.f : c.a.v_scale / l;
+    const int64_t to = out_row(c, k, in_seq) * D;
+    constexpr int NR = RW * RW / 64;
+#pragma unroll
+    for (int q = 0; q < QUADS; ++q) {
+        const int d = q / (NR / 4), r = q % (NR / 4) * 4;
+        put4<E>(c.a, true, o[q] * norm, to + RW * d + 2 * r + 4 * g, 0);
+    }
 }
 
 template <class E, bool F8, int D>
 hipError_t launch_dim(const ChunkArgs &c, const ChunkPlan &p, hipStream_t stream) {
-    const int64_t heads = c.a.cache.heads;
-    const dim3 grid((unsigned)(p.blocks * heads * p.parts));
+    const dim3 grid((unsigned)p.grid);
     if (p.waves == 0)
         hipLaunchKernelGGL((chunk_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
+    else if (p.waves == 8 && (1 << c.a.cache.page_shift) < (D == 256 ? 32 : 64))
+        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, true>), grid, dim3(512), 0, stream, c);
     else if (p.waves == 8)
-        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D>), grid, dim3(512), 0, stream, c);
+        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, false>), grid, dim3(512), 0, stream, c);
     else if constexpr (D < 256)
         hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.bytes == 0) return e;
-    constexpr int SETS = 1024 / D;
-    const int sets = p.waves == 0 ? SETS : 1;
-    hipLaunchKernelGGL((chunk_join_kernel<E, D>), dim3((unsigned)(p.blocks * heads * ((1 << p.rows_shift) * sets / SETS))),
-                       dim3(256), 0, stream, c, sets);
+    if (e != hipSuccess || !p.runs) return e;
+    const unsigned blocks = (unsigned)(p.blocks * c.a.cache.heads);
+    if (p.waves == 0)
+        hipLaunchKernelGGL((chunk_join_few_kernel<E, D>), dim3(16 * blocks), dim3(256), 0, stream, c);
+    else if (p.waves == 8)
+        hipLaunchKernelGGL((chunk_join_kernel<E, D, D == 256 ? 16 : 32, 8, FEW_IN_WIDE<E, F8, D> != 0>), dim3(blocks), dim3(512), 0, stream, c);
+    else if constexpr (D < 256)
+        hipLaunchKernelGGL((chunk_join_kernel<E, D, 32, 4, false>), dim3(blocks), dim3(256), 0, stream, c);
     return hipGetLastError();
 }
 

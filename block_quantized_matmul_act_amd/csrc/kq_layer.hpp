@@ -27,21 +27,26 @@ hipError_t launch_norm_quantize(const NormArgs &a, int bs, int x_type, int r_typ
 
 // How attention of chunks is shared out: blocks of 1 << rows_shift query rows of a
 // key head, numbered so that a block's sequence can be found from the offsets
-// alone (some numbers stay unused); a block's keys, in units of CHUNK_UNIT slots, are
-// cut into at most `parts` parts of `part_units` units or more.
+// alone (some numbers stay unused).  A workgroup takes a block, or (runs) `grid`
+// workgroups take equal runs of units of CHUNK_UNIT slots of all the blocks and leave at
+// most two cut blocks each, a slot of the workspace to either.
 constexpr int CHUNK_UNIT_SHIFT = 6, CHUNK_UNIT = 1 << CHUNK_UNIT_SHIFT;
+constexpr int CHUNK_RUN_BLOCKS = 2048;  // block numbers of a key head in a call of runs
 struct ChunkPlan {
     int waves;  // 0: the kernel for up to 16 rows
-    int rows_shift, parts, part_units;
-    int64_t blocks;                 // numbers, for one key head
-    int64_t o_bytes, bytes;         // workspace: sums, then their maxima and weights
+    int rows_shift;
+    bool runs;
+    int64_t blocks;  // numbers, for one key head
+    int64_t grid;    // workgroups
+    // workspace: sums, their maxima and weights (to ml_end), the units before each block
+    int64_t o_bytes, ml_end, bytes;
 };
-ChunkPlan chunk_plan(const kq_cache &cache, int64_t n_seqs, int64_t n_tokens, int64_t q_heads, int64_t window,
-                     int64_t sinks, int64_t max_tokens, int64_t max_len);
+ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_heads, int64_t window, int64_t sinks,
+                     int64_t max_tokens, int64_t max_len);
 struct ChunkArgs {
     AttnArgs a;
     int window, sinks;  // window: INT32_MAX where there is none
-    int rows_shift, blocks, parts, part_units;
+    int rows_shift, blocks, runs;
 };
 hipError_t launch_chunk(const ChunkArgs &a, const ChunkPlan &p, int type, int dim, int q_type, hipStream_t stream);
 
@@ -60,7 +65,15 @@ struct LoraArgs {
     int64_t ldo;
     float *t;  // [M][rank]
 };
-bool lora_few(int64_t M);
+// Few rows: a wave to a value of t and to 64 outputs of a row, whatever adapters the rows
+// have.  More: tiles of rows, an adapter of a tile after another.  rows x outputs of 4096
+// inputs, us of a call, few / tiles (13.4: the call on the host), every row with an adapter
+// of its own, and all with one:
+//   rank 16:  256 x 14336  18.8/44.5 17.8/13.5   256 x 4096  13.4/40.0 13.6/13.5
+//             512 x 14336  30.7/56.7 29.6/15.9   512 x 4096  15.9/40.5 15.5/13.8
+//   rank 64:   96 x 14336  37.1/94.5 18.4/15.4    96 x 4096  16.5/65.0 13.6/13.9
+//             256 x 14336  77.7/109  34.0/18.5   256 x 4096  22.1/64.9 17.6/14.4
+inline bool lora_few(int64_t M, int64_t rank) { return M * rank <= 4096; }
 hipError_t launch_lora(const LoraArgs &a, int type, hipStream_t stream);
 
 }  // namespace kq

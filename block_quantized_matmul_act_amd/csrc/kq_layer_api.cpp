@@ -37,10 +37,8 @@ int check_chunk(const kq_cache *c, const kq_batch *s, int64_t q_heads, int64_t w
     if (rc == KQ_OK) return KQ_OK;
     if (s->n_tokens * q_heads >= ((int64_t)1 << 31) / c->dim) return KQ_ERR_UNSUPPORTED;
     if (max_tokens == 0 || max_len == 0) return KQ_ERR_SHAPE;  // rows to compute, none expected
-    const ChunkPlan p = chunk_plan(*c, s->n_seqs, s->n_tokens, q_heads, window, sinks, max_tokens, max_len);
-    // workgroups of up to 512 threads, and of 256 for 4 rows or more to join the parts
-    if (p.blocks > MAX_GROUPS / 2 / c->heads / p.parts) return KQ_ERR_UNSUPPORTED;
-    if (p.bytes && p.blocks > (MAX_GROUPS >> p.rows_shift) / c->heads) return KQ_ERR_UNSUPPORTED;
+    const ChunkPlan p = chunk_plan(*c, *s, q_heads, window, sinks, max_tokens, max_len);
+    if (p.grid > MAX_GROUPS / 2) return KQ_ERR_UNSUPPORTED;  // workgroups of up to 512 threads
     return 1;
 }
 
@@ -52,9 +50,9 @@ int check_lora(int type, int64_t rank, int64_t n_adapters, int act_fmt, int64_t 
     if (rank != 8 && rank != 16 && rank != 32 && rank != 64 && rank != 128) return KQ_ERR_UNSUPPORTED;
     if (n_adapters && std::max(N, K) > kMaxBytes / rank / n_adapters) return KQ_ERR_SHAPE;
     if (M == 0 || N == 0) return KQ_OK;
-    // 64 rows to a workgroup along a grid's second dimension; columns are counted in
-    // 32 bits, up to 255 past the last
-    if (M > (int64_t)65535 * 64 || N > kMaxDim - 256) return KQ_ERR_UNSUPPORTED;
+    // 32 rows or more to a workgroup along a grid's second dimension; columns are counted
+    // in 32 bits, up to 255 past the last
+    if (M > (int64_t)65535 * 32 || N > kMaxDim - 256) return KQ_ERR_UNSUPPORTED;
     return 1;
 }
 
@@ -68,29 +66,32 @@ void count_layer(int variant) { g_count[variant].fetch_add(1); }
 
 namespace kq {
 
-ChunkPlan chunk_plan(const kq_cache &cache, int64_t n_seqs, int64_t n_tokens, int64_t q_heads, int64_t window,
-                     int64_t sinks, int64_t max_tokens, int64_t max_len) {
+ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_heads, int64_t window, int64_t sinks,
+                     int64_t max_tokens, int64_t max_len) {
     ChunkPlan p;
     const int64_t heads = cache.heads, group = q_heads / heads, dim = cache.dim;
-    max_tokens = std::min(max_tokens, n_tokens);
+    max_tokens = std::min(max_tokens, batch.n_tokens);
     const int64_t rows = max_tokens * group;
     p.waves = rows <= 16 ? 0 : rows <= 128 && dim < 256 ? 4 : 8;
     p.rows_shift = p.waves == 0 ? 4 : p.waves == 4 || dim == 256 ? 7 : 8;
-    p.blocks = ((n_tokens * group) >> p.rows_shift) + n_seqs;
-    // the slots that a block reads at most, and its units with the ends of two runs
-    int64_t slots = max_len;
-    if (window) slots = std::min(slots, window + sinks + ((int64_t)1 << p.rows_shift) / group + 1);
-    const int64_t units = (slots + CHUNK_UNIT - 1) / CHUNK_UNIT + 2;
-    const int64_t want = p.waves == 8 ? 256 : 512, groups = p.blocks * heads;
-    p.parts = groups >= want ? 1 : (int)std::min<int64_t>((want + groups - 1) / groups, (units + 1) / 2);
-    p.part_units = (int)((units + p.parts - 1) / p.parts);
-    const int64_t slot_rows = (groups * p.parts) << p.rows_shift;
-    p.o_bytes = p.parts > 1 ? slot_rows * dim * 4 : 0;
-    p.bytes = p.parts > 1 ? p.o_bytes + slot_rows * 8 : 0;
+    p.blocks = ((batch.n_tokens * group) >> p.rows_shift) + batch.n_seqs;
+    // the units of a block whose sequence has `slots` slots, at most
+    const auto units_of = [&](int64_t slots) {
+        if (window) slots = std::min(slots, window + sinks + ((int64_t)1 << p.rows_shift) / group + 1);
+        return (slots + CHUNK_UNIT - 1) / CHUNK_UNIT + 2;
+    };
+    const int64_t units = units_of(max_len), groups = p.blocks * heads, chip = p.waves == 8 ? 256 : 512;
+    p.runs = units > 4 && (groups < 2 * chip || units >= 256);
+    // (units are counted in int32, whatever the lengths; 16 workgroups of 256 threads or fewer join a block)
+    if (p.blocks > CHUNK_RUN_BLOCKS || groups > MAX_GROUPS / 16 || units_of(batch.max_pages * cache.page) > kMaxInt / groups)
+        p.runs = false;
+    p.grid = p.runs ? std::min(chip, groups * units / 2) : groups;
+    const int64_t slot_rows = p.runs ? 2 * p.grid << p.rows_shift : 0;
+    p.o_bytes = slot_rows * dim * 4;
+    p.ml_end = p.o_bytes + slot_rows * 8;
+    p.bytes = p.runs ? p.ml_end + (p.blocks + 1) * 4 : 0;
     return p;
 }
-
-bool lora_few(int64_t M) { return M <= 64; }
 
 }  // namespace kq
 
@@ -146,7 +147,7 @@ int kq_norm_quantize(int act_fmt, int x_type, const void *x, int64_t ldx, int r_
 size_t kq_attn_chunk_workspace(const kq_cache *cache, const kq_batch *batch, int64_t q_heads, int64_t window,
                                int64_t sinks, int64_t max_tokens, int64_t max_len) {
     if (check_chunk(cache, batch, q_heads, window, sinks, max_tokens, max_len) <= 0) return 0;
-    return (size_t)chunk_plan(*cache, batch->n_seqs, batch->n_tokens, q_heads, window, sinks, max_tokens, max_len).bytes;
+    return (size_t)chunk_plan(*cache, *batch, q_heads, window, sinks, max_tokens, max_len).bytes;
 }
 
 int kq_attn_chunk(const kq_cache *cache, const kq_batch *batch, int q_type, const void *q, int64_t q_heads,
@@ -162,7 +163,7 @@ int kq_attn_chunk(const kq_cache *cache, const kq_batch *batch, int q_type, cons
     if (rc <= 0) return rc;
     rc = check_step(cache, batch);
     if (rc != KQ_OK) return rc;
-    const ChunkPlan p = chunk_plan(*cache, batch->n_seqs, batch->n_tokens, q_heads, window, sinks, max_tokens, max_len);
+    const ChunkPlan p = chunk_plan(*cache, *batch, q_heads, window, sinks, max_tokens, max_len);
     if (!q || !out || (p.bytes && !workspace)) return KQ_ERR_NULL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KQ_ERR_ALIGN;
     if (workspace_bytes < (size_t)p.bytes) return KQ_ERR_SHAPE;
@@ -183,10 +184,11 @@ int kq_attn_chunk(const kq_cache *cache, const kq_batch *batch, int q_type, cons
     a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.o_bytes);
     k.window = window ? (int)window : INT32_MAX;
     k.sinks = window ? (int)sinks : 0;
+    a.ws_seq = p.runs ? reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + p.ml_end) : nullptr;
+    a.grid = (int)p.grid;
     k.rows_shift = p.rows_shift;
     k.blocks = (int)p.blocks;
-    k.parts = p.parts;
-    k.part_units = p.part_units;
+    k.runs = p.runs;
     if (launch_chunk(k, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
     count_layer(p.waves == 0 ? V_CHUNK_FEW : V_CHUNK_ROWS);
     return KQ_OK;
@@ -231,7 +233,7 @@ int kq_lora(int type, int64_t rank, const void *A, const void *B, const float *s
     a.ldo = ldo;
     a.t = static_cast<float *>(workspace);
     if (launch_lora(a, type, stream) != hipSuccess) return KQ_ERR_HIP;
-    count_layer(lora_few(M) ? V_LORA_FEW : V_LORA_TILE);
+    count_layer(lora_few(M, rank) ? V_LORA_FEW : V_LORA_TILE);
     return KQ_OK;
 }
 

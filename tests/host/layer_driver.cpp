@@ -40,15 +40,21 @@ hipError_t launch_norm_quantize(const NormArgs &a, int bs, int, int, hipStream_t
 hipError_t launch_chunk(const ChunkArgs &c, const ChunkPlan &p, int, int dim, int, hipStream_t) {
     ++chunks;
     plan = p;
-    const int64_t heads = c.a.cache.heads, groups = p.blocks * heads * p.parts;
-    EXPECT(groups >= 1 && groups * (p.waves == 8 ? 512 : 256) <= THREADS);
-    if (p.bytes) {
-        // the join: a workgroup of 256 threads to 1024 / dim rows, or (few) to one
-        EXPECT(p.blocks * heads * ((int64_t)1 << p.rows_shift) * 256 <= THREADS);
-        EXPECT(p.o_bytes == (groups << p.rows_shift) * dim * 4 && p.o_bytes % 16 == 0);
-        EXPECT(p.bytes == p.o_bytes + (groups << p.rows_shift) * 8);
+    const int64_t heads = c.a.cache.heads;
+    EXPECT(p.grid >= 1 && p.grid * (p.waves == 8 ? 512 : 256) <= THREADS);
+    EXPECT(p.runs == (p.bytes != 0) && p.runs == (c.runs != 0) && c.window >= 1);
+    if (p.runs) {
+        // units of every length that the pages hold fit an int, block numbers the kernels' arrays
+        const int64_t slots = ((int64_t)c.a.batch.max_pages << c.a.cache.page_shift);
+        const int64_t most = slots < (int64_t)c.window + c.sinks + 300 ? slots : (int64_t)c.window + c.sinks + 300;
+        EXPECT(p.blocks <= CHUNK_RUN_BLOCKS && p.grid <= 512);
+        EXPECT(p.blocks * heads * (most / CHUNK_UNIT) <= INT32_MAX);
+        EXPECT(p.blocks * heads * 16 * 256 <= THREADS);
+        EXPECT(p.o_bytes == (2 * p.grid << p.rows_shift) * dim * 4 && p.ml_end == p.o_bytes + (2 * p.grid << p.rows_shift) * 8);
+        EXPECT(p.bytes == p.ml_end + (p.blocks + 1) * 4 && p.ml_end % 16 == 0);
+    } else {
+        EXPECT(p.grid == p.blocks * heads);
     }
-    EXPECT((p.bytes != 0) == (p.parts > 1) && p.part_units >= 1 && c.window >= 1);
     EXPECT(p.rows_shift == (p.waves == 0 ? 4 : p.waves == 4 ? 7 : dim == 256 ? 7 : 8));
     EXPECT(!(p.waves == 4 && dim == 256));
     return hipSuccess;
@@ -56,7 +62,7 @@ hipError_t launch_chunk(const ChunkArgs &c, const ChunkPlan &p, int, int dim, in
 hipError_t launch_lora(const LoraArgs &a, int, hipStream_t) {
     ++loras;
     EXPECT(a.M > 0 && a.N > 0 && a.N <= INT32_MAX - 256);
-    EXPECT((a.M + 63) / 64 <= 65535);
+    EXPECT((a.M + 31) / 32 <= 65535);
     EXPECT(((int64_t)a.N + 127) / 128 * 256 <= THREADS);
     EXPECT(((int64_t)a.M + 15) / 16 * 512 <= THREADS);
     return hipSuccess;
@@ -105,7 +111,7 @@ int main() {
                             if (n > INT32_MAX / 2) continue;
                             kq_cache c = {P, P, 100, KQ_T_F16, heads, dim, 64, 1.f, 1.f};
                             for (int64_t seqs : {n, n / tokens + 1, (int64_t)1}) {
-                                kq_batch s = {I, I, I, seqs, n, 10};
+                                kq_batch s = {I, I, I, seqs, n, dim == 64 ? 10 : 1 << 20};
                                 const int rc = kq_attn_chunk(&c, &s, KQ_T_F16, P, heads * group, 0, 0, 1.f, tokens, 4096, KQ_T_F32, P, P, SIZE_MAX, nullptr);
                                 EXPECT(rc == KQ_OK || rc == KQ_ERR_UNSUPPORTED);
                             }
@@ -120,7 +126,8 @@ int main() {
         for (int b = 0; b < seqs; ++b) at.push_back(at.back() + gen() % (most + 1));
         if (!at.back()) continue;
         kq_cache c = {P, P, 100, KQ_T_F16, 1, 128, 64, 1.f, 1.f};
-        const kq::ChunkPlan p = kq::chunk_plan(c, seqs, at.back(), group, 0, 0, 1 + gen() % 600, 1 + gen() % 5000);
+        kq_batch s = {I, I, I, seqs, at.back(), 100};
+        const kq::ChunkPlan p = kq::chunk_plan(c, s, group, 0, 0, 1 + gen() % 600, 1 + gen() % 5000);
         int64_t next = 0;
         for (int b = 0; b < seqs; ++b) {
             const int64_t first = (at[b] * group >> p.rows_shift) + b;

@@ -492,7 +492,7 @@ def check_lora(kq, M, N, K, rank, n, ids, t=BF16, act=1, scaled=True, based=True
 @pytest.mark.parametrize("t", [BF16, F16], ids=str)
 @pytest.mark.parametrize("act", [1, 2], ids=["q8_k", "q8_128"])
 @pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
-@pytest.mark.parametrize("M", [1, 5, 65, 200])
+@pytest.mark.parametrize("M", [1, 5, 65, 200, 601])
 def test_lora_types_and_ranks(kq, t, act, rank, M):
     n = 5
     ids = np.random.default_rng(M).integers(-1, n + 1, M)   # some outside at either end
@@ -504,16 +504,17 @@ def test_lora_types_and_ranks(kq, t, act, rank, M):
 def test_lora_sizes(kq, N, M):
     """Rows sorted by request and not; odd numbers of rows and columns."""
     check_lora(kq, M, N, 256, 16, 3, np.arange(M) * 3 // M)
-    check_lora(kq, M, N, 256, 32, 7, np.arange(M) * 5 % 8 - 1)
+    check_lora(kq, M, N, 256, 64, 3, np.arange(M) * 3 // M)
+    check_lora(kq, M, N, 256, 128, 7, np.arange(M) * 5 % 8 - 1)
 
 
 @pytest.mark.parametrize("act,K", [(1, 256), (1, 512), (1, 2304), (1, 14336), (2, 128), (2, 640), (2, 5120)])
-@pytest.mark.parametrize("M", [2, 70])
+@pytest.mark.parametrize("M", [2, 257])
 def test_lora_depths(kq, act, K, M):
     check_lora(kq, M, 100, K, 16, 2, np.arange(M) % 2, F16, act)
 
 
-@pytest.mark.parametrize("M", [4, 100])
+@pytest.mark.parametrize("M", [4, 515])
 def test_lora_without(kq, M):
     for scaled in (False, True):
         for based in (False, True):
@@ -524,7 +525,7 @@ def test_lora_without(kq, M):
 
 
 def test_lora_each_row_its_own(kq):
-    for M in (64, 200):
+    for M in (64, 300):
         check_lora(kq, M, 300, 512, 16, M, np.random.default_rng(1).permutation(M))
 
 
@@ -538,7 +539,7 @@ def test_lora_no_adapters(kq):
     assert (kq.lora(a, *empty, ids) == 0).all()
 
 
-@pytest.mark.parametrize("M", [6, 90])
+@pytest.mark.parametrize("M", [6, 290])
 def test_lora_odd_adapters_and_rows_stay_apart(kq, M):
     """Infinities and NaN in an adapter nobody else uses, and rows whose activations are NaN."""
     N, K, n = 150, 512, 4
@@ -561,7 +562,7 @@ def test_lora_odd_adapters_and_rows_stay_apart(kq, M):
     assert torch.isnan(got[ids == 2][:, 7]).all() and torch.isfinite(got[(ids == 2) & (torch.arange(M) != M - 1)][:, 8:]).all()
 
 
-@pytest.mark.parametrize("M", [7, 150])
+@pytest.mark.parametrize("M", [7, 300])
 def test_lora_bits_streams_and_graphs(kq, M):
     N, K, n = 500, 1024, 3
     rng = np.random.default_rng(5)
@@ -612,7 +613,7 @@ def test_counters(kq):
     kq.kq_layer_count_reset()
     check_norm(kq, 2, 256)
     check_lora(kq, 2, 32, 256, 8, 1, [0, 0])
-    check_lora(kq, 70, 32, 256, 8, 1, [0] * 70)
+    check_lora(kq, 700, 32, 256, 8, 1, [0] * 700)
     check_chunk(kq, Step(1, [5], [1], 16), 2, 1, 64, BF16, BF16, types=(BF16,))
     check_chunk(kq, Step(1, [5], [30], 16), 2, 1, 64, BF16, BF16, types=(BF16,))
     counts = kq.layer_counts()

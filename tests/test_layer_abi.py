@@ -93,17 +93,17 @@ def test_chunk_size_limits(kq):  # noqa: F811
 
 
 def test_chunk_workspace(kq):  # noqa: F811
-    """None where blocks fill the chip; bounded however long the sequences; 0 for bad arguments."""
+    """None where every block is a workgroup's; bounded however long the sequences; 0 for bad arguments."""
     c = cache(kq, heads=8)
     size = lambda n, t, q, w, m: kq.kq_attn_chunk_workspace(c, batch(kq, n_seqs=n, n_tokens=n * t), q, w, 4, t, m)  # noqa: E731
-    assert size(64, 1, 32, 0, 1 << 20) == size(16, 4096, 32, 0, 1 << 20) == 0
+    assert size(200, 1, 32, 0, 500) == size(1, 4096, 32, 0, 4096) == size(1, 1, 32, 0, 64) == size(1, 1, 32, 30, 1 << 20) == 0
     assert size(1, 1, 32, 0, 100000) > size(1, 1, 32, 0, 500) > 0
     for n in (1, 5, 64):
         for t in (1, 7, 64, 1000):
             for m in (1, 128, 1000, 131072, 1 << 30):
                 for w in (0, 1, 5000):
-                    # two grids' worth of blocks of 256 rows at most
-                    assert size(n, t, 16, w, m) <= 2 * 512 * 256 * (128 * 4 + 8)
+                    # two slots to each of 256 workgroups of 256 rows (or 512 of 128) and the blocks' units
+                    assert size(n, t, 16, w, m) <= 2 * 256 * 256 * (128 * 4 + 8) + 2049 * 4
     for bad in (size(-1, 1, 8, 0, 10), size(1, 1, 9, 0, 10), size(1, 1, 8, 0, 0), size(1, 1, 8, -1, 10), size(1, 0, 8, 0, 10)):
         assert bad == 0
 
@@ -115,7 +115,7 @@ def test_chunk_workspace(kq):  # noqa: F811
     (dict(K=-256), "KQ_ERR_SHAPE"), (dict(K=384), "KQ_ERR_SHAPE"), (dict(N=1 << 31, ldo=1 << 31, ldb=1 << 31), "KQ_ERR_SHAPE"),
     (dict(n=1 << 30, N=1 << 20, ldo=1 << 20, ldb=1 << 20), "KQ_ERR_SHAPE"),
     (dict(ldo=99), "KQ_ERR_SHAPE"), (dict(ldb=99), "KQ_ERR_SHAPE"), (dict(ldo=1 << 41), "KQ_ERR_SHAPE"),
-    (dict(base=A, out=A, ldb=100, ldo=101), "KQ_ERR_SHAPE"), (dict(M=65535 * 64 + 1), "KQ_ERR_UNSUPPORTED"),
+    (dict(base=A, out=A, ldb=100, ldo=101), "KQ_ERR_SHAPE"), (dict(M=65535 * 32 + 1), "KQ_ERR_UNSUPPORTED"),
     (dict(n=1, N=(1 << 31) - 256, ldo=1 << 31, ldb=1 << 31), "KQ_ERR_UNSUPPORTED"),
     (dict(A=None), "KQ_ERR_NULL"), (dict(B=None), "KQ_ERR_NULL"), (dict(a_q8=None), "KQ_ERR_NULL"), (dict(ids=None), "KQ_ERR_NULL"),
     (dict(out=None), "KQ_ERR_NULL"), (dict(ws=None), "KQ_ERR_NULL"), (dict(A=A + 8), "KQ_ERR_ALIGN"), (dict(B=A + 2), "KQ_ERR_ALIGN"),
