@@ -29,12 +29,13 @@ namespace kq {
 
 namespace {
 
-// A block's share of the work: units [from, to) of CHUNK_UNIT slots, first those of the
-// sinks, then those of the window.
+// A block's share of the work: units [from, to), first those of the sinks, then those of
+// the window.
 struct Block {
     int b, h, rb;
     Seq sq;
     int pos0, pos1;  // slots of its first and last token
+    int shift;       // a unit is 1 << shift slots
     int sink_units, window_unit, units;
     int from, to;
     bool whole;
@@ -93,9 +94,11 @@ __device__ __forceinline__ bool block_of(const ChunkArgs &c, int b, int j, Block
     k.pos1 = q.len + (int)((uint32_t)(row1 - 1) / (uint32_t)c.a.group);
     const int end = min(k.pos1 + 1, q.total);
     const int begin = min(max(k.pos0 - (c.window - 1), 0), end);
-    k.window_unit = begin >> CHUNK_UNIT_SHIFT;
-    const int end_unit = (int)(((int64_t)end + CHUNK_UNIT - 1) >> CHUNK_UNIT_SHIFT);
-    const int sinks = (min(c.sinks, end) + CHUNK_UNIT - 1) >> CHUNK_UNIT_SHIFT;
+    k.shift = rows <= 16 ? c.few_shift : CHUNK_UNIT_SHIFT;
+    const int64_t up = (1 << k.shift) - 1;
+    k.window_unit = begin >> k.shift;
+    const int end_unit = (int)((end + up) >> k.shift);
+    const int sinks = (int)((min(c.sinks, end) + up) >> k.shift);
     k.sink_units = min(sinks, k.window_unit);
     k.units = k.sink_units + max(end_unit - k.window_unit, 1);
     return true;
@@ -207,7 +210,6 @@ struct Work {
 // The tiles of a part, counted from the block's first, and who sees what of them.
 template <int KEYS>
 struct Tiles {
-    static constexpr int F = CHUNK_UNIT / KEYS;
     const ChunkArgs &c;
     int sink_tiles, start;  // tiles of the sinks; the slot of the first tile after them
     int from, to;
@@ -228,11 +230,12 @@ struct Tiles {
         return e;
     }
     __device__ __forceinline__ Tiles(const ChunkArgs &c_, const Block &k) : c(c_) {
-        sink_tiles = k.sink_units * F;
-        start = k.window_unit << CHUNK_UNIT_SHIFT;
-        from = k.from * F;
-        to = k.to * F;
-        if (F > 1 && to > from && key(to - 1) > k.pos1) --to;  // half a unit past the end
+        const int f = (1 << k.shift) / KEYS;
+        sink_tiles = k.sink_units * f;
+        start = k.window_unit << k.shift;
+        from = k.from * f;
+        to = k.to * f;
+        while (to - 1 > from && key(to - 1) > k.pos1) --to;  // (tiles of the last unit that lie past the end)
         block = edges(k.pos0, k.pos1);
     }
     __device__ __forceinline__ int key(int t) const { return t < sink_tiles ? t * KEYS : start + (t - sink_tiles) * KEYS; }
@@ -465,80 +468,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const 
     }
 }
 
-// Up to 128 rows: 4 waves of 32 share the tiles, two in LDS.
-template <class E, bool F8, int D>
-__global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
-    constexpr int RW = 32, KEYS = D == 128 ? 32 : 64;
-    typedef Tile<E, F8, D, KEYS, RW, 256, false> TL;
-    typedef Rows<E, F8, D, KEYS, RW> RS;
-
-    __shared__ __align__(1024) char lds[2 * TL::BYTES];
-    __shared__ int odd;  // whether masked tiles staged so far have infinite or NaN values
-    __shared__ int before[CHUNK_RUN_BLOCKS + 1], waves[4];
-
-    Work<256> work(c, before, waves);
-    Block k;
-    int64_t slot;
-    const AttnArgs &a = c.a;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    TL tl(a, threadIdx.x);
-    if (threadIdx.x == 0) odd = 0;
-    while (work.next(k, slot)) {
-    const Tiles<KEYS> tiles(c, k);
-    RS rs(a, tiles, threadIdx.x);
-    tl.aim(k.b, k.h, k.sq);
-    const int first = tiles.from;
-    typename TL::Place next = tl.find(tiles.key(first));
-    tl.load_k(next);
-    tl.load_v(next);
-    next = tl.find(tiles.key(first + 1));
-    const int row0 = (k.rb << c.rows_shift) + wave * RW;
-    const bool rows = row0 < k.sq.T * a.group;  // (a wave without rows only stages)
-    rs.begin(k, row0);
-    __syncthreads();
-    tl.store_k(lds, 0);
-    if (tl.store_v(lds, TL::K_BYTES, tiles.key(first), tiles.block.at(first))) odd = 1;
-    tl.load_k(next);
-    tl.load_v(next);
-    next = tl.find(tiles.key(first + 2));
-    int buf = 0;
-    for (int t = first; t < tiles.to; ++t) {
-        __syncthreads();
-        if (rows) rs.tile(lds, buf, t, tiles.key(t));
-        buf = TL::BYTES - buf;
-        if (t + 1 < tiles.to) {
-            const int key1 = tiles.key(t + 1);
-            tl.store_k(lds, buf);
-            if (tl.store_v(lds, buf + TL::K_BYTES, key1, tiles.block.at(t + 1))) odd = 1;
-            tl.load_k(next);
-            tl.load_v(next);
-            next = tl.find(tiles.key(t + 3));
-        }
-    }
-    __syncthreads();
-    if (odd) rs.odd_values(k, tiles.from, 1);
-    rs.put(k, slot, wave);
-    }
-}
-
-// A wave's share of the copies of tiles into LDS (8 waves share them).  A copy fills 1 KB
+// A wave's share of the copies of tiles into LDS.  A copy fills 1 KB
 // of LDS in the order of the lanes, so the places of Tile::k_pos and v_pos are met by
 // what each lane reads: the piece that belongs where it writes.  A wave's keys lie in one
 // page, and so do the values of a tile where a page covers it: their addresses are
 // scalar, looked up a turn before they are needed, and a lane adds an offset that never
 // changes.
 // SMALL: pages smaller than a tile.
-template <class E, bool F8, int D, int KEYS, int RW, bool SMALL>
+template <class E, bool F8, int D, int KEYS, int RW, int WAVES, bool SMALL>
 struct Stage {
     typedef Tile<E, F8, D, KEYS, RW, 64, true> PL;  // (for the places in LDS alone)
     typedef Frag<E, F8> FR;
     static constexpr int ES = FR::BYTES, KB = PL::KB, VB = PL::VB;
     static constexpr int COPIES = KEYS * KB / 1024;             // of a tile's keys, and of its values
-    static constexpr int N = COPIES >= 8 ? COPIES / 8 : 1;      // a wave's of each
-    static constexpr bool HALF = COPIES < 8;                    // the first 4 waves: keys, the others: values
-    static constexpr int TURN = HALF ? 1 : 2 * N;               // a wave's of a tile
+    static constexpr int N = COPIES / WAVES;                    // a wave's of each
+    static constexpr int TURN = 2 * N;                          // a wave's of a tile
     static constexpr int K_ROWS = N * 1024 / KB;                // keys of a wave, in one run of 16
-    static_assert(16 % K_ROWS == 0 && (HALF ? COPIES == 4 : COPIES % 8 == 0), "a wave's keys share a page");
+    static_assert(16 % K_ROWS == 0 && COPIES % WAVES == 0, "a wave's keys share a page");
 
     const_ints pages;     // the sequence's row of the table
     const char *k_head, *v_head;  // the head's place in page 0
@@ -569,10 +515,8 @@ struct Stage {
             v_off[i] = ((uint32_t)d << shift) * ES + (SMALL ? 0 : v_piece * 16);
         }
     }
-    __device__ __forceinline__ int copy(int i) const { return HALF ? wave & 3 : N * wave + i; }
+    __device__ __forceinline__ int copy(int i) const { return N * wave + i; }
     __device__ __forceinline__ int k_row() const { return copy(0) * 1024 / KB; }
-    __device__ __forceinline__ bool has_k() const { return !HALF || wave < 4; }
-    __device__ __forceinline__ bool has_v() const { return !HALF || wave >= 4; }
 
     // A slot past the sequence's end is taken to lie in its last run (masked later).
     __device__ __forceinline__ int k_slot(int key0) const { return min(key0 + k_row(), (total - 1) & -K_ROWS); }
@@ -583,39 +527,35 @@ struct Stage {
     __device__ __forceinline__ uint64_t page_at(int e) const { return (uint64_t)(uint32_t)min(max(e, 0), last_page) * page_bytes; }
     // The tile's page entries.
     __device__ __forceinline__ int k_entry(int key0) const { return pages[k_slot(key0) >> shift]; }
-    struct Pages {
-        int e[SMALL ? KEYS / 16 : 1];  // of its runs of 16 slots, or one for all
-    };
+    typedef int Pages __attribute__((ext_vector_type(SMALL ? KEYS / 16 : 1)));  // of its runs of 16 slots, or one for all
     __device__ __forceinline__ Pages v_entry(int key0) const {
         Pages p;
         if constexpr (SMALL) {
 #pragma unroll
-            for (int r = 0; r < KEYS / 16; ++r) p.e[r] = pages[min(key0 + 16 * r, (total - 1) & ~15) >> shift];
+            for (int r = 0; r < KEYS / 16; ++r) p[r] = pages[min(key0 + 16 * r, (total - 1) & ~15) >> shift];
         } else {
-            p.e[0] = pages[v_slot(key0) >> shift];
+            p[0] = pages[v_slot(key0) >> shift];
         }
         return p;
     }
     __device__ __forceinline__ void copy_k(int buf, int key0, int e) const {
-        if (!has_k()) return;
         const char *p = k_head + page_at(e) + (uint32_t)((k_slot(key0) & ((1 << shift) - 1)) * KB);
 #pragma unroll
         for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, k_off[i]);
     }
-    __device__ __forceinline__ void copy_v(int buf, int key0, const Pages &e) const {
-        if (!has_v()) return;
+    __device__ __forceinline__ void copy_v(int buf, int key0, Pages e) const {
         const int mask = (1 << shift) - 1;
         if constexpr (SMALL) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int run = v_key[i] >> 4;
-                int mine = e.e[0];
+                int mine = e[0];
 #pragma unroll
-                for (int r = 1; r < KEYS / 16; ++r) mine = run == r ? e.e[r] : mine;
+                for (int r = 1; r < KEYS / 16; ++r) mine = run == r ? e[r] : mine;
                 copy16(lds + buf + copy(i) * 1024, v_head + page_at(mine) + (v_off[i] + (uint32_t)((lane_slot(key0, i) & mask) * ES)));
             }
         } else {
-            const char *p = v_head + page_at(e.e[0]) + (uint32_t)((v_slot(key0) & mask) * ES);
+            const char *p = v_head + page_at(e[0]) + (uint32_t)((v_slot(key0) & mask) * ES);
 #pragma unroll
             for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, v_off[i]);
         }
@@ -625,7 +565,6 @@ struct Stage {
     // whether this lane met any of those.
     __device__ __forceinline__ bool clean_v(char *at, int buf, int key0) const {
         bool found = false;
-        if (!has_v()) return false;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             v4u *p = reinterpret_cast<v4u *>(at + buf + copy(i) * 1024 + lane * 16);
@@ -650,6 +589,69 @@ struct Stage {
     }
 };
 
+// Up to 128 rows, and all of heads of 64: 4 waves of 32 rows share the tiles, three in LDS: one
+// in use and two on their way.  Copies of tile i + 2 start when all waves are done with
+// tile i - 1.
+template <class E, bool F8, int D, bool SMALL>
+__global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
+    constexpr int RW = 32, KEYS = D == 128 ? 32 : 64;  // (64 at dim 128 would not fit the registers)
+    typedef Stage<E, F8, D, KEYS, RW, 4, SMALL> ST;
+    typedef Rows<E, F8, D, KEYS, RW> RS;
+    constexpr int BYTES = RS::AT::TL::BYTES, K_BYTES = RS::AT::TL::K_BYTES;
+
+    __shared__ __align__(1024) char lds[3 * BYTES];
+    __shared__ int odd;  // whether masked tiles copied so far have infinite or NaN values
+    __shared__ int before[CHUNK_RUN_BLOCKS + 1], waves[4];
+
+    Work<256> work(c, before, waves);
+    Block k;
+    int64_t slot;
+    const AttnArgs &a = c.a;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (threadIdx.x == 0) odd = 0;
+    while (work.next(k, slot)) {
+        __syncthreads();  // the piece before has been read
+        const Tiles<KEYS> ts(c, k);
+        const unsigned thread = this_thread();
+        const ST st(a, k, lds, wave, thread & 63);
+        RS rs(a, ts, thread);
+        const int first = ts.from, n = ts.to - ts.from;
+        int key0 = ts.key(first), key1 = ts.key(first + 1), key2 = ts.key(first + 2);
+        st.copy_v(K_BYTES, key0, st.v_entry(key0));
+        st.copy_k(0, key0, st.k_entry(key0));
+        st.copy_v(BYTES + K_BYTES, key1, st.v_entry(key1));
+        st.copy_k(BYTES, key1, st.k_entry(key1));
+        int ke = st.k_entry(key2);  // of the tile to be copied next
+        typename ST::Pages ve = st.v_entry(key2);
+        const int row0 = (k.rb << c.rows_shift) + wave * RW;
+        const bool rows = row0 < k.sq.T * a.group;  // (a wave without rows only copies)
+        rs.begin(k, row0);
+        int buf = 0;
+        for (int i = 0; i < n; ++i) {
+            const int t = first + i;
+            // (q's loads and a lookup may be among the newest: then this waits for less than it could)
+            arrived<ST::TURN>();
+            if (ts.block.at(t) && st.clean_v(lds, buf + K_BYTES, key0)) odd = 1;
+            __syncthreads();
+            const int next = buf >= BYTES ? buf - BYTES : 2 * BYTES;  // tile i + 2
+            st.copy_v(next + K_BYTES, key2, ve);
+            st.copy_k(next, key2, ke);
+            const int key3 = ts.key(t + 3);
+            ke = st.k_entry(key3);
+            ve = st.v_entry(key3);
+            if (rows) rs.tile(lds, buf, t, key0);
+            key0 = key1;
+            key1 = key2;
+            key2 = key3;
+            buf = buf == 2 * BYTES ? 0 : buf + BYTES;
+        }
+        arrived<0>();  // (copies of tiles past the last)
+        __syncthreads();
+        if (odd) rs.odd_values(k, ts.from, 1);
+        rs.put(k, slot, wave);
+    }
+}
+
 // More rows: 8 waves, two to a SIMD, share the tiles, and the second four run half a turn
 // behind the first.  A turn has a half of matrix products (the values of the tile before,
 // the scores of this one) and a half of vector work (softmax, copies), so that one wave
@@ -667,7 +669,7 @@ struct Stage {
 template <class E, bool F8, int D, bool SMALL>
 __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
     constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
-    typedef Stage<E, F8, D, KEYS, RW, SMALL> ST;
+    typedef Stage<E, F8, D, KEYS, RW, 8, SMALL> ST;
     typedef Rows<E, F8, D, KEYS, RW> RS;
     typedef typename RS::AT AT;
     constexpr int BYTES = AT::TL::BYTES, K_BYTES = AT::TL::K_BYTES, FEW_BYTES = Few<E, F8, D>::WAVE_BYTES;
@@ -773,15 +775,16 @@ __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
     }
 }
 
-// Where the parts of a cut block lie: workgroups w0 .. w1 have one each.
+// Where the parts of block j of head h lie: workgroups w0 .. w1 have one each.
 struct Parts {
     int from, w0, w1;
     Runs runs;
-    __device__ __forceinline__ Parts(const ChunkArgs &c, int j, int h, int units)
-        : runs(c.a.ws_seq[c.blocks] * c.a.cache.heads, min(c.a.grid, c.a.ws_seq[c.blocks] * c.a.cache.heads)) {
-        from = h * c.a.ws_seq[c.blocks] + c.a.ws_seq[j];
+    __device__ __forceinline__ Parts(const ChunkArgs &c, int j, int h, int all)
+        : runs(all * c.a.cache.heads, min(c.a.grid, all * c.a.cache.heads)) {
+        from = h * all + c.a.ws_seq[j];
+        const int to = h * all + c.a.ws_seq[j + 1];  // (blocks' units follow each other)
         w0 = runs.holder(from);
-        w1 = runs.holder(from + units - 1);
+        w1 = runs.holder(max(to - 1, from));
     }
     // a workgroup's first piece lies in its first slot
     __device__ __forceinline__ int64_t slot(int w) const { return 2 * (int64_t)w + (runs.begin(w) < from); }
@@ -796,23 +799,18 @@ __device__ __forceinline__ void join(v4f (&o)[N], float &m, float &l, v2f ml, co
 #pragma unroll
     for (int q = 0; q < N; ++q) o[q] = o[q] * f + po[q] * pf;
 }
-__device__ __forceinline__ int64_t out_row(const ChunkArgs &c, const Block &k, int in_seq) {
-    const int G = c.a.group, tok = in_seq / G;
-    return (int64_t)(k.sq.first + tok) * ((int64_t)c.a.cache.heads * G) + k.h * G + (in_seq - tok * G);
-}
-// A row of up to 16 that few_rows left: D / 4 threads to a row, `sets` sets of them, which
-// share out its parts.
-template <class E, int D, int THREADS>
-__device__ __forceinline__ void join_few(const ChunkArgs &c, const Block &k, const Parts &parts, int row, int sets, v4f *so, v2f *sml) {
+// A row of a cut block that few_rows left: D / 4 threads to a row, `sets` sets of them, which
+// share out its parts.  Threads of a set without a row (used) only meet the barrier.
+template <class E, int D>
+__device__ __forceinline__ void join_few(const ChunkArgs &c, const Parts &parts, int row_in_block, int64_t out_row, bool used,
+                                         int sets, v4f *so, v2f *sml) {
     constexpr int TPP = D / 4;
     const int lane = threadIdx.x % TPP, set = threadIdx.x / TPP, sub = set % sets;
-    const int in_seq = (k.rb << c.rows_shift) + row;
-    const bool used = row < 16 && in_seq < k.sq.T * c.a.group;
     float m = M_START, l = 0.f;
     v4f o[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
     if (used) {
         for (int w = parts.w0 + sub; w <= parts.w1; w += sets) {
-            const int64_t r = (parts.slot(w) << c.rows_shift) + row;
+            const int64_t r = (parts.slot(w) << c.rows_shift) + row_in_block;
             const v4f po[1] = {*reinterpret_cast<const v4f *>(c.a.ws_o + r * D + 4 * lane)};
             join<1>(o, m, l, *reinterpret_cast<const v2f *>(c.a.ws_ml + 2 * r), po);
         }
@@ -827,41 +825,51 @@ __device__ __forceinline__ void join_few(const ChunkArgs &c, const Block &k, con
             join<1>(o, m, l, sml[set + s], po);
         }
     }
-    if (!used) return;
-    put4<E>(c.a, true, o[0] * (l == 0.f ? 0.f : c.a.v_scale / l), out_row(c, k, in_seq) * D + 4 * lane, 0);
+    if (used) put4<E>(c.a, true, o[0] * (l == 0.f ? 0.f : c.a.v_scale / l), out_row * D + 4 * lane, 0);
 }
 // out = sum over the parts of a cut block, each weighted by exp2(its maximum - the
-// largest).  Blocks of 16 rows: a workgroup to a row.
+// largest).  Blocks of 16 rows: a workgroup to `rows` heads of a token (a divisor of the
+// group, as many sets of threads to each as there are).
 template <class E, int D>
-__global__ __launch_bounds__(256) void chunk_join_few_kernel(const ChunkArgs c) {
+__global__ __launch_bounds__(256) void chunk_join_few_kernel(const ChunkArgs c, int rows) {
+    constexpr int SETS = 1024 / D;
     __shared__ v4f so[256];
-    __shared__ v2f sml[1024 / D];
-    const unsigned jh = blockIdx.x >> 4;
-    const int j = (int)(jh / (unsigned)c.a.cache.heads);
-    Block k;
-    k.h = (int)(jh - (unsigned)j * c.a.cache.heads);
-    if (!block_of(c, block_seq(c, j), j, k)) return;
-    const Parts parts(c, j, k.h, k.units);
-    if (parts.w0 == parts.w1) return;  // finished there
-    join_few<E, D, 256>(c, k, parts, blockIdx.x & 15, 1024 / D, so, sml);
+    __shared__ v2f sml[SETS];
+    const int G = c.a.group, q_heads = c.a.cache.heads * G;
+    const int tok = blockIdx.x, head0 = blockIdx.y * rows, h = head0 / G;
+    const int b = __builtin_amdgcn_readfirstlane(batch_seq(c.a.batch, tok));
+    int first, count;
+    batch_rows(c.a.batch, b, first, count);
+    const int i = tok - first;
+    if (i < 0 || i >= count) return;  // (a row of no sequence)
+    const int all = c.a.ws_seq[c.blocks];
+    const int sets = SETS / rows, set = threadIdx.x / (D / 4);
+    const int row = i * G + head0 % G + min(set / sets, rows - 1);
+    const int j = (int)first_block(c, b) + (row >> c.rows_shift);
+    const Parts parts(c, j, h, all);
+    const bool used = set / sets < rows && parts.w0 != parts.w1;  // (one workgroup: finished there)
+    join_few<E, D>(c, parts, row & ((1 << c.rows_shift) - 1), (int64_t)tok * q_heads + head0 + set / sets, used, sets, so, sml);
 }
 // More rows: a workgroup to a block, a wave to the rows that one wave left.
 template <class E, int D, int RW, int WAVES, bool FEW>
 __global__ __launch_bounds__(WAVES * 64) void chunk_join_kernel(const ChunkArgs c) {
     constexpr int QUADS = RW * D / 256;
-    const int j = (int)(blockIdx.x / (unsigned)c.a.cache.heads);
-    Block k;
-    k.h = (int)(blockIdx.x - (unsigned)j * c.a.cache.heads);
-    if (!block_of(c, block_seq(c, j), j, k)) return;
-    const Parts parts(c, j, k.h, k.units);
-    if (parts.w0 == parts.w1) return;  // finished there
-    if (FEW && k.sq.T * c.a.group <= 16) {
+    const int G = c.a.group, j = (int)(blockIdx.x / (unsigned)c.a.cache.heads), h = (int)(blockIdx.x - (unsigned)j * c.a.cache.heads);
+    const Parts parts(c, j, h, max(c.a.ws_seq[c.blocks], 1));
+    if (parts.w0 == parts.w1) return;  // finished there, or no block
+    const int b = block_seq(c, j);
+    int first, count;
+    batch_rows(c.a.batch, b, first, count);
+    const int64_t rows = (int64_t)count * G;
+    const int row0 = (j - (int)first_block(c, b)) << c.rows_shift;
+    // the output's row of the sequence's row r
+    const auto out_row = [&](int r) { return (int64_t)(first + r / G) * ((int64_t)c.a.cache.heads * G) + h * G + r % G; };
+    if (FEW && rows <= 16) {
         constexpr int TPP = D / 4, SETS = WAVES * 64 / TPP;
-        for (int row = threadIdx.x / TPP; row < 16; row += SETS) join_few<E, D, WAVES * 64>(c, k, parts, row, 1, nullptr, nullptr);
+        for (int r = threadIdx.x / TPP; r < rows; r += SETS) join_few<E, D>(c, parts, r, out_row(r), true, 1, nullptr, nullptr);
         return;
     }
     const int lane = threadIdx.x & 63, n = lane & (RW - 1), g = lane / RW, row = (threadIdx.x >> 6) * RW + n;
-    const int in_seq = (k.rb << c.rows_shift) + row;
     float m = M_START, l = 0.f;
     v4f o[QUADS];
 #pragma unroll
@@ -874,9 +882,9 @@ __global__ __launch_bounds__(WAVES * 64) void chunk_join_kernel(const ChunkArgs 
         for (int q = 0; q < QUADS; ++q) po[q] = from[q * 64];
         join<QUADS>(o, m, l, *reinterpret_cast<const v2f *>(c.a.ws_ml + 2 * r), po);
     }
-    if (in_seq >= k.sq.T * c.a.group) return;
+    if (row0 + row >= rows) return;
     const float norm = l == 0.f ? 0.f : c.a.v_scale / l;
-    const int64_t to = out_row(c, k, in_seq) * D;
+    const int64_t to = out_row(row0 + row) * D;
     constexpr int NR = RW * RW / 64;
 #pragma unroll
     for (int q = 0; q < QUADS; ++q) {
@@ -886,25 +894,47 @@ __global__ __launch_bounds__(WAVES * 64) void chunk_join_kernel(const ChunkArgs 
 }
 
 template <class E, bool F8, int D>
-hipError_t launch_dim(const ChunkArgs &c, const ChunkPlan &p, hipStream_t stream) {
+hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t stream) {
+    ChunkArgs c = args;
+    // among many rows, few take half as long for their keys: 128 slots of one row of 4 heads are
+    // read while 64 of 256 rows are multiplied
+    c.few_shift = p.waves == 8 && FEW_IN_WIDE<E, F8, D> ? CHUNK_UNIT_SHIFT + 1 : CHUNK_UNIT_SHIFT;
     const dim3 grid((unsigned)p.grid);
-    if (p.waves == 0)
-        hipLaunchKernelGGL((chunk_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
-    else if (p.waves == 8 && (1 << c.a.cache.page_shift) < (D == 256 ? 32 : 64))
-        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, true>), grid, dim3(512), 0, stream, c);
-    else if (p.waves == 8)
-        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, false>), grid, dim3(512), 0, stream, c);
-    else if constexpr (D < 256)
-        hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.runs) return e;
+    const int page = 1 << c.a.cache.page_shift;
     const unsigned blocks = (unsigned)(p.blocks * c.a.cache.heads);
-    if (p.waves == 0)
-        hipLaunchKernelGGL((chunk_join_few_kernel<E, D>), dim3(16 * blocks), dim3(256), 0, stream, c);
-    else if (p.waves == 8)
+    if (p.waves == 0) {
+        hipLaunchKernelGGL((chunk_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || !p.runs) return e;
+        // many rows: the heads of a group together, as far as there are threads, which find their parts once
+        const int heads = c.a.cache.heads * c.a.group;
+        int rows = 1;
+        if ((int64_t)c.a.batch.n_tokens * heads > 2048)
+            while (2 * rows <= 1024 / D && c.a.group % (2 * rows) == 0) rows *= 2;
+        hipLaunchKernelGGL((chunk_join_few_kernel<E, D>), dim3((unsigned)c.a.batch.n_tokens, (unsigned)(heads / rows)), dim3(256), 0, stream, c, rows);
+        return hipGetLastError();
+    }
+    if constexpr (D < 256) {
+        if (p.waves == 4) {
+            if (page < (D == 128 ? 32 : 64))
+                hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D, true>), grid, dim3(256), 0, stream, c);
+            else
+                hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D, false>), grid, dim3(256), 0, stream, c);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess || !p.runs) return e;
+            hipLaunchKernelGGL((chunk_join_kernel<E, D, 32, 4, false>), dim3(blocks), dim3(256), 0, stream, c);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (D > 64) {
+        if (page < (D == 256 ? 32 : 64))
+            hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, true>), grid, dim3(512), 0, stream, c);
+        else
+            hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, false>), grid, dim3(512), 0, stream, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || !p.runs) return e;
         hipLaunchKernelGGL((chunk_join_kernel<E, D, D == 256 ? 16 : 32, 8, FEW_IN_WIDE<E, F8, D> != 0>), dim3(blocks), dim3(512), 0, stream, c);
-    else if constexpr (D < 256)
-        hipLaunchKernelGGL((chunk_join_kernel<E, D, 32, 4, false>), dim3(blocks), dim3(256), 0, stream, c);
+    }
     return hipGetLastError();
 }
 

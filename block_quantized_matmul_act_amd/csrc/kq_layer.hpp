@@ -28,7 +28,7 @@ hipError_t launch_norm_quantize(const NormArgs &a, int bs, int x_type, int r_typ
 // How attention of chunks is shared out: blocks of 1 << rows_shift query rows of a
 // key head, numbered so that a block's sequence can be found from the offsets
 // alone (some numbers stay unused).  A workgroup takes a block, or (runs) `grid`
-// workgroups take equal runs of units of CHUNK_UNIT slots of all the blocks and leave at
+// workgroups take equal runs of units of CHUNK_UNIT slots (or 2) of all the blocks and leave at
 // most two cut blocks each, a slot of the workspace to either.
 constexpr int CHUNK_UNIT_SHIFT = 6, CHUNK_UNIT = 1 << CHUNK_UNIT_SHIFT;
 constexpr int CHUNK_RUN_BLOCKS = 2048;  // block numbers of a key head in a call of runs
@@ -47,6 +47,7 @@ struct ChunkArgs {
     AttnArgs a;
     int window, sinks;  // window: INT32_MAX where there is none
     int rows_shift, blocks, runs;
+    int few_shift;  // units of a block of 16 rows or fewer: 1 << few_shift slots (set by the launcher)
 };
 hipError_t launch_chunk(const ChunkArgs &a, const ChunkPlan &p, int type, int dim, int q_type, hipStream_t stream);
 

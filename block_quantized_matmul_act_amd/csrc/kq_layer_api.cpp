@@ -72,7 +72,7 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
     const int64_t heads = cache.heads, group = q_heads / heads, dim = cache.dim;
     max_tokens = std::min(max_tokens, batch.n_tokens);
     const int64_t rows = max_tokens * group;
-    p.waves = rows <= 16 ? 0 : rows <= 128 && dim < 256 ? 4 : 8;
+    p.waves = rows <= 16 ? 0 : dim == 64 || (rows <= 128 && dim == 128) ? 4 : 8;
     p.rows_shift = p.waves == 0 ? 4 : p.waves == 4 || dim == 256 ? 7 : 8;
     p.blocks = ((batch.n_tokens * group) >> p.rows_shift) + batch.n_seqs;
     // the units of a block whose sequence has `slots` slots, at most
@@ -81,9 +81,11 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
         return (slots + CHUNK_UNIT - 1) / CHUNK_UNIT + 2;
     };
     const int64_t units = units_of(max_len), groups = p.blocks * heads, chip = p.waves == 8 ? 256 : 512;
-    p.runs = units > 4 && (groups < 2 * chip || units >= 256);
-    // (units are counted in int32, whatever the lengths; 16 workgroups of 256 threads or fewer join a block)
-    if (p.blocks > CHUNK_RUN_BLOCKS || groups > MAX_GROUPS / 16 || units_of(batch.max_pages * cache.page) > kMaxInt / groups)
+    // blocks there are, rather than numbers of blocks
+    const int64_t real = std::min(groups, batch.n_seqs * (((rows - 1) >> p.rows_shift) + 1) * heads);
+    p.runs = units > 4 && (p.waves ? real < 2 * chip || units >= 256 : real < chip || units >= 64);
+    // (units are counted in int32, whatever the lengths; 512 threads or fewer join a block, 256 a token)
+    if (p.blocks > CHUNK_RUN_BLOCKS || batch.n_tokens > MAX_GROUPS || groups > MAX_GROUPS / 2 || units_of(batch.max_pages * cache.page) > kMaxInt / groups)
         p.runs = false;
     p.grid = p.runs ? std::min(chip, groups * units / 2) : groups;
     const int64_t slot_rows = p.runs ? 2 * p.grid << p.rows_shift : 0;
