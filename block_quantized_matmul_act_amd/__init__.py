@@ -380,13 +380,18 @@ def act_views(a_q8, act_fmt, M, K):
     buffer.  d is stored block-major ([K/bs][M]); the view is its transpose."""
     import torch
     bs = 256 if act_fmt == KQ_ACT_Q8_K else 128
-    od = kq_act_section_offset(act_fmt, KQ_SEC_D, M, K)
-    qs = a_q8[:M * K].view(torch.int8).view(M, K)
-    d = a_q8[od:od + M * (K // bs) * 4].view(torch.float32).view(K // bs, M).t()
+    section, size, need = lib().kq_act_section_offset, a_q8.numel(), lib().kq_act_bytes(act_fmt, M, K)
+    if size < need:
+        raise ValueError(f"act_views: {size} bytes, {need} needed")
+    if size % 4:  # (a longer buffer: viewed as far as whole words go)
+        a_q8 = a_q8[:size - size % 4]
+    words = a_q8.view(torch.float32)
+    at = words.storage_offset()
+    qs = a_q8.view(torch.int8).as_strided((M, K), (K, 1), 4 * at)
+    d = words.as_strided((M, K // bs), (1, M), at + section(act_fmt, KQ_SEC_D, M, K) // 4)
     bsums = None
     if act_fmt == KQ_ACT_Q8_K:
-        ob = kq_act_section_offset(act_fmt, KQ_SEC_BSUMS, M, K)
-        bsums = a_q8[ob:ob + M * (K // 16) * 2].view(torch.int16).view(M, K // 16)
+        bsums = a_q8.view(torch.int16).as_strided((M, K // 16), (K // 16, 1), 2 * at + section(act_fmt, KQ_SEC_BSUMS, M, K) // 2)
     return qs, d, bsums
 
 

@@ -104,8 +104,9 @@ __device__ __forceinline__ bool block_of(const ChunkArgs &c, int b, int j, Block
     return true;
 }
 
-// The units of all blocks of a key head, added up by the whole workgroup: before[j] (in
-// LDS) is what comes before block j, before[blocks] all.
+// The units of all blocks of a key head, c.begin more to each (what its begin and end
+// take), added up by the whole workgroup: before[j] (in LDS) is what comes before block j,
+// before[blocks] all.
 template <int THREADS>
 __device__ __forceinline__ void add_up(const ChunkArgs &c, int *before, int *waves) {
     int base = 0;
@@ -114,7 +115,7 @@ __device__ __forceinline__ void add_up(const ChunkArgs &c, int *before, int *wav
         const int j = j0 + threadIdx.x;
         Block k;
         k.units = 0;
-        if (j < c.blocks) block_of(c, lane_seq(c, j), j, k);
+        if (j < c.blocks && block_of(c, lane_seq(c, j), j, k)) k.units += c.begin;
         int incl = k.units;
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);  // in rows of 16: from 1, 2, 4, 8 to the left
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
@@ -170,22 +171,24 @@ struct Work {
     }
     // The next piece and, where it is a part, its slot; false at the end.
     __device__ __forceinline__ bool next(Block &k, int64_t &slot) {
-        if (u >= end) return false;
         const int heads = c.a.cache.heads;
-        int j;
         slot = 0;
         if (!c.runs) {
-            const unsigned w = blockIdx.x, back = w / heads;
+            if (u >= end) return false;
             u = end;
-            j = c.blocks - 1 - (int)back;
+            const unsigned w = blockIdx.x, back = w / heads;
+            const int j = c.blocks - 1 - (int)back;
             k.h = (int)(w - back * heads);
             if (!block_of(c, block_seq(c, j), j, k)) return false;
             k.from = 0;
             k.to = k.units;
-        } else {
+            k.whole = true;
+            return true;
+        }
+        while (u < end) {
             k.h = u / all;
             const int x = u - k.h * all;
-            // the last block with before[j] <= x
+            // the last block with before[j] <= x (those without units share their number with it)
             const int lane = __lane_id();
             int lo = 0, n = c.blocks;
             while (n > 1) {
@@ -195,15 +198,18 @@ struct Work {
                 n = min(step, lo + n - from);
                 lo = from;
             }
-            j = __builtin_amdgcn_readfirstlane(lo);
+            const int j = __builtin_amdgcn_readfirstlane(lo);
             block_of(c, block_seq(c, j), j, k);
-            k.from = x - __builtin_amdgcn_readfirstlane(before[j]);
-            k.to = min(k.units, k.from + end - u);
+            // the run's share [x, x + some) of the block's c.begin + units
+            const int in = x - __builtin_amdgcn_readfirstlane(before[j]), some = min(k.units + c.begin - in, end - u);
             slot = 2 * (int64_t)group + (u != begin);
-            u += k.to - k.from;
+            u += some;
+            k.from = max(in - c.begin, 0);
+            k.to = max(in + some - c.begin, 0);
+            k.whole = k.to - k.from == k.units;
+            if (k.to > k.from) return true;
         }
-        k.whole = k.to - k.from == k.units;
-        return true;
+        return false;
     }
 };
 
@@ -783,8 +789,8 @@ struct Parts {
         : runs(all * c.a.cache.heads, min(c.a.grid, all * c.a.cache.heads)) {
         from = h * all + c.a.ws_seq[j];
         const int to = h * all + c.a.ws_seq[j + 1];  // (blocks' units follow each other)
-        w0 = runs.holder(from);
-        w1 = runs.holder(max(to - 1, from));
+        w0 = runs.holder(min(from + c.begin, max(to - 1, 0)));
+        w1 = runs.holder(max(to - 1, 0));
     }
     // a workgroup's first piece lies in its first slot
     __device__ __forceinline__ int64_t slot(int w) const { return 2 * (int64_t)w + (runs.begin(w) < from); }
@@ -896,9 +902,11 @@ __global__ __launch_bounds__(WAVES * 64) void chunk_join_kernel(const ChunkArgs 
 template <class E, bool F8, int D>
 hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t stream) {
     ChunkArgs c = args;
-    // among many rows, few take half as long for their keys: 128 slots of one row of 4 heads are
-    // read while 64 of 256 rows are multiplied
-    c.few_shift = p.waves == 8 && FEW_IN_WIDE<E, F8, D> ? CHUNK_UNIT_SHIFT + 1 : CHUNK_UNIT_SHIFT;
+    // Among many rows, few count by their bytes: 64 KB of keys and values are read about while 64
+    // slots are multiplied by 256 rows (a piece of 512 rows and 23 single tokens over 6000
+    // slots of 8 heads of 128, us: 32 KB 155, 64 KB 124, 128 KB 141; in 8 bits 124, 105, 141).
+    c.few_shift = CHUNK_UNIT_SHIFT;
+    if (p.waves == 8 && FEW_IN_WIDE<E, F8, D>) c.few_shift = D * (F8 ? 1 : 2) == 128 ? 8 : 7;
     const dim3 grid((unsigned)p.grid);
     const int page = 1 << c.a.cache.page_shift;
     const unsigned blocks = (unsigned)(p.blocks * c.a.cache.heads);

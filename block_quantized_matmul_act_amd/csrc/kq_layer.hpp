@@ -31,7 +31,8 @@ hipError_t launch_norm_quantize(const NormArgs &a, int bs, int x_type, int r_typ
 // workgroups take equal runs of units of CHUNK_UNIT slots (or 2) of all the blocks and leave at
 // most two cut blocks each, a slot of the workspace to either.
 constexpr int CHUNK_UNIT_SHIFT = 6, CHUNK_UNIT = 1 << CHUNK_UNIT_SHIFT;
-constexpr int CHUNK_RUN_BLOCKS = 2048;  // block numbers of a key head in a call of runs
+constexpr int CHUNK_BEGIN = 6;  // what the begin and end of a block of many rows take, in units
+constexpr int CHUNK_RUN_BLOCKS = 1024;  // block numbers of a key head in a call of runs (2048 take a workgroup of 4 waves its place)
 struct ChunkPlan {
     int waves;  // 0: the kernel for up to 16 rows
     int rows_shift;
@@ -47,6 +48,7 @@ struct ChunkArgs {
     AttnArgs a;
     int window, sinks;  // window: INT32_MAX where there is none
     int rows_shift, blocks, runs;
+    int begin;      // units that the begin and end of a block count for
     int few_shift;  // units of a block of 16 rows or fewer: 1 << few_shift slots (set by the launcher)
 };
 hipError_t launch_chunk(const ChunkArgs &a, const ChunkPlan &p, int type, int dim, int q_type, hipStream_t stream);

@@ -80,12 +80,33 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
         if (window) slots = std::min(slots, window + sinks + ((int64_t)1 << p.rows_shift) / group + 1);
         return (slots + CHUNK_UNIT - 1) / CHUNK_UNIT + 2;
     };
-    const int64_t units = units_of(max_len), groups = p.blocks * heads, chip = p.waves == 8 ? 256 : 512;
-    // blocks there are, rather than numbers of blocks
-    const int64_t real = std::min(groups, batch.n_seqs * (((rows - 1) >> p.rows_shift) + 1) * heads);
-    p.runs = units > 4 && (p.waves ? real < 2 * chip || units >= 256 : real < chip || units >= 64);
+    const int64_t units = units_of(max_len), groups = p.blocks * heads;
+    const int64_t chip = p.waves == 8 ? 256 : p.waves == 4 && dim == 64 ? 768 : 512;  // places for workgroups
+    // Whole blocks or runs?  Few rows: runs where blocks are fewer than places for them on the
+    // chip, or long (their lengths then differ by much).  More: runs where some sequences bring far
+    // fewer rows than others, or are long, or by what either way takes in units: as many turns of
+    // the longest block as there are blocks to a place, against an equal share of all
+    // and what the cuts and the second kernel take (some 20 units).  Whole / in runs, us: 4096
+    // tokens, 8 heads of 128 139/157, 2048 61/66, 1024 37/37, 16 prompts of 512 68/81; 8 pieces
+    // of 512 over 4000 slots 310/316; 2 over 32k 1067/704; one among 23 single tokens 201/123.
+    const int64_t each = ((rows - 1) >> p.rows_shift) + 1;  // blocks of a sequence of max_tokens
+    const int64_t there = std::min(groups, batch.n_seqs * each * heads);
+    if (p.waves == 0) {
+        p.runs = there < chip || units >= 64;
+    } else if (4 * batch.n_tokens < batch.n_seqs * max_tokens) {
+        p.runs = there < 16 * chip;
+    } else if (units >= 256) {
+        p.runs = true;
+    } else {
+        // (a prompt's blocks have half the longest one's units, and long and short ones pair)
+        const bool prompt = max_len < 2 * max_tokens && !window;
+        const int64_t share = there * ((prompt ? units / 2 : units) + CHUNK_BEGIN) / chip;
+        const int64_t turns = prompt ? std::max(units + CHUNK_BEGIN, share) : (there + chip - 1) / chip * (units + CHUNK_BEGIN);
+        p.runs = there < 4 * chip && turns > share + 20;
+    }
+    p.runs = p.runs && units > 4;
     // (units are counted in int32, whatever the lengths; 512 threads or fewer join a block, 256 a token)
-    if (p.blocks > CHUNK_RUN_BLOCKS || batch.n_tokens > MAX_GROUPS || groups > MAX_GROUPS / 2 || units_of(batch.max_pages * cache.page) > kMaxInt / groups)
+    if (p.blocks > CHUNK_RUN_BLOCKS || batch.n_tokens > MAX_GROUPS || groups > MAX_GROUPS / 2 || units_of(batch.max_pages * cache.page) + CHUNK_BEGIN > kMaxInt / groups)
         p.runs = false;
     p.grid = p.runs ? std::min(chip, groups * units / 2) : groups;
     const int64_t slot_rows = p.runs ? 2 * p.grid << p.rows_shift : 0;
@@ -191,6 +212,7 @@ int kq_attn_chunk(const kq_cache *cache, const kq_batch *batch, int q_type, cons
     k.rows_shift = p.rows_shift;
     k.blocks = (int)p.blocks;
     k.runs = p.runs;
+    k.begin = p.waves ? CHUNK_BEGIN : 0;
     if (launch_chunk(k, p, cache->type, cache->dim, q_type, stream) != hipSuccess) return KQ_ERR_HIP;
     count_layer(p.waves == 0 ? V_CHUNK_FEW : V_CHUNK_ROWS);
     return KQ_OK;

@@ -96,8 +96,12 @@ __global__ __launch_bounds__((WAVES == 1 ? NORM_WIDE : WAVES) * 64) void norm_ke
     const int rows_wg = WAVES == 1 ? NORM_WIDE : 1;
     const int t = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
     const ActSections act = {a.qs, a.d, a.bsums, a.alpha};
-    for (int64_t row = (int64_t)blockIdx.x * rows_wg + (WAVES == 1 ? threadIdx.x >> 6 : 0); row < a.M;
-         row += (int64_t)gridDim.x * rows_wg) {
+    // Workgroups go round the chip's 8 dies, each with a cache of its own.  A die takes 8
+    // neighbouring rows of 64, whose scales and sums share lines of the buffer, so that
+    // they leave one cache together.
+    for (int64_t b = blockIdx.x; b < (((a.M + rows_wg - 1) / rows_wg + 63) & ~(int64_t)63); b += gridDim.x) {
+        const int64_t row = ((b & ~(int64_t)63) + (b & 7) * 8 + ((b >> 3) & 7)) * rows_wg + (WAVES == 1 ? threadIdx.x >> 6 : 0);
+        if (row >= a.M) continue;  // (the same for all threads of the row)
         v4f v[C][4];
         Run16<XT> x[C];
         Run16<RT> r[C];
@@ -174,9 +178,10 @@ template <class XT, class RT, int BS>
 hipError_t launch_types(const NormArgs &a, hipStream_t stream) {
     const int need = (a.K + 1023) / 1024;  // waves with a run to each lane
     constexpr int64_t MOST = 1 << 20;      // workgroups to a launch: they go on to further rows
+    const auto groups = [&](int waves) { return waves == 1 ? (a.M + NORM_WIDE - 1) / NORM_WIDE : a.M; };
 #define KQ_NORM(W, C)                                                                                     \
     hipLaunchKernelGGL((norm_kernel<XT, RT, BS, W, C>),                                                   \
-                       dim3((unsigned)std::min<int64_t>(MOST, W == 1 ? (a.M + NORM_WIDE - 1) / NORM_WIDE : a.M)), \
+                       dim3((unsigned)std::min<int64_t>(MOST, (groups(W) + 63) / 64 * 64)),                      \
                        dim3((W == 1 ? NORM_WIDE : W) * 64), 0, stream, a)
     if (need <= 1)
         KQ_NORM(1, 1);

@@ -47,7 +47,7 @@ hipError_t launch_chunk(const ChunkArgs &c, const ChunkPlan &p, int, int dim, in
         // units of every length that the pages hold fit an int, block numbers the kernels' arrays
         const int64_t slots = ((int64_t)c.a.batch.max_pages << c.a.cache.page_shift);
         const int64_t most = slots < (int64_t)c.window + c.sinks + 300 ? slots : (int64_t)c.window + c.sinks + 300;
-        EXPECT(p.blocks <= CHUNK_RUN_BLOCKS && p.grid <= 512);
+        EXPECT(p.blocks <= CHUNK_RUN_BLOCKS && p.grid <= 768);
         EXPECT(p.blocks * heads * (most / CHUNK_UNIT) <= INT32_MAX);
         EXPECT(p.blocks * heads * 512 <= THREADS && c.a.batch.n_tokens * (int64_t)256 <= THREADS);
         EXPECT(p.o_bytes == (2 * p.grid << p.rows_shift) * dim * 4 && p.ml_end == p.o_bytes + (2 * p.grid << p.rows_shift) * 8);

@@ -103,7 +103,7 @@ def test_chunk_workspace(kq):  # noqa: F811
             for m in (1, 128, 1000, 131072, 1 << 30):
                 for w in (0, 1, 5000):
                     # two slots to each of 256 workgroups of 256 rows (or 512 of 128) and the blocks' units
-                    assert size(n, t, 16, w, m) <= 2 * 256 * 256 * (128 * 4 + 8) + 2049 * 4
+                    assert size(n, t, 16, w, m) <= 2 * 256 * 256 * (128 * 4 + 8) + 1025 * 4
     for bad in (size(-1, 1, 8, 0, 10), size(1, 1, 9, 0, 10), size(1, 1, 8, 0, 0), size(1, 1, 8, -1, 10), size(1, 0, 8, 0, 10)):
         assert bad == 0
 
