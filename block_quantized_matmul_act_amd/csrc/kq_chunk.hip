@@ -200,12 +200,14 @@ struct Work {
             }
             const int j = __builtin_amdgcn_readfirstlane(lo);
             block_of(c, block_seq(c, j), j, k);
-            // the run's share [x, x + some) of the block's c.begin + units
-            const int in = x - __builtin_amdgcn_readfirstlane(before[j]), some = min(k.units + c.begin - in, end - u);
+            // the run's share [x, x + some) of the block's c.begin + units, as they were added up (with
+            // offsets that fall, the search can find another sequence than add_up did)
+            const int in = x - __builtin_amdgcn_readfirstlane(before[j]);
+            const int some = min(__builtin_amdgcn_readfirstlane(before[j + 1]) - x, end - u);
             slot = 2 * (int64_t)group + (u != begin);
             u += some;
             k.from = max(in - c.begin, 0);
-            k.to = max(in + some - c.begin, 0);
+            k.to = min(max(in + some - c.begin, 0), k.units);
             k.whole = k.to - k.from == k.units;
             if (k.to > k.from) return true;
         }
@@ -785,6 +787,7 @@ __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
 struct Parts {
     int from, w0, w1;
     Runs runs;
+    // all: the units of a key head (1, with nothing to be found, where offsets that fall leave none)
     __device__ __forceinline__ Parts(const ChunkArgs &c, int j, int h, int all)
         : runs(all * c.a.cache.heads, min(c.a.grid, all * c.a.cache.heads)) {
         from = h * all + c.a.ws_seq[j];
@@ -848,7 +851,7 @@ __global__ __launch_bounds__(256) void chunk_join_few_kernel(const ChunkArgs c, 
     batch_rows(c.a.batch, b, first, count);
     const int i = tok - first;
     if (i < 0 || i >= count) return;  // (a row of no sequence)
-    const int all = c.a.ws_seq[c.blocks];
+    const int all = max(c.a.ws_seq[c.blocks], 1);
     const int sets = SETS / rows, set = threadIdx.x / (D / 4);
     const int row = i * G + head0 % G + min(set / sets, rows - 1);
     const int j = (int)first_block(c, b) + (row >> c.rows_shift);
@@ -868,6 +871,7 @@ __global__ __launch_bounds__(WAVES * 64) void chunk_join_kernel(const ChunkArgs 
     batch_rows(c.a.batch, b, first, count);
     const int64_t rows = (int64_t)count * G;
     const int row0 = (j - (int)first_block(c, b)) << c.rows_shift;
+    if (row0 < 0) return;  // (offsets that fall)
     // the output's row of the sequence's row r
     const auto out_row = [&](int r) { return (int64_t)(first + r / G) * ((int64_t)c.a.cache.heads * G) + h * G + r % G; };
     if (FEW && rows <= 16) {

@@ -458,6 +458,29 @@ def test_chunk_arrays_that_break_the_contract_stay_inside(kq):
                 assert (whole[:8] == 7).all() and (whole[8 + M:] == 7).all()
 
 
+@pytest.mark.parametrize("heads,group,dim,t", [(2, 2, 64, F16), (1, 16, 128, BF16), (4, 4, 256, F8)])
+def test_chunk_arrays_that_break_the_contract_in_runs(kq, heads, group, dim, t):
+    """The same where the work is cut into runs: with offsets that fall, two searches of them may find
+    different sequences for a block, and blocks may be none at all."""
+    page, M = 16, 900
+    qt = BF16 if t == F8 else t
+    k, v = (a.to(DEV) for a in ref.empty_cache(90, heads, page, dim, t, 0.5))
+    q = torch.ones((M, heads * group, dim), dtype=qt, device=DEV)
+    whole = torch.full((M + 16, heads * group, dim), 7.0, dtype=qt, device=DEV)
+    rng = np.random.default_rng(11)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, np.int64).astype(np.int32)).to(DEV)  # noqa: E731
+    cache = kq.PagedCache(k, v)
+    for n in (1, 3, 70):
+        for offsets in (rng.integers(-50, M + 50, n + 1), rng.integers(0, M + 1, n + 1), np.full(n + 1, M), np.full(n + 1, -3),
+                        np.sort(rng.integers(0, M + 1, n + 1))[::-1], np.where(np.arange(n + 1) % 2, M, 0)):
+            batch = kq.Batch(i32(offsets), i32(rng.integers(-100, 1500, n)), i32(rng.integers(-10, 100, (n, 80))))
+            for most in (1, 8, 60, M):
+                for window, most_len in ((0, 20000), (300, 2000), (0, 1 << 20)):
+                    kq.attn_chunk(cache, batch, q, window, 9, max_tokens=most, max_len=most_len, out=whole[8:8 + M])
+                    torch.cuda.synchronize()
+                    assert (whole[:8] == 7).all() and (whole[8 + M:] == 7).all()
+
+
 # ----------------------------------------------------------------------- lora
 
 def activations(kq, rng, M, K, act):
