@@ -472,7 +472,10 @@ struct Tile {
 };
 
 // The softmax sums of RW rows of a wave over tiles of KEYS keys.
-template <class E, bool F8, int D, int KEYS, int RW>
+// RUNS: values lie in LDS by runs of 16 slots, [run][feature][16], not by feature; in 16
+// bits the halves of features 16 .. 31 of each 32 are swapped where a wave reads 32 features at
+// once, which makes the reads conflict-free.
+template <class E, bool F8, int D, int KEYS, int RW, bool RUNS = false>
 struct Attend {
     typedef Mfma<E, RW> MM;
     typedef typename MM::op op_t;
@@ -484,6 +487,7 @@ struct Attend {
     static constexpr int NK = D / (8 * NG), ND = D / RW;         // steps of the first product, results of the second
     static constexpr int NT = KEYS / RW, NS = KEYS / (8 * NG);   // results of the first, steps of the second
     static constexpr int NR = RW * RW / 64;
+    static constexpr int RUN_BYTES = D * 16 * FR::BYTES;  // values of 16 slots
 
     const AttnArgs &a;
     int lane, n, g;
@@ -507,7 +511,10 @@ struct Attend {
         // this lane's row of the first product's results: see the head of the file
         const int krow = RW == 16 ? 8 * (n >> 2) + (n & 3) : 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
         k_from = TL::k_pos(krow, F8 ? g >> 1 : g) + (F8 ? 8 * (g & 1) : 0);
-        v_from = TL::v_pos(n, F8 ? g >> 1 : g) + (F8 ? 8 * (g & 1) : 0);
+        if constexpr (RUNS)
+            v_from = (g >> 1) * RUN_BYTES + n * 16 * FR::BYTES + ((g & 1) ^ (!F8 && RW == 32 ? n >> 4 : 0)) * 8 * FR::BYTES;
+        else
+            v_from = TL::v_pos(n, F8 ? g >> 1 : g) + (F8 ? 8 * (g & 1) : 0);
     }
     // 8 values of this lane: row t (and step kk) of the keys, row d (step s) of the values
     __device__ __forceinline__ raw_t k_frag(const char *lds, int at, int t, int kk) const {
@@ -515,6 +522,8 @@ struct Attend {
         return *reinterpret_cast<const raw_t *>(lds + (at ^ (kk * NG * 8 * FR::BYTES)) + row * TL::KB);
     }
     __device__ __forceinline__ raw_t v_frag(const char *lds, int at, int d, int s) const {
+        if constexpr (RUNS)
+            return *reinterpret_cast<const raw_t *>(lds + at + s * (NG / 2 * RUN_BYTES) + RW * d * 16 * FR::BYTES);
         return *reinterpret_cast<const raw_t *>(lds + (at ^ (s * NG * 8 * FR::BYTES)) + RW * d * TL::VB);
     }
     // begin rows row0 .. of key head h; this lane's token
@@ -604,22 +613,24 @@ struct Attend {
         }
         lift(p);
     }
+    // top: this lane's largest score
+    __device__ __forceinline__ void raise_to(float top) {
+        top = groups_max<RW>(top);
+        const float up = fmaxf(m, top - M_BELOW<E>);
+        const float f = __builtin_amdgcn_exp2f(m - up);
+        m = up;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] *= f;
+        far = __any(fabsf(m) >= M_FAR && m > M_START);  // (M_START: a row that has seen nothing)
+    }
     // Raises m and rescales the sums where it must.
     __device__ __forceinline__ void lift(float (&p)[NT * NR]) {
         float top = p[0];
 #pragma unroll
         for (int r = 1; r < NT * NR; ++r) top = fmaxf(top, p[r]);
         top *= a.score_scale;
-        if (__any(top - m > M_SLACK<E>)) {  // (exact where it is near; P past the slack could be infinite)
-            top = groups_max<RW>(top);
-            const float up = fmaxf(m, top - M_BELOW<E>);
-            const float f = __builtin_amdgcn_exp2f(m - up);
-            m = up;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d] *= f;
-            far = __any(fabsf(m) >= M_FAR && m > M_START);  // (M_START: a row that has seen nothing)
-        }
+        if (__any(top - m > M_SLACK<E>)) raise_to(top);  // (exact where it is near; P past the slack could be infinite)
         if (far) {
 #pragma unroll
             for (int r = 0; r < NT * NR; ++r) p[r] *= a.score_scale;

@@ -276,9 +276,9 @@ __device__ __forceinline__ float add2(uint32_t w, float sum, _Float16) {
 }
 
 // One wave's rows over the tiles.
-template <class E, bool F8, int D, int KEYS, int RW>
+template <class E, bool F8, int D, int KEYS, int RW, bool RUNS>
 struct Rows {
-    typedef Attend<E, F8, D, KEYS, RW> AT;
+    typedef Attend<E, F8, D, KEYS, RW, RUNS> AT;
     AT at;
     const Tiles<KEYS> &tiles;
     int pos;  // slot of this lane's row
@@ -292,8 +292,7 @@ struct Rows {
         if (!at.used) pos = pos1;
         edge = tiles.edges(pos0, pos1);
     }
-    // Masks the scores of tile t, the one at key0, and raises m where it must.  p[r] is key
-    // key0 + 8 NG (r / 8) + 8 g + r % 8.
+    // Masks the scores of tile t, the one at key0.  p[r] is key key0 + 8 NG (r / 8) + 8 g + r % 8.
     __device__ __forceinline__ void mask(int t, int key0, float (&p)[AT::NT * AT::NR]) {
         if (edge.at(t)) {
             int k0 = key0;
@@ -312,32 +311,57 @@ struct Rows {
                 }
             }
         }
-        at.lift(p);
     }
-    // The probabilities of step s, as operands of the second product.  Their sum is taken
-    // after their rounding: the weights of a row then add up to 1, and what rounding does
-    // to a large one is taken back by the division.
-    __device__ __forceinline__ typename AT::op_t probabilities(const float (&p)[AT::NT * AT::NR], int s, float (&sum)[2]) {
-        v4u w;
-        const float by = at.far ? 1.f : at.a.score_scale;  // (far: scaled already)
+    // The probabilities of a tile's scores, as operands of the second product; their sum is added
+    // to the rows' weights.  It is taken after their rounding: the weights of a row then
+    // add up to 1, and what rounding does to a large one is taken back by the division.
+    // m is not compared with every score: a score too far above it shows in the sum,
+    // which is as large as the largest, and then the tile is weighed again under a new m
+    // (a maximum of 32 scores would be a tenth of the vector work of a tile at dim 64).
+    __device__ __forceinline__ void weigh(float (&p)[AT::NT * AT::NR], typename AT::op_t (&pf)[AT::NS]) {
+        constexpr float MOST = M_SLACK<E> > 0 ? (float)(1u << (int)(M_SLACK<E> > 0 ? M_SLACK<E> : 0))
+                                              : 1.f / (float)(1u << (int)(M_SLACK<E> > 0 ? 0 : -M_SLACK<E>));
+        bool scaled = at.far, raised = false;
+        float sum[2];
+        if (scaled) scale(p);
+        while (true) {
+            const float by = scaled ? 1.f : at.a.score_scale;
+            sum[0] = sum[1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], by, -at.m));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], by, -at.m));
-            w[j] = pack2<E>(p0, p1);
-            sum[j & 1] = add2(w[j], sum[j & 1], E{});
+            for (int s = 0; s < AT::NS; ++s) {
+                v4u w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j], by, -at.m));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(p[8 * s + 2 * j + 1], by, -at.m));
+                    w[j] = pack2<E>(p0, p1);
+                    sum[j & 1] = add2(w[j], sum[j & 1], E{});
+                }
+                pf[s] = __builtin_bit_cast(typename AT::op_t, w);
+            }
+            if (raised || !__any(sum[0] + sum[1] > MOST)) break;
+            float top = p[0];
+#pragma unroll
+            for (int r = 1; r < AT::NT * AT::NR; ++r) top = fmaxf(top, p[r]);
+            at.raise_to(top * by);
+            raised = true;
+            if (at.far && !scaled) {
+                scale(p);
+                scaled = true;
+            }
         }
-        return __builtin_bit_cast(typename AT::op_t, w);
+        at.l += sum[0] + sum[1];
+    }
+    __device__ __forceinline__ void scale(float (&p)[AT::NT * AT::NR]) {
+#pragma unroll
+        for (int r = 0; r < AT::NT * AT::NR; ++r) p[r] *= at.a.score_scale;
     }
     __device__ __forceinline__ void tile(const char *lds, int buf, int t, int key0) {
         float p[AT::NT * AT::NR];
         typename AT::op_t pf[AT::NS];
         at.template products<false, true, 4>(lds, 0, pf, buf, p);
         mask(t, key0, p);
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < AT::NS; ++s) pf[s] = probabilities(p, s, sum);
-        at.l += sum[0] + sum[1];
+        weigh(p, pf);
         at.template products<true, false, 4>(lds, buf + AT::TL::K_BYTES, pf, 0, p);
     }
     // The wave's rows to the output or, a part, to the workspace as they lie in the lanes.
@@ -371,12 +395,14 @@ struct Rows {
 };
 
 // Up to 16 rows: the waves take tiles in turn, each its own in LDS without a barrier,
-// and their sums are joined in LDS.
+// and their sums are joined in LDS.  What bounds them is memory, and what keeps it busy the waves
+// on a compute unit: tiles of 32 keys leave room for 3 workgroups (8 bits, dim 128; 96 sequences
+// under a window of 2048, 64 query and 8 key heads: 79 us, 5.1 TB/s; tiles of 64 keys 87).
 template <class E, bool F8, int D>
 struct Few {
-    static constexpr int RW = 16, KEYS = D * (F8 ? 1 : 2) >= 256 ? 32 : 64;
+    static constexpr int RW = 16, KEYS = 32;
     typedef Tile<E, F8, D, KEYS, RW, 64, true> TL;
-    typedef Rows<E, F8, D, KEYS, RW> RS;
+    typedef Rows<E, F8, D, KEYS, RW, false> RS;
     static constexpr int O_FLOATS = RW * (D + 4);
     static constexpr int WAVE_BYTES = TL::BYTES > O_FLOATS * 4 ? TL::BYTES : (O_FLOATS * 4 + 1023) / 1024 * 1024;
 };
@@ -476,31 +502,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void chunk_few_kernel(const 
     }
 }
 
-// A wave's share of the copies of tiles into LDS.  A copy fills 1 KB
-// of LDS in the order of the lanes, so the places of Tile::k_pos and v_pos are met by
-// what each lane reads: the piece that belongs where it writes.  A wave's keys lie in one
-// page, and so do the values of a tile where a page covers it: their addresses are
-// scalar, looked up a turn before they are needed, and a lane adds an offset that never
-// changes.
-// SMALL: pages smaller than a tile.
-template <class E, bool F8, int D, int KEYS, int RW, int WAVES, bool SMALL>
+// A wave's share of the copies of tiles into LDS.  A copy fills 1 KB of LDS in the order of
+// the lanes, so the places in LDS (Tile::k_pos, and values by runs of 16 slots: see
+// Attend) are met by what each lane reads: the piece that belongs where it writes.  A
+// wave's keys lie in one page and so do its values: their addresses are scalar, looked up a
+// turn before they are needed, and a lane adds an offset that never changes.  (With values by
+// features in LDS, every lane of a tile of small pages chose its page: ragged prompts under a
+// window, heads of 64, took 108 us with pages of 16 and 99 with 64, and take 94 now with both.)
+template <class E, bool F8, int D, int KEYS, int RW, int WAVES>
 struct Stage {
-    typedef Tile<E, F8, D, KEYS, RW, 64, true> PL;  // (for the places in LDS alone)
+    typedef Tile<E, F8, D, KEYS, RW, 64, true> PL;  // (for the places of keys alone)
     typedef Frag<E, F8> FR;
-    static constexpr int ES = FR::BYTES, KB = PL::KB, VB = PL::VB;
+    static constexpr int ES = FR::BYTES, KB = PL::KB;
     static constexpr int COPIES = KEYS * KB / 1024;             // of a tile's keys, and of its values
     static constexpr int N = COPIES / WAVES;                    // a wave's of each
     static constexpr int TURN = 2 * N;                          // a wave's of a tile
     static constexpr int K_ROWS = N * 1024 / KB;                // keys of a wave, in one run of 16
-    static_assert(16 % K_ROWS == 0 && COPIES % WAVES == 0, "a wave's keys share a page");
+    static constexpr int RUN_BYTES = D * 16 * ES;               // values of 16 slots
+    static_assert(16 % K_ROWS == 0 && COPIES % WAVES == 0 && RUN_BYTES % (N * 1024) == 0, "a wave's keys share a page, and its values");
 
     const_ints pages;     // the sequence's row of the table
     const char *k_head, *v_head;  // the head's place in page 0
     uint64_t page_bytes;  // from page to page
     int last_page, shift;
     int wave, lane, total;
-    uint32_t k_off[N], v_off[N];  // of this lane's pieces from the first key's row / the tile's first value
-    int v_key[N];         // the first key of its piece of the values
+    uint32_t k_off[N], v_off[N];  // of this lane's pieces from the first key's row / the run's first value
     uint32_t lds;
 
     __device__ __forceinline__ Stage(const AttnArgs &a, const Block &k, char *lds_, int wave_, int lane_) : wave(wave_), lane(lane_) {
@@ -515,58 +541,38 @@ struct Stage {
         lds = lds_offset(lds_);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int k_at = copy(i) * 1024 + lane * 16, v_at = copy(i) * 1024 + lane * 16;  // in the tile
+            const int k_at = copy(i) * 1024 + lane * 16;  // in the tile
             const int row = k_at / KB, piece = (k_at % KB / 16) ^ PL::k_xor(row);
             k_off[i] = (row - k_row()) * KB + piece * 16;
-            const int d = v_at / VB, v_piece = (v_at % VB / 16) ^ PL::v_xor(d);
-            v_key[i] = v_piece * (16 / ES);
-            v_off[i] = ((uint32_t)d << shift) * ES + (SMALL ? 0 : v_piece * 16);
+            const int v_at = k_at - v_run() * RUN_BYTES;  // in the run
+            v_off[i] = ((uint32_t)(v_at / (16 * ES)) << shift) * ES + v_half(i) * 16;
         }
     }
     __device__ __forceinline__ int copy(int i) const { return N * wave + i; }
     __device__ __forceinline__ int k_row() const { return copy(0) * 1024 / KB; }
+    __device__ __forceinline__ int v_run() const { return copy(0) * 1024 / RUN_BYTES; }
+    // Which 16 bytes of a feature's run this lane copies.
+    __device__ __forceinline__ int v_half(int i) const {
+        const int d = (copy(i) * 64 + lane) / ES % D;
+        return F8 ? 0 : (lane & 1) ^ (RW == 32 ? d >> 4 & 1 : 0);
+    }
 
     // A slot past the sequence's end is taken to lie in its last run (masked later).
     __device__ __forceinline__ int k_slot(int key0) const { return min(key0 + k_row(), (total - 1) & -K_ROWS); }
-    __device__ __forceinline__ int v_slot(int key0) const { return min(key0, (total - 1) & -KEYS); }
-    __device__ __forceinline__ int lane_slot(int key0, int i) const {
-        return min(key0 + v_key[i], ((total - 1) & ~15) + (v_key[i] & 15));
-    }
+    __device__ __forceinline__ int v_slot(int key0) const { return min(key0 + 16 * v_run(), (total - 1) & ~15); }
     __device__ __forceinline__ uint64_t page_at(int e) const { return (uint64_t)(uint32_t)min(max(e, 0), last_page) * page_bytes; }
-    // The tile's page entries.
+    // The page entries of a tile's copies.
     __device__ __forceinline__ int k_entry(int key0) const { return pages[k_slot(key0) >> shift]; }
-    typedef int Pages __attribute__((ext_vector_type(SMALL ? KEYS / 16 : 1)));  // of its runs of 16 slots, or one for all
-    __device__ __forceinline__ Pages v_entry(int key0) const {
-        Pages p;
-        if constexpr (SMALL) {
-#pragma unroll
-            for (int r = 0; r < KEYS / 16; ++r) p[r] = pages[min(key0 + 16 * r, (total - 1) & ~15) >> shift];
-        } else {
-            p[0] = pages[v_slot(key0) >> shift];
-        }
-        return p;
-    }
+    __device__ __forceinline__ int v_entry(int key0) const { return pages[v_slot(key0) >> shift]; }
     __device__ __forceinline__ void copy_k(int buf, int key0, int e) const {
         const char *p = k_head + page_at(e) + (uint32_t)((k_slot(key0) & ((1 << shift) - 1)) * KB);
 #pragma unroll
         for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, k_off[i]);
     }
-    __device__ __forceinline__ void copy_v(int buf, int key0, Pages e) const {
-        const int mask = (1 << shift) - 1;
-        if constexpr (SMALL) {
+    __device__ __forceinline__ void copy_v(int buf, int key0, int e) const {
+        const char *p = v_head + page_at(e) + (uint32_t)((v_slot(key0) & ((1 << shift) - 1)) * ES);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int run = v_key[i] >> 4;
-                int mine = e[0];
-#pragma unroll
-                for (int r = 1; r < KEYS / 16; ++r) mine = run == r ? e[r] : mine;
-                copy16(lds + buf + copy(i) * 1024, v_head + page_at(mine) + (v_off[i] + (uint32_t)((lane_slot(key0, i) & mask) * ES)));
-            }
-        } else {
-            const char *p = v_head + page_at(e[0]) + (uint32_t)((v_slot(key0) & mask) * ES);
-#pragma unroll
-            for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, v_off[i]);
-        }
+        for (int i = 0; i < N; ++i) copy16(lds + buf + copy(i) * 1024, p, v_off[i]);
     }
     // In a tile that some row does not see whole, after this wave's copies of it have arrived:
     // zeros for values past the end, which may be anything, and for infinite and NaN ones;
@@ -577,7 +583,7 @@ struct Stage {
         for (int i = 0; i < N; ++i) {
             v4u *p = reinterpret_cast<v4u *>(at + buf + copy(i) * 1024 + lane * 16);
             v4u w = *p;
-            const int left = total - (key0 + v_key[i]);
+            const int left = total - (key0 + 16 * v_run() + 8 * v_half(i));
             if constexpr (F8) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -597,17 +603,20 @@ struct Stage {
     }
 };
 
-// Up to 128 rows, and all of heads of 64: 4 waves of 32 rows share the tiles, three in LDS: one
-// in use and two on their way.  Copies of tile i + 2 start when all waves are done with
-// tile i - 1.
-template <class E, bool F8, int D, bool SMALL>
-__global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
+// Up to 128 rows, and all of heads of 64: 4 waves of 32 rows share the tiles; one is in use and
+// AHEAD are on their way.  Copies of tile i + AHEAD start when all waves are done with tile i - 1.
+// Heads of 64 leave room for four workgroups on a compute unit if only one tile is on its
+// way (98 -> 95 us against three workgroups with two).  There the softmax takes as many
+// cycles as the products: what bounds it is the vector unit.
+template <class E, bool F8, int D>
+__global__ __launch_bounds__(256, D == 64 ? 4 : 2) void chunk_tile_kernel(const ChunkArgs c) {
     constexpr int RW = 32, KEYS = D == 128 ? 32 : 64;  // (64 at dim 128 would not fit the registers)
-    typedef Stage<E, F8, D, KEYS, RW, 4, SMALL> ST;
-    typedef Rows<E, F8, D, KEYS, RW> RS;
+    constexpr int AHEAD = D == 64 ? 1 : 2, BUFS = AHEAD + 1;  // tiles on their way
+    typedef Stage<E, F8, D, KEYS, RW, 4> ST;
+    typedef Rows<E, F8, D, KEYS, RW, true> RS;
     constexpr int BYTES = RS::AT::TL::BYTES, K_BYTES = RS::AT::TL::K_BYTES;
 
-    __shared__ __align__(1024) char lds[3 * BYTES];
+    __shared__ __align__(1024) char lds[BUFS * BYTES];
     __shared__ int odd;  // whether masked tiles copied so far have infinite or NaN values
     __shared__ int before[CHUNK_RUN_BLOCKS + 1], waves[4];
 
@@ -624,34 +633,37 @@ __global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
         const ST st(a, k, lds, wave, thread & 63);
         RS rs(a, ts, thread);
         const int first = ts.from, n = ts.to - ts.from;
-        int key0 = ts.key(first), key1 = ts.key(first + 1), key2 = ts.key(first + 2);
-        st.copy_v(K_BYTES, key0, st.v_entry(key0));
-        st.copy_k(0, key0, st.k_entry(key0));
-        st.copy_v(BYTES + K_BYTES, key1, st.v_entry(key1));
-        st.copy_k(BYTES, key1, st.k_entry(key1));
-        int ke = st.k_entry(key2);  // of the tile to be copied next
-        typename ST::Pages ve = st.v_entry(key2);
+        int key[BUFS];  // the first slots of this tile and those after it
+#pragma unroll
+        for (int i = 0; i < BUFS; ++i) key[i] = ts.key(first + i);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            st.copy_v(i * BYTES + K_BYTES, key[i], st.v_entry(key[i]));
+            st.copy_k(i * BYTES, key[i], st.k_entry(key[i]));
+        }
+        int ke = st.k_entry(key[AHEAD]);  // of the tile to be copied next
+        int ve = st.v_entry(key[AHEAD]);
         const int row0 = (k.rb << c.rows_shift) + wave * RW;
         const bool rows = row0 < k.sq.T * a.group;  // (a wave without rows only copies)
         rs.begin(k, row0);
         int buf = 0;
         for (int i = 0; i < n; ++i) {
             const int t = first + i;
-            // (q's loads and a lookup may be among the newest: then this waits for less than it could)
-            arrived<ST::TURN>();
-            if (ts.block.at(t) && st.clean_v(lds, buf + K_BYTES, key0)) odd = 1;
+            // (where q's loads are among the newest, this waits for more than it has to)
+            arrived<(AHEAD - 1) * ST::TURN>();
+            if (ts.block.at(t) && st.clean_v(lds, buf + K_BYTES, key[0])) odd = 1;
             __syncthreads();
-            const int next = buf >= BYTES ? buf - BYTES : 2 * BYTES;  // tile i + 2
-            st.copy_v(next + K_BYTES, key2, ve);
-            st.copy_k(next, key2, ke);
-            const int key3 = ts.key(t + 3);
-            ke = st.k_entry(key3);
-            ve = st.v_entry(key3);
-            if (rows) rs.tile(lds, buf, t, key0);
-            key0 = key1;
-            key1 = key2;
-            key2 = key3;
-            buf = buf == 2 * BYTES ? 0 : buf + BYTES;
+            const int next = buf == 0 ? AHEAD * BYTES : buf - BYTES;  // of tile i + AHEAD
+            st.copy_v(next + K_BYTES, key[AHEAD], ve);
+            st.copy_k(next, key[AHEAD], ke);
+            const int then = ts.key(t + BUFS);
+            ke = st.k_entry(then);
+            ve = st.v_entry(then);
+            if (rows) rs.tile(lds, buf, t, key[0]);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) key[j] = key[j + 1];
+            key[AHEAD] = then;
+            buf = buf == AHEAD * BYTES ? 0 : buf + BYTES;
         }
         arrived<0>();  // (copies of tiles past the last)
         __syncthreads();
@@ -674,11 +686,11 @@ __global__ __launch_bounds__(256, 2) void chunk_tile_kernel(const ChunkArgs c) {
 // 2 i + 4; keys i + 3 at 2 i + 6) after the barrier that follows.
 // A sequence that brings only a few rows among others that bring many takes the way of
 // the few.
-template <class E, bool F8, int D, bool SMALL>
+template <class E, bool F8, int D>
 __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
     constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
-    typedef Stage<E, F8, D, KEYS, RW, 8, SMALL> ST;
-    typedef Rows<E, F8, D, KEYS, RW> RS;
+    typedef Stage<E, F8, D, KEYS, RW, 8> ST;
+    typedef Rows<E, F8, D, KEYS, RW, true> RS;
     typedef typename RS::AT AT;
     constexpr int BYTES = AT::TL::BYTES, K_BYTES = AT::TL::K_BYTES, FEW_BYTES = Few<E, F8, D>::WAVE_BYTES;
     constexpr int FEW_WAVES = FEW_IN_WIDE<E, F8, D>;
@@ -719,7 +731,7 @@ __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
         }
         int kn = ts.key(first + 2 + ahead), vn = ts.key(first + 1 + ahead);  // the slots of the next
         int ke = st.k_entry(kn);
-        typename ST::Pages ve = st.v_entry(vn);
+        int ve = st.v_entry(vn);
         int kb = late ? 0 : 2 * BYTES, vb = late ? 2 * BYTES : BYTES;  // and their buffers
         rs.begin(k, (k.rb << c.rows_shift) + wave * RW);
         float p[AT::NT * AT::NR];
@@ -737,7 +749,7 @@ __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
             const int old = vb == 0 ? 2 * BYTES : vb - BYTES;
             if (more) {
                 const int kn2 = ts.key(t + 3 + ahead), ke2 = st.k_entry(kn2);
-                const typename ST::Pages ve2 = st.v_entry(kn);
+                const int ve2 = st.v_entry(kn);
                 st.copy_v(vb + K_BYTES, vn, ve);
                 st.copy_k(kb, kn, ke);
                 vn = kn;
@@ -748,14 +760,13 @@ __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
                 vb = vb == 2 * BYTES ? 0 : vb + BYTES;
             }
             rs.mask(t, key0, p);
-            float sum[2] = {0.f, 0.f};
+            rs.weigh(p, pf);
 #pragma unroll
             for (int s = 0; s < AT::NS; ++s) {
-                v4u w = __builtin_bit_cast(v4u, rs.probabilities(p, s, sum));
+                v4u w = __builtin_bit_cast(v4u, pf[s]);
                 asm volatile("" : "+v"(w));  // (here, and not among the products)
                 pf[s] = __builtin_bit_cast(typename AT::op_t, w);
             }
-            at.l += sum[0] + sum[1];
             key0 = ts.key(t + 1);
             if (more)
                 arrived<ST::TURN>();
@@ -912,7 +923,6 @@ hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t str
     c.few_shift = CHUNK_UNIT_SHIFT;
     if (p.waves == 8 && FEW_IN_WIDE<E, F8, D>) c.few_shift = D * (F8 ? 1 : 2) == 128 ? 8 : 7;
     const dim3 grid((unsigned)p.grid);
-    const int page = 1 << c.a.cache.page_shift;
     const unsigned blocks = (unsigned)(p.blocks * c.a.cache.heads);
     if (p.waves == 0) {
         hipLaunchKernelGGL((chunk_few_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
@@ -928,10 +938,7 @@ hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t str
     }
     if constexpr (D < 256) {
         if (p.waves == 4) {
-            if (page < (D == 128 ? 32 : 64))
-                hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D, true>), grid, dim3(256), 0, stream, c);
-            else
-                hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D, false>), grid, dim3(256), 0, stream, c);
+            hipLaunchKernelGGL((chunk_tile_kernel<E, F8, D>), grid, dim3(256), 0, stream, c);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess || !p.runs) return e;
             hipLaunchKernelGGL((chunk_join_kernel<E, D, 32, 4, false>), dim3(blocks), dim3(256), 0, stream, c);
@@ -939,10 +946,7 @@ hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t str
         }
     }
     if constexpr (D > 64) {
-        if (page < (D == 256 ? 32 : 64))
-            hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, true>), grid, dim3(512), 0, stream, c);
-        else
-            hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, false>), grid, dim3(512), 0, stream, c);
+        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D>), grid, dim3(512), 0, stream, c);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !p.runs) return e;
         hipLaunchKernelGGL((chunk_join_kernel<E, D, D == 256 ? 16 : 32, 8, FEW_IN_WIDE<E, F8, D> != 0>), dim3(blocks), dim3(512), 0, stream, c);

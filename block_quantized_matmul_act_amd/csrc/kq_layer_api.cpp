@@ -81,7 +81,7 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
         return (slots + CHUNK_UNIT - 1) / CHUNK_UNIT + 2;
     };
     const int64_t units = units_of(max_len), groups = p.blocks * heads;
-    const int64_t chip = p.waves == 8 ? 256 : p.waves == 4 && dim == 64 ? 768 : 512;  // places for workgroups
+    const int64_t chip = p.waves == 8 ? 256 : p.waves == 4 && dim == 64 ? 768 : 512;  // places for workgroups (dim 64: 1024, but runs are shorter then: a prompt 90 -> 107)
     // Whole blocks or runs?  Few rows: runs where blocks are fewer than places for them on the
     // chip, or long (their lengths then differ by much).  More: runs where some sequences bring far
     // fewer rows than others, or are long, or by what either way takes in units: as many turns of
