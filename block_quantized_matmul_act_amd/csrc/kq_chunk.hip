@@ -603,7 +603,7 @@ struct Stage {
     }
 };
 
-// Up to 128 rows, and all of heads of 64: 4 waves of 32 rows share the tiles; one is in use and
+// Up to 128 rows, short texts with heads of 128, and all of heads of 64: 4 waves of 32 rows share the tiles; one is in use and
 // AHEAD are on their way.  Copies of tile i + AHEAD start when all waves are done with tile i - 1.
 // Heads of 64 leave room for four workgroups on a compute unit if only one tile is on its
 // way (98 -> 95 us against three workgroups with two).  There the softmax takes as many
@@ -691,9 +691,12 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void chunk_tile_kernel(const 
 // of 128, 137 us; 2 pieces of 512 over 32768, 64 query heads, 691 us; a library's
 // product of two matrices of 8192: 1310).  All waves in step: 160 and 800 us.  Staged through
 // registers instead of copied: 148 and 864.
-template <class E, bool F8, int D>
+// RW: rows of a wave, 32, or 16 for less work at dim 256.
+template <class E, bool F8, int D, int RW>
 __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
-    constexpr int RW = D == 256 ? 16 : 32, KEYS = D == 256 ? 32 : 64;
+    constexpr int KEYS = D == 256 ? 32 : 64;
+    // operands read ahead (6 do not fit the registers beside 32 rows of 256: 363 us for 268)
+    constexpr int AHEAD = D == 256 && RW == 32 && !F8 ? 2 : 6;
     typedef Stage<E, F8, D, KEYS, RW, 8> ST;
     typedef Rows<E, F8, D, KEYS, RW, true> RS;
     typedef typename RS::AT AT;
@@ -779,19 +782,19 @@ __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
                 arrived<0>();
             if (i && clean < ts.to && ts.block.at(clean) && st.clean_v(lds, old + K_BYTES, ts.key(clean))) odd = 1;
         };
-        at.template products<false, true, 6>(lds, 0, pf, 0, p);
+        at.template products<false, true, AHEAD>(lds, 0, pf, 0, p);
         __syncthreads();
         vector_half(0);
         __syncthreads();
         for (int i = 1; i < n; ++i) {
             const int before = buf;
             buf = buf == 2 * BYTES ? 0 : buf + BYTES;
-            at.template products<true, true, 6>(lds, before + K_BYTES, pf, buf, p);
+            at.template products<true, true, AHEAD>(lds, before + K_BYTES, pf, buf, p);
             __syncthreads();
             vector_half(i);
             __syncthreads();
         }
-        at.template products<true, false, 6>(lds, buf + K_BYTES, pf, 0, p);
+        at.template products<true, false, AHEAD>(lds, buf + K_BYTES, pf, 0, p);
         __syncthreads();
         if (!late) __syncthreads();
         if (odd) rs.odd_values(k, ts.from, 1);
@@ -933,6 +936,16 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(const ChunkArgs c) {
     }
 }
 
+template <class E, bool F8, int D, int RW>
+hipError_t launch_wide(const ChunkArgs &c, const ChunkPlan &p, hipStream_t stream) {
+    hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D, RW>), dim3((unsigned)p.grid), dim3(512), 0, stream, c);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.runs) return e;
+    hipLaunchKernelGGL((chunk_join_kernel<E, D, RW, FEW_IN_WIDE<E, F8, D> != 0>), dim3((unsigned)(p.blocks * c.a.cache.heads), 8), dim3(256),
+                       0, stream, c);
+    return hipGetLastError();
+}
+
 template <class E, bool F8, int D>
 hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t stream) {
     ChunkArgs c = args;
@@ -965,12 +978,10 @@ hipError_t launch_dim(const ChunkArgs &args, const ChunkPlan &p, hipStream_t str
             return hipGetLastError();
         }
     }
-    if constexpr (D > 64) {
-        hipLaunchKernelGGL((chunk_wide_kernel<E, F8, D>), grid, dim3(512), 0, stream, c);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || !p.runs) return e;
-        hipLaunchKernelGGL((chunk_join_kernel<E, D, D == 256 ? 16 : 32, FEW_IN_WIDE<E, F8, D> != 0>), dim3(blocks, 8), dim3(256), 0, stream, c);
+    if constexpr (D == 256) {
+        if (p.rows_shift == 7) return launch_wide<E, F8, D, 16>(c, p, stream);
     }
+    if constexpr (D > 64) return launch_wide<E, F8, D, 32>(c, p, stream);
     return hipGetLastError();
 }
 

@@ -72,15 +72,37 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
     const int64_t heads = cache.heads, group = q_heads / heads, dim = cache.dim;
     max_tokens = std::min(max_tokens, batch.n_tokens);
     const int64_t rows = max_tokens * group;
-    p.waves = rows <= 16 ? 0 : dim == 64 || (rows <= 128 && dim == 128) ? 4 : 8;
-    p.rows_shift = p.waves == 0 ? 4 : p.waves == 4 || dim == 256 ? 7 : 8;
-    p.blocks = ((batch.n_tokens * group) >> p.rows_shift) + batch.n_seqs;
     // the units of a block whose sequence has `slots` slots, at most
-    const auto units_of = [&](int64_t slots) {
-        if (window) slots = std::min(slots, window + sinks + ((int64_t)1 << p.rows_shift) / group + 1);
+    const auto units_of = [&](int64_t slots, int rows_shift) {
+        if (window) slots = std::min(slots, window + sinks + ((int64_t)1 << rows_shift) / group + 1);
         return (slots + CHUNK_UNIT - 1) / CHUNK_UNIT + 2;
     };
-    const int64_t units = units_of(max_len), groups = p.blocks * heads;
+    // Which blocks?  Larger ones read a tile for more rows, smaller ones spread over more of the
+    // chip and cost less to begin and end.  Heads of 128, 4 waves for 128 rows or 8 for 256, us:
+    // 16 prompts of 512 57/68, 8 pieces of 300 over 600 37/54, a window of 1024 over 2 pieces of 512
+    // 41/50, a prompt of 1024 33/37, of 2048 59/62, 4 of them 118/110, of 4096 166/140.  Heads of
+    // 256, 8 waves for 128 rows or 256: a prompt of 1024 45/63, of 2500 144/136, of 4096 318/264, 8
+    // pieces of 300 over 600 73/85, 16 of 40 over 3000 121/104; in 8 bits a piece of 512 over
+    // 2000 79/70.
+    const bool few_among_many = 4 * batch.n_tokens < batch.n_seqs * max_tokens;
+    if (rows <= 16) {
+        p.waves = 0;
+        p.rows_shift = 4;
+    } else if (dim == 64 || (dim == 128 && (rows <= 128 || (!few_among_many && units_of(max_len, 7) <= 32)))) {
+        p.waves = 4;
+        p.rows_shift = 7;
+    } else {
+        p.waves = 8;
+        p.rows_shift = 8;
+        if (dim == 256) {
+            const bool f8 = cache.type == KQ_T_F8;
+            const bool large = batch.n_seqs * (((rows - 1) >> 8) + 1) * heads > 320 || units_of(max_len, 8) >= (f8 ? 40 : 48);
+            // (16 bits: the few have no way of their own there)
+            if (rows <= 128 || !large || (few_among_many && !f8)) p.rows_shift = 7;
+        }
+    }
+    p.blocks = ((batch.n_tokens * group) >> p.rows_shift) + batch.n_seqs;
+    const int64_t units = units_of(max_len, p.rows_shift), groups = p.blocks * heads;
     const int64_t chip = p.waves == 8 ? 256 : p.waves == 4 && dim == 64 ? 768 : 512;  // places for workgroups (dim 64: 1024, but runs are shorter then: a prompt 90 -> 107)
     // Whole blocks or runs?  Few rows: runs where blocks are fewer than places for them on the
     // chip, or long (their lengths then differ by much).  More: runs where some sequences bring far
@@ -93,7 +115,7 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
     const int64_t there = std::min(groups, batch.n_seqs * each * heads);
     if (p.waves == 0) {
         p.runs = there < chip || units >= 64;
-    } else if (4 * batch.n_tokens < batch.n_seqs * max_tokens) {
+    } else if (few_among_many) {
         p.runs = there < 16 * chip;
     } else if (units >= 256) {
         p.runs = true;
@@ -106,7 +128,7 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
     }
     p.runs = p.runs && units > 4;
     // (units are counted in int32, whatever the lengths; 512 threads or fewer join a block, 256 a token)
-    if (p.blocks > CHUNK_RUN_BLOCKS || batch.n_tokens > MAX_GROUPS || groups > MAX_GROUPS / 2 || units_of(batch.max_pages * cache.page) + CHUNK_BEGIN > kMaxInt / groups)
+    if (p.blocks > CHUNK_RUN_BLOCKS || batch.n_tokens > MAX_GROUPS || groups > MAX_GROUPS / 2 || units_of(batch.max_pages * cache.page, p.rows_shift) + CHUNK_BEGIN > kMaxInt / groups)
         p.runs = false;
     p.grid = p.runs ? std::min(chip, groups * units / 2) : groups;
     const int64_t slot_rows = p.runs ? 2 * p.grid << p.rows_shift : 0;

@@ -55,7 +55,7 @@ hipError_t launch_chunk(const ChunkArgs &c, const ChunkPlan &p, int, int dim, in
     } else {
         EXPECT(p.grid == p.blocks * heads);
     }
-    EXPECT(p.rows_shift == (p.waves == 0 ? 4 : p.waves == 4 ? 7 : dim == 256 ? 7 : 8));
+    EXPECT(p.rows_shift == (p.waves == 0 ? 4 : p.waves == 4 ? 7 : 8) || (p.waves == 8 && dim == 256 && p.rows_shift == 7));
     EXPECT(!(p.waves == 4 && dim == 256));
     return hipSuccess;
 }

@@ -218,7 +218,8 @@ def test_norm_feeds_the_product(kq):
 
 def check_chunk(kq, step, hq, hkv, dim, qt, kvt, window=0, sinks=0, k=None, v=None, k_scale=1.0, v_scale=1.0, scale=None,
                 max_tokens=None, max_len=None, types=None, q=None):
-    """One call in q's type and one in float32 against the plain form."""
+    """One call in q's type and one in float32 against the plain form; without a max_len, in q's type
+    also as if sequences were longer (larger blocks of rows) and far longer (in runs)."""
     if k is None:
         k, v = ref.fill_cache(step, hkv, dim, kvt)
     q = ref.draw(step.rng, (step.M, hq, dim), 1.5).to(qt) if q is None else q
@@ -227,16 +228,16 @@ def check_chunk(kq, step, hq, hkv, dim, qt, kvt, window=0, sinks=0, k=None, v=No
     cache, batch = kq.PagedCache(up(k), up(v), k_scale, v_scale), step.batch(kq)
     worst = 0.0
     for out_dtype in types or (qt, F32):
-        got = torch.full((step.M, hq, dim), math.nan, dtype=out_dtype, device=DEV)
-        kq.attn_chunk(cache, batch, up(q), window, sinks, scale, max_tokens or max(1, step.max_new), max_len or step.max_len,
-                      out=got)
-        torch.cuda.synchronize()
-        got = got.cpu().double()
         tol = bound if out_dtype == F32 else ref.rounded_bound(want, bound, out_dtype)
-        assert torch.isfinite(got).all(), (out_dtype, int((~torch.isfinite(got)).sum()))
-        err = ((got - want).abs() / tol.clamp(min=1e-30)).max().item() if got.numel() else 0.0
-        assert ((got - want).abs() <= tol).all(), (out_dtype, err)
-        worst = max(worst, err)
+        for most in [max_len or step.max_len] + [5000, 40000] * (not max_len and out_dtype == qt):
+            got = torch.full((step.M, hq, dim), math.nan, dtype=out_dtype, device=DEV)
+            kq.attn_chunk(cache, batch, up(q), window, sinks, scale, max_tokens or max(1, step.max_new), most, out=got)
+            torch.cuda.synchronize()
+            got = got.cpu().double()
+            assert torch.isfinite(got).all(), (out_dtype, most, int((~torch.isfinite(got)).sum()))
+            err = ((got - want).abs() / tol.clamp(min=1e-30)).max().item() if got.numel() else 0.0
+            assert ((got - want).abs() <= tol).all(), (out_dtype, most, err)
+            worst = max(worst, err)
     return worst
 
 
@@ -262,7 +263,7 @@ def test_chunk_lengths_and_rows(kq, qt, kvt, dim, group, tokens):
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (16, 0), (63, 64), (64, 1), (65, 200), (128, 63), (200, 4),
                                           (1000, 1000), (1 << 30, 0), (1 << 30, 1 << 30), (7, 1 << 30)])
-@pytest.mark.parametrize("dim,group,tokens", [(128, 4, 1), (64, 4, 20), (128, 2, 200), (256, 3, 90)])
+@pytest.mark.parametrize("dim,group,tokens", [(128, 4, 1), (64, 4, 20), (128, 2, 200), (256, 3, 90), (256, 4, 400)])
 def test_chunk_windows(kq, window, sinks, dim, group, tokens):
     """Windows and sinks that meet, overlap, end inside tiles, cover everything and leave one slot."""
     step = Step(window + sinks, [0, 3, 64, 333, 900], [tokens, max(1, tokens // 2), tokens, tokens, 1], 32)
@@ -327,18 +328,20 @@ def test_chunk_equals_tree(kq):
 
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("qt,kvt,dim,group,tokens", [(BF16, BF16, 128, 1, 12), (F16, F16, 64, 4, 30), (BF16, F8, 128, 8, 60),
-                                                     (F16, F8, 256, 2, 40), (BF16, BF16, 128, 4, 150), (F16, F16, 64, 2, 8)])
-def test_chunk_what_unseen_slots_hold_does_not_count(kq, bad, qt, kvt, dim, group, tokens):
+                                                     (F16, F8, 256, 2, 40), (BF16, BF16, 128, 4, 150), (F16, F16, 64, 2, 8),
+                                                     (BF16, BF16, 256, 4, 60), (BF16, F8, 256, 3, 90)])
+@pytest.mark.parametrize("window,longer", [(50, 0), (3100, 3300)], ids=["short", "long"])
+def test_chunk_what_unseen_slots_hold_does_not_count(kq, bad, qt, kvt, dim, group, tokens, window, longer):
     """Slots with infinite or NaN keys and values: later tokens, slots before the window and between
     it and the sinks.  They reach the rows that see them and no other."""
-    window, sinks = 50, 3
-    step = Step(9, [137, 0, 64, 300], [tokens, 5, max(1, tokens - 7), 1], 16)
+    sinks = 3
+    step = Step(9, [137 + longer, 0, 64, 300 + longer], [tokens, 5, max(1, tokens - 7), 1], 16)
     k, v = ref.fill_cache(step, 2, dim, kvt)
     kf, vf = k.float(), v.float()
     rotten = []
     for b, (L, n) in enumerate(zip(step.lens, step.new)):
         total = int(L + n)
-        spots = [s for s in (5, total - 2, total // 2, total - 60) if 0 <= s < total]
+        spots = [s for s in (5, total - 2, total // 2, total - window - 10) if 0 <= s < total]
         p, at = step.where(b, spots)
         vf[p, :, 3:dim:17, at] = bad
         kf[p[:1], :, at[:1]] = bad
@@ -349,15 +352,16 @@ def test_chunk_what_unseen_slots_hold_does_not_count(kq, bad, qt, kvt, dim, grou
     q = ref.draw(step.rng, (step.M, 2 * group, dim)).to(qt)
     clean_k, clean_v = (torch.where(torch.isfinite(t.float()), t.float(), 0.0).to(kvt) for t in (k, v))
     want, bound = lref.chunk(step, clean_k, clean_v, q, window, sinks, dim ** -0.5)
-    got = kq.attn_chunk(kq.PagedCache(up(k), up(v)), step.batch(kq), up(q), window, sinks, max_tokens=tokens,
-                        max_len=step.max_len).cpu().double()
     clean = ~rotten
     assert clean.sum() >= 1 and rotten.sum() > 5
     tol = ref.rounded_bound(want, bound, qt)
-    assert torch.isfinite(got[clean]).all()
-    assert ((got - want).abs() <= tol)[clean].all()
-    if kvt != F8 or math.isnan(bad):   # (8 bits have no infinities: clamped when stored)
-        assert not torch.isfinite(got[rotten]).all(-1).any()
+    for most in (step.max_len, 40000):
+        got = kq.attn_chunk(kq.PagedCache(up(k), up(v)), step.batch(kq), up(q), window, sinks, max_tokens=tokens,
+                            max_len=most).cpu().double()
+        assert torch.isfinite(got[clean]).all()
+        assert ((got - want).abs() <= tol)[clean].all()
+        if kvt != F8 or math.isnan(bad):   # (8 bits have no infinities: clamped when stored)
+            assert not torch.isfinite(got[rotten]).all(-1).any()
 
 
 @pytest.mark.parametrize("qt", [BF16, F16])
