@@ -641,7 +641,7 @@ def test_counters(kq):
     check_norm(kq, 2, 256)
     check_lora(kq, 2, 32, 256, 8, 1, [0, 0])
     check_lora(kq, 700, 32, 256, 8, 1, [0] * 700)
-    check_chunk(kq, Step(1, [5], [1], 16), 2, 1, 64, BF16, BF16, types=(BF16,))
-    check_chunk(kq, Step(1, [5], [30], 16), 2, 1, 64, BF16, BF16, types=(BF16,))
+    check_chunk(kq, Step(1, [5], [1], 16), 2, 1, 64, BF16, BF16, types=(BF16,), max_len=40)
+    check_chunk(kq, Step(1, [5], [30], 16), 2, 1, 64, BF16, BF16, types=(BF16,), max_len=40)
     counts = kq.layer_counts()
     assert counts == {"norm_quantize": 1, "chunk_few": 1, "chunk_rows": 1, "lora_few": 2, "lora_tile": 2}
