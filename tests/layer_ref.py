@@ -74,11 +74,13 @@ def chunk(step, k, v, q, window, sinks, scale, k_scale=1.0, v_scale=1.0):
             qq = q[r, h].double()
             w = (qq @ kk.t() * scale).masked_fill(~on, -math.inf).softmax(-1)
             # a score is a sum of dim products in fp32 (each step off by 2^-24 of the sum of
-            # magnitudes), so p is off by that times p; rounding p adds u p
+            # magnitudes), so p is off by that times p; rounding p adds u p.  The weights are divided
+            # by the sum of the rounded ones: with w_i (1 + e_i), |e_i| <= u, the result is off by
+            # sum w_i e_i (v_i - out) to first order, at most u (sum w_i |v_i| + |out|)
             most = (qq.abs() @ kk.abs().t() * abs(scale)).masked_fill(~on, 0.0).amax(-1, keepdim=True)
             rel = u + EPS32 * (dim + 16) * (1.0 + most) + 2.0 ** -18
             out[r, h] = w @ vv
-            bound[r, h] = rel * (w @ vv.abs()) + TINY[q.dtype] * (L + T) * vv.abs().amax()
+            bound[r, h] = rel * (w @ vv.abs()) + u * out[r, h].abs() + TINY[q.dtype] * (L + T) * vv.abs().amax()
     return out, bound
 
 

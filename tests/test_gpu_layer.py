@@ -299,6 +299,16 @@ def test_chunk_expectations_change_the_speed_alone(kq, max_tokens, max_len):
     check_chunk(kq, step, 8, 2, 128, BF16, BF16, 300, 7, max_tokens=max_tokens, max_len=max_len, types=(BF16,))
 
 
+@pytest.mark.parametrize("qt", [BF16, F16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_chunk_few_keys(kq, qt, dim):
+    """Two or three keys to a row, where the roundings of their weights do not average out; more heads
+    to a key head than a block of 16 rows holds, and a number of them that is no power of 2."""
+    check_chunk(kq, Step(7, [0, 1], [1, 140], 64), 8, 2, dim, qt, qt, 2, 1)
+    check_chunk(kq, Step(8, [0, 1, 2], [2, 1, 1], 16), 100, 1, dim, qt, qt)
+    check_chunk(kq, Step(9, [1, 0], [3, 30], 32), 72, 3, dim, qt, F8, 3, 0)
+
+
 def test_chunk_many_sequences(kq):
     """More sequences than a wave looks at together, many of them without rows; single tokens among
     pieces of prompts."""
