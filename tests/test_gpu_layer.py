@@ -646,6 +646,53 @@ def test_lora_past_four_gigabytes(kq):
 
 # -------------------------------------------------------------------- together
 
+@pytest.mark.parametrize("act", [1, 2], ids=["q8_k", "q8_128"])
+@pytest.mark.parametrize("max_len", [300, 40000])
+def test_a_layer_captured(kq, act, max_len):
+    """norm_quantize, a product, its adapters in place, rope_append and attn_chunk of a step with prompts
+    and single tokens, captured twice (two activation formats and two cuts of the work) and replayed
+    with other inputs: the eager calls' bits every time."""
+    import datagen
+    K, heads, dim = 512, 2, 64
+    N = 4 * heads * dim
+    step = Step(12, [250, 0, 33, 7], [1, 40, 7, 1], 32)
+    M, fmt = step.M, kq.KQ_Q4_K if act == 1 else kq.KQ_TQ2
+    W = up(datagen.make_weights(fmt, N, K, 5))
+    x, r = up(ref.draw(step.rng, (M, K))), up(ref.draw(step.rng, (M, K)).to(BF16))
+    total = torch.empty_like(r)
+    A, B = up(ref.draw(step.rng, (3, 16, K), 0.05).to(BF16)), up(ref.draw(step.rng, (3, N, 16), 0.25).to(BF16))
+    ids = up((np.arange(M) % 4 - 1).astype(np.int32))
+    angle = np.arange(300)[:, None] / 100.0 ** (np.arange(dim // 2) / (dim // 2))
+    rope = up(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32))
+    cache, batch = kq.PagedCache(*(up(t) for t in ref.fill_cache(step, heads, dim, BF16))), step.batch(kq)
+
+    def layer(out=None):
+        a = kq.norm_quantize(x, r, act_fmt=act, sum_out=total)
+        qkv = kq.gemm(fmt, W, a, M, N, K)
+        kq.lora(a, A, B, ids, base=qkv, act_fmt=act, out=qkv)
+        q = kq.rope_append(cache, batch, qkv, 2 * heads, rope)
+        return kq.attn_chunk(cache, batch, q, 100, 2, max_tokens=40, max_len=max_len, out=out)
+
+    first = layer()
+    assert torch.isfinite(first).all()
+    outs, graphs = [torch.empty_like(first) for _ in range(2)], []
+    for out in outs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            layer(out)
+    for n in range(4):
+        x.add_(0.125 * (n + 1)).mul_(-0.5)
+        r.mul_(0.75)
+        want = layer()
+        kept = total.clone()
+        total.zero_()
+        for i in ((0, 1), (1, 0))[n % 2]:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and torch.equal(total, kept), n
+        assert not torch.equal(want, first)
+
+
 def test_counters(kq):
     kq.kq_layer_count_reset()
     check_norm(kq, 2, 256)
