@@ -51,8 +51,8 @@ int check_lora(int type, int64_t rank, int64_t n_adapters, int act_fmt, int64_t 
     if (n_adapters && std::max(N, K) > kMaxBytes / rank / n_adapters) return KQ_ERR_SHAPE;
     if (M == 0 || N == 0) return KQ_OK;
     // 32 rows or more to a workgroup along a grid's second dimension; columns are counted
-    // in 32 bits, up to 255 past the last
-    if (M > (int64_t)65535 * 32 || N > kMaxDim - 256) return KQ_ERR_UNSUPPORTED;
+    // in 32 bits, outputs up to 255 past the last, inputs (in steps of up to 4096) a step
+    if (M > (int64_t)65535 * 32 || N > kMaxDim - 256 || K > kMaxDim - 4096) return KQ_ERR_UNSUPPORTED;
     return 1;
 }
 

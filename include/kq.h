@@ -475,8 +475,9 @@ size_t kq_attn_chunk_workspace(const kq_cache *cache, const kq_batch *batch, int
  * as they are and the values between the two products stay in fp32.  An adapter's
  * infinities and NaN reach the rows that use it (where there are many rows, an infinity
  * as a NaN) and no other.  The workspace (kq_lora_workspace bytes, 16-byte aligned) holds
- * those values; calls that may run at the same time need one each.  M up to 65535 * 32, N below 2^31 - 256; A, B and a_q8
- * 16-byte aligned.  The same call gives the same bits.
+ * those values; calls that may run at the same time need one each.  M up to 65535 * 32, N
+ * below 2^31 - 256, K below 2^31 - 4096 (KQ_ERR_UNSUPPORTED beyond); A, B and a_q8 16-byte
+ * aligned.  The same call gives the same bits.
  */
 int kq_lora(int type, int64_t rank, const void *A, const void *B, const float *scale, int64_t n_adapters,
             int act_fmt, const void *a_q8, int64_t M, int64_t N, int64_t K, const int32_t *ids,
