@@ -377,21 +377,24 @@ def quantize_act(x, act_fmt=KQ_ACT_Q8_K, stream=None):
 
 def act_views(a_q8, act_fmt, M, K):
     """(qs int8 [M][K], d fp32 [M][K/bs], bsums int16 [M][K/16] or None) views of a
-    buffer.  d is stored block-major ([K/bs][M]); the view is its transpose."""
+    buffer, which may end with them.  d is stored block-major ([K/bs][M]); the view is
+    its transpose."""
     import torch
     bs = 256 if act_fmt == KQ_ACT_Q8_K else 128
-    section, size, need = lib().kq_act_section_offset, a_q8.numel(), lib().kq_act_bytes(act_fmt, M, K)
-    if size < need:
-        raise ValueError(f"act_views: {size} bytes, {need} needed")
+    section, size = lib().kq_act_section_offset, a_q8.numel()
+    of_d, of_sums = section(act_fmt, KQ_SEC_D, M, K), section(act_fmt, KQ_SEC_BSUMS, M, K)
+    end = of_d + M * (K // bs) * 4 if of_sums < 0 else of_sums + M * (K // 16) * 2
+    if size < end:
+        raise ValueError(f"act_views: {size} bytes, {end} needed")
     if size % 4:  # (a longer buffer: viewed as far as whole words go)
         a_q8 = a_q8[:size - size % 4]
     words = a_q8.view(torch.float32)
     at = words.storage_offset()
     qs = a_q8.view(torch.int8).as_strided((M, K), (K, 1), 4 * at)
-    d = words.as_strided((M, K // bs), (1, M), at + section(act_fmt, KQ_SEC_D, M, K) // 4)
+    d = words.as_strided((M, K // bs), (1, M), at + of_d // 4)
     bsums = None
     if act_fmt == KQ_ACT_Q8_K:
-        bsums = a_q8.view(torch.int16).as_strided((M, K // 16), (K // 16, 1), 2 * at + section(act_fmt, KQ_SEC_BSUMS, M, K) // 2)
+        bsums = a_q8.view(torch.int16).as_strided((M, K // 16), (K // 16, 1), 2 * at + of_sums // 2)
     return qs, d, bsums
 
 

@@ -1,5 +1,6 @@
 """CPU tests of the operators around the products of a layer at the ends of their
-ranges: sizes that the kernels' 32-bit counts do not hold."""
+ranges: sizes that the kernels' 32-bit counts do not hold, and buffers that act_views
+takes."""
 from __future__ import annotations
 
 import pytest
@@ -14,3 +15,28 @@ def test_lora_inputs_that_a_step_of_the_loops_would_overflow(kq, act, K, M):  # 
     the last column has to stay in them."""
     assert lora(kq, rank=8, n=1, act=act, M=M, K=K) == kq.KQ_ERR_UNSUPPORTED
     assert lora(kq, rank=8, n=1, act=act, M=0, K=K) == kq.KQ_OK
+
+
+@pytest.mark.parametrize("act,M,K", [(1, 5, 512), (1, 1, 256), (1, 64, 1280), (2, 3, 384), (2, 7, 128)])
+@pytest.mark.parametrize("at", [0, 16])
+def test_act_views_want_only_what_they_show(kq, act, M, K, at):  # noqa: F811
+    """A buffer that ends with the last section that is viewed (without Q8_K's alpha, or the
+    bytes that round a section's size up) is enough, one byte less is not."""
+    torch = pytest.importorskip("torch")
+    section = lambda s: kq.kq_act_section_offset(act, s, M, K)  # noqa: E731
+    bs = 256 if act == 1 else 128
+    end = section(kq.KQ_SEC_BSUMS) + 2 * M * (K // 16) if act == 1 else section(kq.KQ_SEC_D) + 4 * M * (K // bs)
+    assert end < kq.kq_act_bytes(act, M, K)
+    data = torch.arange(at + end + 9).remainder(251).to(torch.uint8)
+    for size in (end, end + 1, end + 4):
+        buf = data[at:at + size]
+        qs, d, bsums = kq.act_views(buf, act, M, K)
+        assert torch.equal(qs, buf[:M * K].view(torch.int8).view(M, K))
+        from_d = buf[section(kq.KQ_SEC_D):][:4 * M * (K // bs)].clone().view(torch.int32).view(K // bs, M)
+        assert d.shape == (M, K // bs) and torch.equal(d.t().contiguous().view(torch.int32), from_d)
+        if act == 1:
+            assert torch.equal(bsums, buf[section(kq.KQ_SEC_BSUMS):end].clone().view(torch.int16).view(M, K // 16))
+        else:
+            assert bsums is None
+    with pytest.raises(ValueError):
+        kq.act_views(data[at:at + end - 1], act, M, K)
