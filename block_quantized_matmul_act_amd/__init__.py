@@ -383,6 +383,8 @@ def act_views(a_q8, act_fmt, M, K):
     bs = 256 if act_fmt == KQ_ACT_Q8_K else 128
     section, size = lib().kq_act_section_offset, a_q8.numel()
     of_d, of_sums = section(act_fmt, KQ_SEC_D, M, K), section(act_fmt, KQ_SEC_BSUMS, M, K)
+    if of_d < 0 or not a_q8.is_contiguous():
+        raise ValueError(f"act_views: format {act_fmt}, M {M}, K {K}" if of_d < 0 else "act_views: expected a contiguous buffer")
     end = of_d + M * (K // bs) * 4 if of_sums < 0 else of_sums + M * (K // 16) * 2
     if size < end:
         raise ValueError(f"act_views: {size} bytes, {end} needed")

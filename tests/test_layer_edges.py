@@ -40,3 +40,25 @@ def test_act_views_want_only_what_they_show(kq, act, M, K, at):  # noqa: F811
             assert bsums is None
     with pytest.raises(ValueError):
         kq.act_views(data[at:at + end - 1], act, M, K)
+
+
+@pytest.mark.parametrize("act,M,K", [(0, 4, 256), (3, 4, 128), (1, 4, 384), (1, 3, 100), (2, 4, 192), (2, -1, 128), (1, 0, 100)])
+def test_act_views_refuse_what_is_no_buffer(kq, act, M, K):  # noqa: F811
+    """An unknown format, or sizes that no buffer has, inside a longer tensor: an error, and no
+    view of what lies around."""
+    torch = pytest.importorskip("torch")
+    whole = torch.zeros(1 << 14, dtype=torch.uint8)
+    for buf in (whole, whole[256:], whole[4096:8192]):
+        with pytest.raises(ValueError, match="act_views"):
+            kq.act_views(buf, act, M, K)
+
+
+def test_act_views_refuse_bytes_that_lie_apart(kq):  # noqa: F811
+    """Columns of a wider tensor hold as many bytes, but not one after another."""
+    torch = pytest.importorskip("torch")
+    need = kq.kq_act_bytes(1, 2, 256)
+    wide = torch.zeros((4, need), dtype=torch.uint8)
+    for buf in (wide[:, :need // 2], wide[:, 0], wide.view(-1)[::2]):
+        with pytest.raises(ValueError, match="act_views"):
+            kq.act_views(buf, 1, 2, 256)
+    assert kq.act_views(wide[1], 1, 2, 256)[0].shape == (2, 256)
