@@ -62,3 +62,32 @@ def test_act_views_refuse_bytes_that_lie_apart(kq):  # noqa: F811
         with pytest.raises(ValueError, match="act_views"):
             kq.act_views(buf, 1, 2, 256)
     assert kq.act_views(wide[1], 1, 2, 256)[0].shape == (2, 256)
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("f16", [False, True], ids=["bf16", "f16"])
+def test_the_bound_of_the_second_product_tells_24_bits_from_16(rank, f16):
+    """What holds lora's second product on the GPU: with all three parts of t the plain form
+    keeps to its bound, with two of them, or with B's first 8 bits in float16, it does not."""
+    torch = pytest.importorskip("torch")
+    import numpy as np
+
+    import layer_edge_ref as eref
+    rng = np.random.default_rng(rank)
+    M, N, K, n, kind = 40, 150, 512, 3, torch.float16 if f16 else torch.bfloat16
+    A, B, scale, ids, base, picked = eref.pick_case(rng, M, N, rank, K, n, kind, dense=False)
+    qs, d = torch.from_numpy(rng.integers(-127, 128, (M, K)).astype(np.int8)), torch.from_numpy(rng.uniform(1e-3, 1e-1, (M, 2)).astype(np.float32))
+    t = eref.picked_t(qs, d, 256, scale, ids, picked)
+    x = qs.double() * d.double().repeat_interleave(256, 1)
+    for i in range(n):   # (t is the adapter's first product)
+        rows = ids == i
+        want = (x[rows] @ A[i].double().t()) * float(scale[i])
+        assert ((t[rows].double() - want).abs() <= 2.0 ** -23 * want.abs()).all()
+    want, bound = eref.second(t, B, ids, base, dense=False)
+
+    def off(t, B):
+        return ((eref.second(t, B, ids, base, dense=False)[0] - want).abs() - bound).max().item()
+    assert torch.equal(eref.parts(t, 3), t) and off(eref.parts(t, 3), B) <= 0
+    assert off(eref.parts(t, 2), B) > 0 and off(eref.parts(t, 1), B) > 0
+    if f16:
+        assert off(t, B.to(torch.bfloat16).to(torch.float16)) > 0
