@@ -251,10 +251,10 @@ struct ValueRows {
 // see its token and to no other, but a product with P would spoil them all (0 *
 // inf).  Such values are zeros in the product; here they are added for one step
 // of it (512 / RW keys from key0): marks of them times a 0 / 1 matrix of who
-// sees what count the infinities and NaNs that reach each sum.  on: which of this lane's
-// 8 keys its row sees.
-template <class E, bool F8, int D, int RW>
-__device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane, uint32_t on,
+// sees what count the infinities and NaNs that reach each sum.  sees(k): which of the 8
+// keys from k this lane's row sees.
+template <class E, bool F8, int D, int RW, class SEES>
+__device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane, SEES sees,
                                         typename Mfma<E, RW>::acc (&o)[D / RW]) {
     typedef Mfma<E, RW> MM;
     typedef Frag<E, F8> FR;
@@ -263,6 +263,7 @@ __device__ __forceinline__ void add_odd(const ValueRows &va, int key0, int lane,
     const int key = key0 + 8 * g;  // the first of this lane's 8
     const Marks<E> marks;
     const float inf = __builtin_bit_cast(float, here(0x7F800000u));
+    const uint32_t on = sees(key);
     v4u w = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e >> 1] |= (on >> e & 1u) * (marks.pos << (16 * (e & 1)));
@@ -435,16 +436,14 @@ struct Tile {
         for (int i = 0; i < N; ++i)
             *reinterpret_cast<v4u *>(lds + ((k_to + buf) ^ (k_xor(i * KSTEP) * 16)) + i * KSTEP * KB) = stage[i];
     }
-    // The values to LDS.  In a tile that some row does not see whole (edge; here, one that
-    // reaches past the cached slots): zeros for slots past the end, which may hold
+    // The values to LDS.  In a tile that some row does not see whole (one that reaches past
+    // the cached slots, or `edge` if not DRAFTS): zeros for slots past the end, which may hold
     // anything, and for infinite and NaN values; whether this thread met any of those.
-    __device__ __forceinline__ bool store_v(char *lds, int buf, int key0) {
-        return store_v(lds, buf, key0, key0 + KEYS > len);
-    }
-    __device__ __forceinline__ bool store_v(char *lds, int buf, int key0, bool edge) {
+    template <bool DRAFTS = true>
+    __device__ __forceinline__ bool store_v(char *lds, int buf, int key0, bool edge = false) {
         bool found = false;
         if (!stages) return false;
-        if (edge) {
+        if (DRAFTS ? key0 + KEYS > len : edge) {
             const int left = total - (key0 + v_piece * (16 / ES));
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -526,8 +525,10 @@ struct Attend {
             return *reinterpret_cast<const raw_t *>(lds + at + s * (NG / 2 * RUN_BYTES) + RW * d * 16 * FR::BYTES);
         return *reinterpret_cast<const raw_t *>(lds + (at ^ (s * NG * 8 * FR::BYTES)) + RW * d * TL::VB);
     }
-    // begin rows row0 .. of key head h; this lane's token
-    __device__ __forceinline__ int begin_rows(const Seq &sq, int h, int row0) {
+    // begin rows row0 .. of key head h (DRAFTS: and what they see of the drafted tokens); this
+    // lane's token
+    template <bool DRAFTS = true>
+    __device__ __forceinline__ int begin(const Seq &sq, int h, int row0) {
         const int G = a.group, row = row0 + n;
         used = row < sq.T * G;
         const int tok = used ? row / G : 0;
@@ -538,18 +539,16 @@ struct Attend {
             if (used) w = (*reinterpret_cast<const v4u *>(a.q + (q_row * D + 8 * (NG * kk + g)) * 2) & a.q_keep) ^ a.q_flip;
             qf[kk] = __builtin_bit_cast(op_t, w);
         }
+        if constexpr (DRAFTS) {
+            sees = 0;
+            if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(sq.total - sq.len);
+        }
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[d] = acc_t{};
         m = M_START;
         l = 0.f;
         far = false;
         return tok;
-    }
-    // and what they see of the drafted tokens
-    __device__ __forceinline__ void begin(const Seq &sq, int h, int row0) {
-        const int tok = begin_rows(sq, h, row0);
-        sees = 0;
-        if (used) sees = (a.mask ? a.mask[sq.first + tok] : (2ull << tok) - 1ull) & first_bits(sq.total - sq.len);
     }
     // Matrix products of one stream: with VALUES the probabilities pf times the values
     // at byte v of the LDS are added to the sums, with SCORES p gets the scores of
@@ -594,22 +593,17 @@ struct Attend {
             for (int r = 0; r < NT * NR; ++r) p[r] = sc[r / NR][r % NR];
         }
     }
-    // Masks the scores.  on(s): which of the 8 keys of step s this lane's row sees.
-    template <class ON>
-    __device__ __forceinline__ void hide(float (&p)[NT * NR], ON on_step) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const uint32_t on = on_step(s);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
-        }
-    }
     // Masks the scores, and raises m and rescales the sums where it must.
     __device__ __forceinline__ void raise(int key0, int len, float (&p)[NT * NR]) {
         if (key0 + KEYS > len) {
             int k0 = key0;
             asm volatile("" : "+s"(k0));  // (the masks are not worked out ahead of this branch)
-            hide(p, [&](int s) { return seen8(sees, k0 + 8 * NG * s + 8 * g - len); });
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t on = seen8(sees, k0 + 8 * NG * s + 8 * g - len);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) p[8 * s + r] = on >> r & 1u ? p[8 * s + r] : -__builtin_inff();
+            }
         }
         lift(p);
     }
@@ -655,10 +649,6 @@ struct Attend {
         op_t pf[NS];
         products<false, true, 4>(lds, 0, pf, buf, p);
         raise(key0, len, p);
-        add_values(lds, buf, p, pf);
-    }
-    // the tile's probabilities, and their products with its values
-    __device__ __forceinline__ void add_values(const char *lds, int buf, float (&p)[NT * NR], op_t (&pf)[NS]) {
         float sum = 0.f;
 #pragma unroll
         for (int s = 0; s < NS; ++s) pf[s] = probabilities(p, s, sum);
@@ -670,7 +660,7 @@ struct Attend {
     __device__ __forceinline__ void odd_values(int b, int h, const Seq &sq, int from, int to) {
 #pragma nounroll
         for (int key = max(from, sq.len & -KEYS); key < to; key += 8 * NG)
-            add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, sq.total}, key, lane, seen8(sees, key + 8 * g - sq.len), o);
+            add_odd<E, F8, D, RW>(ValueRows{a.cache, a.batch, b, h, sq.total}, key, lane, [&](int k) { return seen8(sees, k - sq.len); }, o);
     }
     // the whole rows' weights (the lane groups hold parts of them)
     __device__ __forceinline__ void end() {

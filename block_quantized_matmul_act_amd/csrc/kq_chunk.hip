@@ -286,7 +286,7 @@ struct Rows {
     __device__ __forceinline__ Rows(const AttnArgs &a, const Tiles<KEYS> &t, unsigned thread) : at(a, thread), tiles(t) {}
     __device__ __forceinline__ void begin(const Block &k, int row0) {
         const int G = at.a.group;
-        pos = k.sq.len + at.begin_rows(k.sq, k.h, row0);
+        pos = k.sq.len + at.template begin<false>(k.sq, k.h, row0);
         const int pos0 = __builtin_amdgcn_readfirstlane(min(k.sq.len + row0 / G, k.pos1));
         const int pos1 = __builtin_amdgcn_readfirstlane(min(k.sq.len + (row0 + RW - 1) / G, k.pos1));
         if (!at.used) pos = pos1;
@@ -389,7 +389,7 @@ struct Rows {
 #pragma nounroll
             for (int key = key0; key < key0 + KEYS; key += 8 * AT::NG)
                 add_odd<E, F8, D, RW>(ValueRows{at.a.cache, at.a.batch, k.b, k.h, k.sq.total}, key, at.lane,
-                                      tiles.on(key + 8 * at.g, pos), at.o);
+                                      [&](int k8) { return tiles.on(k8, pos); }, at.o);
         }
     }
 };
@@ -437,7 +437,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs &c, const Block &k, int
     for (; t < tiles.to; t += WAVES) {
         const int key0 = tiles.key(t);
         tl.store_k(lds, mine);
-        odd |= tl.store_v(lds, mine + TL::K_BYTES, key0, tiles.block.at(t));
+        odd |= tl.template store_v<false>(lds, mine + TL::K_BYTES, key0, tiles.block.at(t));
         if (t + WAVES < tiles.to) {
             tl.load_k(next);
             tl.load_v(next);
