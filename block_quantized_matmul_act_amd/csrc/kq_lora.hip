@@ -220,7 +220,7 @@ __global__ __launch_bounds__((Shrink<E, RB, BS>::WAVES * 64)) void shrink_tile_k
 }
 
 // 16-bit parts of fp32 values, on the matrix cores: t in three bfloat16 parts of 8 bits each is
-// exact, an adapter's bfloat16 is one part and its float16 two.  The products of parts
+// exact (below 2^-110 to 2^-133, the smallest bfloat16), an adapter's bfloat16 is one part and its float16 two.  The products of parts
 // below 2^-24 of the whole are left out; the rest, added in fp32, is as near to fp32
 // products as their sum is.  (fp32 matrix products take 5 times as long: 77 us for
 // the 48 of memory at 2048 x 14336, rank 64.)
@@ -285,12 +285,15 @@ __global__ __launch_bounds__(256, 3) void expand_tile_kernel(const LoraArgs a) {
             if (k < R) x = *reinterpret_cast<const v4f *>(a.t + (int64_t)(m0 + min(row, last)) * R + k);
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
+                // (cut off: three times 8 bits are all 24; rounded, the largest would become infinite)
                 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
                 v4bf y;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y[e] = (__bf16)x[e];
-                    x[e] -= (float)y[e];
+                    const float whole = x[e];  // (a bit cast of an element itself takes the first)
+                    const uint32_t top = __builtin_bit_cast(uint32_t, whole) & 0xFFFF0000u;
+                    y[e] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
+                    x[e] = whole - __builtin_bit_cast(float, top);
                 }
                 *reinterpret_cast<v4bf *>(&t[p][row * LT + k]) = y;
             }

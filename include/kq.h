@@ -472,7 +472,8 @@ size_t kq_attn_chunk_workspace(const kq_cache *cache, const kq_batch *batch, int
  * base is fp32 with rows ldb elements apart (NULL: zeros), out fp32 with rows ldo apart; out
  * may be base itself (ldb == ldo) and overlaps nothing else, so the adapters of a
  * part of a wider product are a call on its columns.  Sums are fp32, the adapters are used
- * as they are and the values between the two products stay in fp32.  An adapter's
+ * as they are and the values between the two products stay in fp32 (where there are many
+ * rows, those below 2^-110 lose what is below 2^-133).  An adapter's
  * infinities and NaN reach the rows that use it (where there are many rows, an infinity
  * as a NaN) and no other.  The workspace (kq_lora_workspace bytes, 16-byte aligned) holds
  * those values; calls that may run at the same time need one each.  M up to 65535 * 32, N

@@ -74,6 +74,26 @@ def test_lora_workspace_may_hold_anything(kq, M, rank):
     assert all(torch.equal(o, outs[0]) for o in outs) and torch.isfinite(outs[0]).all()
 
 
+@pytest.mark.parametrize("t", [BF16, F16], ids=str)
+@pytest.mark.parametrize("M,rank", [(3, 16), (600, 8), (300, 64), (70, 128)])
+def test_lora_values_between_the_products_at_the_end_of_the_range(kq, t, M, rank):
+    """t up to 3.4e38, past the largest bfloat16 but not past fp32, and adapters that bring it back:
+    finite, and as near as anywhere."""
+    N, K, n = 150, 512, 3
+    rng = np.random.default_rng(rank)
+    A, B, _, ids, _, picked = eref.pick_case(rng, M, N, rank, K, n, t, dense=False)
+    B = (B.float() * 2.0 ** -10).to(t)
+    x = torch.from_numpy((3.402e38 * rng.choice([-1.0, 1.0, 0.999, -0.5], (M, K))).astype(np.float32))
+    a = kq.quantize_act(up(x), 1)
+    qs, d, _ = kq.act_views(a, 1, M, K)
+    middle = eref.picked_t(qs.cpu(), d.cpu(), 256, torch.ones(n), ids, picked)
+    assert torch.isfinite(middle).all() and (middle.abs() > 3.397e38).any()
+    want, bound = eref.second(middle, B, ids, torch.zeros(M, N), dense=False)
+    got = kq.lora(a, up(A), up(B), up(ids)).cpu().double()
+    assert torch.isfinite(got).all()
+    assert ((got - want).abs() <= bound + 2.0 ** -24 * want.abs()).all()
+
+
 # ----------------------------------------------------------------- attn_chunk
 
 # rows to a key head: the kernels for few, for blocks of 128 and of 256 (heads of 256: 128 too)
