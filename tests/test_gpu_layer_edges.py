@@ -250,3 +250,19 @@ def test_chunk_workspace_may_hold_anything(kq, tokens, group, dim, kvt):
         assert ((out[:step.M].cpu().double() - want).abs() <= bound).all()
         assert (out[step.M:] == 3).all()
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("tokens", [1, 9, 40, 150])
+@pytest.mark.parametrize("qt,kvt", [(BF16, BF16), (F16, F8)], ids=str)
+def test_chunk_pages_of_wide_heads(kq, page, tokens, qt, kvt):
+    """Heads of 256 over pages of every size, ends of sequences around the ends of pages."""
+    step = Step(page, [3, page - 1, page, page + 1, 2 * page + 5, 700], [tokens] * 6, page)
+    k, v = ref.fill_cache(step, 2, 256, kvt)
+    q = ref.draw(step.rng, (step.M, 6, 256), 1.5).to(qt)
+    cache, batch, dq = kq.PagedCache(up(k), up(v)), step.batch(kq), up(q)
+    for window, sinks in ((0, 0), (100, 20)):
+        want, bound = lref.chunk(step, k, v, q, window, sinks, 1 / 16)
+        for max_len in (step.max_len, 5000, 40000):
+            got = kq.attn_chunk(cache, batch, dq, window, sinks, max_tokens=tokens, max_len=max_len, out_dtype=F32).cpu().double()
+            assert ((got - want).abs() <= bound).all(), ((got - want).abs() / bound).max()
