@@ -145,9 +145,8 @@ struct Work {
     const ChunkArgs &c;
     int *before;
     int u, end, begin, group, all;
-    bool first;
     // lds: CHUNK_RUN_BLOCKS + 1 and a wave's number of ints
-    __device__ __forceinline__ Work(const ChunkArgs &c_, int *lds, int *waves) : c(c_), before(lds), first(true) {
+    __device__ __forceinline__ Work(const ChunkArgs &c_, int *lds, int *waves) : c(c_), before(lds) {
         u = begin = 0;
         end = 1;
         group = blockIdx.x;
