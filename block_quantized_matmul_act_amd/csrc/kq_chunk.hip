@@ -605,8 +605,11 @@ struct Stage {
 // Up to 128 rows, short texts with heads of 128, and all of heads of 64: 4 waves of 32 rows share the tiles; one is in use and
 // AHEAD are on their way.  Copies of tile i + AHEAD start when all waves are done with tile i - 1.
 // Heads of 64 leave room for four workgroups on a compute unit if only one tile is on its
-// way (98 -> 95 us against three workgroups with two).  There the softmax takes as many
-// cycles as the products: what bounds it is the vector unit.
+// way (98 -> 95 us against three workgroups with two).  Ragged prompts under a window of 1024,
+// 24 + 8 heads of 64: 95 us, 600 TFLOP/s.  The vector unit works in 51% of the cycles (some 200
+// instructions to a tile of 64 keys and a wave, half of them the softmax's), the matrix unit in
+// 28%, both at once in 11%; waves wait 40% of their time for their turn to issue and 28% for
+// copies and barriers.  Neither unit is full: what bounds it is how the two take turns.
 template <class E, bool F8, int D>
 __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void chunk_tile_kernel(const ChunkArgs c) {
     constexpr int RW = 32, KEYS = D == 128 ? 32 : 64;  // (64 at dim 128 would not fit the registers)
@@ -685,11 +688,13 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void chunk_tile_kernel(const 
 // 2 i + 4; keys i + 3 at 2 i + 6) after the barrier that follows.
 // A sequence that brings only a few rows among others that bring many takes the way of
 // the few.
-// What bounds it is the power that the chip has for products: their loop alone runs at 1440
-// TFLOP/s, with copies and softmax at 1000 to 1020 (a prompt of 4096, 32 query and 8 key heads
-// of 128, 137 us; 2 pieces of 512 over 32768, 64 query heads, 691 us; a library's
-// product of two matrices of 8192: 1310).  All waves in step: 160 and 800 us.  Staged through
-// registers instead of copied: 148 and 864.
+// What bounds it is the chip's clock under products, and the waits of a turn: their loop alone
+// runs at 1440 TFLOP/s, with copies and softmax at 1000 to 1020 (a prompt of 4096, 32 query and 8
+// key heads of 128, 137 to 142 us; 2 pieces of 512 over 32768, 64 query heads, 691 us; a
+// library's product of two matrices of 8192: 1310).  The clock, 2.4 GHz at most, is 2.05 in the
+// first and 1.6 in the second, where the matrix unit works in 41% and 53% of the cycles and the
+// vector unit in 35% and 39%.  All waves in step: 160 and 800 us.  Staged through registers
+// instead of copied: 148 and 864.
 // RW: rows of a wave, 32, or 16 for less work at dim 256.
 template <class E, bool F8, int D, int RW>
 __global__ __launch_bounds__(512, 2) void chunk_wide_kernel(const ChunkArgs c) {
