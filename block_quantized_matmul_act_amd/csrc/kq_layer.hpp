@@ -71,8 +71,8 @@ struct LoraArgs {
 // Few rows: a wave to a value of t and to 64 outputs of a row, whatever adapters the rows
 // have.  More: tiles of rows, an adapter of a tile after another.  The ids lie on the device, so
 // the bound counts on prompts: past it rows of one adapter gain up to 16 us, and rows with
-// one each lose 20 to 57.  rows x outputs of 4096 inputs, us of a call, few / tiles (13.4: the call on the host), every row with an adapter
-// of its own, and all with one:
+// one each lose 20 to 57.  rows x outputs of 4096 inputs, us of a call, few / tiles (13.4: the
+// call on the host), every row with an adapter of its own, and all with one:
 //   rank 16:  256 x 14336  18.8/44.5 17.8/13.5   256 x 4096  13.4/40.0 13.6/13.5
 //             512 x 14336  30.7/56.7 29.6/15.9   512 x 4096  15.9/40.5 15.5/13.8
 //   rank 64:   96 x 14336  37.1/94.5 18.4/15.4    96 x 4096  16.5/65.0 13.6/13.9

@@ -104,7 +104,7 @@ ChunkPlan chunk_plan(const kq_cache &cache, const kq_batch &batch, int64_t q_hea
     p.blocks = ((batch.n_tokens * group) >> p.rows_shift) + batch.n_seqs;
     const int64_t units = units_of(max_len, p.rows_shift), groups = p.blocks * heads;
     // Places for workgroups on the chip.  (Heads of 64 have 1024, but runs are shorter then: a prompt 90
-    // -> 107 us.  The kernel for few rows has 256 to 1024, by type and head; of 8 bits and heads of 128,
+    // -> 107 us.  The kernel for few rows has 256 to 1280, by type and head; of 8 bits and heads of 128,
     // which have 768, runs over 768 take what they take over 512, 79 us, over 1024 99.)
     const int64_t chip = p.waves == 8 ? 256 : p.waves == 4 && dim == 64 ? 768 : 512;
     // Whole blocks or runs?  Few rows: runs where blocks are fewer than places for them on the
